@@ -24,6 +24,19 @@ DEVERR_INDPTR = 0x2
 DEVERR_TIMEOUT = 0x4
 DEVERR_PARENT = 0x8
 DEVERR_PREFIX = 0x10
+DEVERR_PAGES = 0x20
+DEVERR_TOKEN = 0x40
+DEVERR_LOGITS = 0x80
+MAX_REQUESTS = 8192
+MAX_ROPE_DIM = 256
+MAX_TOP = 32
+MAX_VOCAB = 1 << 20
+ROPE_INTERLEAVED = 0
+ROPE_HALF = 1
+ROPE_SCALE_NONE = 0
+ROPE_SCALE_LINEAR = 1
+ROPE_SCALE_YARN = 2
+ROPE_SCALE_WAVELENGTH = 3
 PLAN_MAGIC = 0x4D545650
 ABI_VERSION = 2
 
@@ -47,6 +60,13 @@ class MtvPlan(ctypes.Structure):
         return {f: getattr(self, f) for f, _ in self._fields_ if not f.startswith("reserved")}
 
 
+class RopeScaling(ctypes.Structure):
+    """``mtv_rope_scaling_t``: scaling of the rotary frequencies for long contexts."""
+    _fields_ = [("kind", ctypes.c_int32), ("reserved", ctypes.c_int32), ("factor", ctypes.c_double),
+                ("original_len", ctypes.c_double), ("beta_fast", ctypes.c_double), ("beta_slow", ctypes.c_double),
+                ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double), ("amplitude", ctypes.c_double)]
+
+
 class MtvError(RuntimeError):
     def __init__(self, code: int, what: str):
         super().__init__(f"{what}: {strerror(code)} (code {code})")
@@ -57,7 +77,8 @@ _lib = None
 SYMBOLS = ("mla_tree_verify_plan", "mla_tree_verify_choose_nsplit", "mla_tree_verify_run", "mla_tree_verify_run_steps", "mla_tree_verify_strerror",
            "mla_tree_verify_clear_device_error", "mla_tree_verify_read_device_error",
            "mla_tree_verify_run_static", "mla_tree_verify_read_static_device_error", "mla_tree_mask_build", "mla_tree_accept", "mla_kv_defrag",
-           "mla_tree_group_prefix")
+           "mla_tree_group_prefix", "mla_page_table_update", "mla_slot_map_build", "mla_rope_freqs", "mla_rope_write",
+           "mla_token_logprobs")
 
 
 def library_path() -> str:
@@ -104,6 +125,18 @@ def load(path: str | None = None):
     lib.mla_kv_defrag.restype = I32
     lib.mla_tree_group_prefix.argtypes = [P, I32, I64, P, P, P, P, P, P, P, P, P, P]
     lib.mla_tree_group_prefix.restype = I32
+    lib.mla_page_table_update.argtypes = [P, I32, I32, P, I64, I64, P, P, I64, P, P, P]
+    lib.mla_page_table_update.restype = I32
+    lib.mla_slot_map_build.argtypes = [P, I64, I64, I64, I64, I32, P, P, P, P, I32, P, P, I64, P, P, P, I64, P, P]
+    lib.mla_slot_map_build.restype = I32
+    lib.mla_rope_freqs.argtypes = [I32, ctypes.c_double, ctypes.POINTER(RopeScaling), P,
+                                   ctypes.POINTER(ctypes.c_float)]
+    lib.mla_rope_freqs.restype = I32
+    lib.mla_rope_write.argtypes = [P, I32, ctypes.c_float, I32, I32, P, I64, P, I32, P, I64, I64, P, I64, I64, I32,
+                                   P, I64, P, I64, P, P, I64, P, P]
+    lib.mla_rope_write.restype = I32
+    lib.mla_token_logprobs.argtypes = [P, I32, I64, I32, I64, P, P, P, I64, P, P, I32, P, P, P, P]
+    lib.mla_token_logprobs.restype = I32
     if path == library_path():
         _lib = lib
     return lib
@@ -314,6 +347,200 @@ def tree_group_prefix(group_indptr, num_groups: int, max_group_prefix: int, kv_i
     if check and rc != MTV_OK:
         raise MtvError(rc, "mla_tree_group_prefix")
     return rc
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+
+class _Args:
+    """Device addresses of one call's tensors, which have to share a device;
+    the call is made on that device and, by default, on its current stream."""
+    __slots__ = ("device",)
+
+    def __init__(self):
+        self.device = None
+
+    def strided(self, t, dtype, name):
+        """Address of a tensor whose strides the call takes."""
+        if t.dtype != dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        device = t.get_device()
+        if device != self.device:
+            if device < 0:
+                raise TypeError(f"{name} must be a CUDA tensor")
+            if self.device is not None:
+                raise ValueError(f"{name} is on another device")
+            self.device = device
+        return t.data_ptr()
+
+    def dense(self, t, dtype, name, shape=None):
+        """Address of a contiguous tensor (None stays NULL)."""
+        if t is None:
+            return None
+        p = self.strided(t, dtype, name)
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        return p
+
+    def call(self, fn, what, stream, check, *args):
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        if isinstance(stream, torch.cuda.Stream):
+            if stream.device_index != self.device:
+                raise ValueError(f"{what}: the stream is on another device than the tensors")
+            stream = stream.cuda_stream
+        if self.device == torch.cuda.current_device():
+            rc = fn(*args, stream)
+        else:
+            with torch.cuda.device(self.device):
+                rc = fn(*args, stream)
+        if check and rc != MTV_OK:
+            raise MtvError(rc, what)
+        return rc
+
+
+def page_table_update(lens, page_size: int, page_table, held, free_pages, num_free, err=None, stream=None,
+                      check: bool = True) -> int:
+    """Enqueues the growing and shrinking of every row of ``page_table``
+    [rows, max_pages] to ``lens`` tokens, from and to the ``free_pages`` stack
+    (see the header)."""
+    a = _Args()
+    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be [rows, max_pages] with dense rows")
+    rows, max_pages = page_table.shape
+    if num_free.numel() != 1:
+        raise ValueError("num_free must hold one element")
+    lp = a.dense(lens, torch.int32, "lens", (rows,))
+    args = (lp, rows, page_size, a.strided(page_table, torch.int32, "page_table"),
+            page_table.stride(0) if rows > 1 else max_pages, max_pages, a.dense(held, torch.int32, "held", (rows,)),
+            a.dense(free_pages, torch.int32, "free_pages"), free_pages.numel(),
+            a.dense(num_free, torch.int32, "num_free"), a.dense(err, torch.int32, "err"))
+    return a.call(load().mla_page_table_update, "mla_page_table_update", stream, check, *args)
+
+
+def slot_map_build(page_table, prefix_lens, tree_sizes, page_size: int, kv_indptr, kv_indices, qo_indptr,
+                   out_cache_loc, positions=None, rows=None, parents=None, num_pages=None, err=None, stream=None,
+                   check: bool = True) -> int:
+    """Enqueues the build of ``kv_indptr``, ``kv_indices``, ``qo_indptr``,
+    ``out_cache_loc`` and ``positions`` from a page table [rows, max_pages] and
+    request lengths (see the header).  The outputs' element counts are their
+    capacities; ``num_pages`` bounds the page table's entries."""
+    a = _Args()
+    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
+        raise ValueError("page_table must be [rows, max_pages] with dense rows")
+    if num_pages is None:
+        raise ValueError("num_pages is needed: the pages of the pool")
+    num_rows, max_pages = page_table.shape
+    bs = prefix_lens.numel()
+    if rows is None and bs > num_rows:
+        raise ValueError("more requests than rows of page_table")
+    q = [t for t in (out_cache_loc, positions, parents) if t is not None]
+    q_capacity = min(t.numel() for t in q) if q else 0
+    args = (a.strided(page_table, torch.int32, "page_table"), page_table.stride(0) if num_rows > 1 else max_pages,
+            num_rows, max_pages, num_pages, page_size, a.dense(rows, torch.int32, "rows", (bs,)),
+            a.dense(prefix_lens, torch.int32, "prefix_lens", (bs,)),
+            a.dense(tree_sizes, torch.int32, "tree_sizes", (bs,)), a.dense(parents, torch.int32, "parents"), bs,
+            a.dense(kv_indptr, torch.int32, "kv_indptr", (bs + 1,)), a.dense(kv_indices, torch.int64, "kv_indices"),
+            kv_indices.numel() if kv_indices is not None else 0,
+            a.dense(qo_indptr, torch.int64, "qo_indptr", (bs + 1,)),
+            a.dense(out_cache_loc, torch.int64, "out_cache_loc"), a.dense(positions, torch.int64, "positions"),
+            q_capacity, a.dense(err, torch.int32, "err"))
+    return a.call(load().mla_slot_map_build, "mla_slot_map_build", stream, check, *args)
+
+
+def rope_freqs(rope_dim: int, base: float, scaling: RopeScaling | None = None):
+    """(turns, amplitude) of the rotary frequencies: an int64 CPU tensor
+    [rope_dim / 2] holding the table's 64-bit fractions of a turn, for
+    ``rope_write`` after a copy to the device, and the factor on its values."""
+    turns = torch.empty(max(int(rope_dim) // 2, 0), dtype=torch.int64)
+    amplitude = ctypes.c_float(0.0)
+    rc = load().mla_rope_freqs(int(rope_dim), float(base), ctypes.byref(scaling) if scaling is not None else None,
+                               turns.data_ptr() or None, ctypes.byref(amplitude))
+    if rc != MTV_OK:
+        raise MtvError(rc, "mla_rope_freqs")
+    return turns, float(amplitude.value)
+
+
+def rope_write(turns, positions, layout: int = ROPE_INTERLEAVED, amplitude: float = 1.0, inverse: bool = False,
+               q_in=None, q_out=None, k_in=None, c_in=None, out_cache_loc=None, kv_pool=None, num_valid=None, err=None,
+               stream=None, check: bool = True) -> int:
+    """Enqueues the rotation of the queries' rotary part, ``q_in`` [tokens,
+    heads, rope_dim] to ``q_out`` (views of any strides with a dense last
+    dimension; ``q_out`` may be ``q_in``), and the write of every token's
+    latent row (``c_in`` [tokens, 512] and the rotated ``k_in`` [tokens, 64])
+    into ``kv_pool`` at ``out_cache_loc``.  Either half may be left out."""
+    a = _Args()
+    tokens, rope_dim = positions.numel(), 2 * turns.numel()
+    if (q_in is None) != (q_out is None):
+        raise ValueError("q_in and q_out go together")
+    some = q_in if q_in is not None else c_in
+    if some is None:
+        raise ValueError("neither q_in nor c_in is given")
+    dtype = some.dtype
+    code = _DTYPES.get(dtype)
+    if code is None:
+        raise TypeError(f"{dtype} is not one of {list(_DTYPES)}")
+
+    tp = a.dense(turns, torch.int64, "turns")
+    pp = a.dense(positions, torch.int64, "positions")
+
+    def part(t, name, shape):
+        p = a.strided(t, dtype, name)
+        if t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+        if t.stride(-1) != 1:
+            raise ValueError(f"{name} must be dense in its last dimension")
+        return p
+
+    q_args = (None, 0, 0, None, 0, 0, 0)
+    if q_in is not None:
+        heads = q_in.shape[1] if q_in.dim() == 3 else -1
+        shape = (tokens, heads, rope_dim)
+        q_args = (part(q_in, "q_in", shape), q_in.stride(0), q_in.stride(1), part(q_out, "q_out", shape),
+                  q_out.stride(0), q_out.stride(1), heads)
+    kv_args = (None, 0, None, 0, None, None, 0)
+    if kv_pool is not None or c_in is not None or k_in is not None or out_cache_loc is not None:
+        if kv_pool is None or c_in is None or k_in is None or out_cache_loc is None:
+            raise ValueError("kv_pool, c_in, k_in and out_cache_loc go together")
+        slots = kv_pool.shape[0]
+        if slots == 0:
+            raise ValueError("kv_pool is empty")
+        kv_args = (part(k_in, "k_in", (tokens, 64)), k_in.stride(0), part(c_in, "c_in", (tokens, 512)), c_in.stride(0),
+                   a.dense(out_cache_loc, torch.int64, "out_cache_loc", (tokens,)),
+                   a.dense(kv_pool, torch.bfloat16, "kv_pool", (slots, 576)), slots)
+    if num_valid is not None and num_valid.numel() != 1:
+        raise ValueError("num_valid must hold one element")
+    return a.call(load().mla_rope_write, "mla_rope_write", stream, check, tp, rope_dim, amplitude, layout, int(inverse),
+                  pp, tokens, a.dense(num_valid, torch.int64, "num_valid"), code, *q_args, *kv_args,
+                  a.dense(err, torch.int32, "err"))
+
+
+def token_logprobs(logits, stats, tokens=None, logprobs=None, top_tokens=None, top_logprobs=None, token_rows=None,
+                   inv_temperature=None, err=None, stream=None, check: bool = True) -> int:
+    """Enqueues the log probabilities of ``tokens`` (under ``token_rows``, or
+    token i under row i), the rows' ``stats`` [3, rows] (scaled maximum, ln of
+    the sum relative to it, entropy) and their top alternatives [k, rows], from
+    ``logits`` [rows, vocab] with dense rows (see the header)."""
+    a = _Args()
+    code = _DTYPES.get(logits.dtype)
+    if code is None:
+        raise TypeError(f"logits must be one of {list(_DTYPES)}, got {logits.dtype}")
+    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+        raise ValueError("logits must be [rows, vocab] with dense rows")
+    rows, vocab = logits.shape
+    if (tokens is None) != (logprobs is None) or (top_tokens is None) != (top_logprobs is None):
+        raise ValueError("tokens and logprobs go together, and so do top_tokens and top_logprobs")
+    n = tokens.numel() if tokens is not None else 0
+    k = top_tokens.shape[0] if top_tokens is not None else 0
+    args = (a.strided(logits, logits.dtype, "logits"), code, rows, vocab, logits.stride(0),
+            a.dense(inv_temperature, torch.float32, "inv_temperature", (rows,)),
+            a.dense(tokens, torch.int32, "tokens", (n,)), a.dense(token_rows, torch.int32, "token_rows", (n,)), n,
+            a.dense(logprobs, torch.float32, "logprobs", (n,)), a.dense(stats, torch.float32, "stats", (3, rows)), k,
+            a.dense(top_tokens, torch.int32, "top_tokens", (k, rows)),
+            a.dense(top_logprobs, torch.float32, "top_logprobs", (k, rows)), a.dense(err, torch.int32, "err"))
+    return a.call(load().mla_token_logprobs, "mla_token_logprobs", stream, check, *args)
 
 
 class MlaTreeVerify:
