@@ -180,7 +180,7 @@ def test_token_logprobs_refusals(lib):
              tt=FAKE, tl=FAKE):
         return lib.mla_token_logprobs(x, dtype, rows, vocab, stride, None, tokens, trows, n, lp, stats, k, tt, tl, None, None)
     for kw in [dict(dtype=3), dict(dtype=-1), dict(rows=-1), dict(vocab=0), dict(vocab=(1 << 20) + 1), dict(stride=-1),
-               dict(n=-1), dict(n=5), dict(k=-1), dict(k=33)]:
+               dict(n=-1), dict(n=5), dict(k=-1), dict(k=33), dict(x=ctypes.c_void_p(0x100001))]:
         assert call(**kw) == -3, kw
     assert call(rows=1 << 31) == -2
     for kw in [dict(x=None), dict(stats=None), dict(tokens=None), dict(lp=None), dict(tt=None), dict(tl=None)]:
