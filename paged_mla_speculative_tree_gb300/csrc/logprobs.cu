@@ -57,62 +57,64 @@ __device__ __forceinline__ bool usable_temperature(float s) { return s > 0.f && 
 
 // ---------------------------------------------------------------------------
 // A row is read once, by a cluster of 1 to 8 blocks that each take a
-// contiguous share of it in groups of 16 logits (one or two 32-byte loads of a
-// thread).  Per thread: the sums S and U = sum e^d d of d = z - ref relative to
-// a reference that moves only when a logit passes it by 20, and the largest
-// group maximum with its group.  Every group's maximum also goes to shared
-// memory, so the top k needs no second pass: the k-th largest of the threads'
-// maxima (by value, then lower group) bounds the k-th logit from below, only
-// groups whose maximum reaches it are read again (about k of thousands), and
-// the survivors' order is counted.
+// contiguous share of it in groups of 64 bytes.  Per thread: the sums S = sum
+// 2^t and U = sum 2^t t of t = c x - ref, c = log2(e) / temperature, relative
+// to a reference that moves only when a logit passes it by 2^29, and the
+// largest group maximum with its group.  Every group's maximum also goes to
+// shared memory, so the top k needs no second pass: the k-th largest maximum of
+// 64 buckets of groups bounds the k-th logit from below, only groups whose
+// maximum reaches it are read again (about k of thousands), and the survivors'
+// order is counted.
 //
 // What bounds it: the bytes of the logits; then issue slots -- about 5
 // instructions a logit, with the fp32 work in pairs (f32x2) and one MUFU
 // exponential each.
 // ---------------------------------------------------------------------------
-constexpr int kGroup = 16;            // logits a group
 constexpr int kMaxGroups = 8192;      // groups a block: their maxima fill 16 or 32 KB
-constexpr int kOwners = 48;           // most threads whose maxima may reach the bound
-constexpr int kPicked = 64;           // most groups read again
-constexpr int kEdge = 32;             // logits before and after the aligned groups, at most 15 each
-constexpr int kListed = kOwners * (kMaxGroups / kLpThreads);
+constexpr int kListed = 256;          // groups that may reach the bound before they are searched by rank
+constexpr int kPicked = MTV_MAX_TOP;  // groups read again at most
+constexpr int kMaxGroup = 32;         // logits a group at most
+constexpr int kEdge = 64;             // logits before and after the aligned groups, under 32 each
+constexpr int kBuckets = 64;
+constexpr int kBucketThreads = kLpThreads / kBuckets;
 constexpr int kMaxCluster = 8;
 
-template <typename T> struct Groups;  // one group in registers
-template <> struct Groups<__nv_bfloat16> {
-  static constexpr int kWords = 8;
+// 16 bytes of logits in four registers.
+template <typename T> struct Chunk;
+template <> struct Chunk<__nv_bfloat16> {
+  static constexpr uint32_t kNone = 0xff80ff80u;  // -inf
   static __device__ __forceinline__ float max(const uint32_t* v) {
-    __nv_bfloat162 m = pair(v[0]);
-#pragma unroll
-    for (int i = 1; i < kWords; ++i) m = __hmax2_nan(m, pair(v[i]));
+    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(pair(v[0]), pair(v[1])), __hmax2_nan(pair(v[2]), pair(v[3])));
     return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
   }
   static __device__ __forceinline__ float2 get(const uint32_t* v, int i) {
     return make_float2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u));
   }
   static __device__ __forceinline__ __nv_bfloat162 pair(uint32_t x) { return *reinterpret_cast<__nv_bfloat162*>(&x); }
-  static __device__ __forceinline__ __nv_bfloat16 narrow(float x) { return __float2bfloat16_rn(x); }
+  static __device__ __forceinline__ __nv_bfloat16 narrow(float x) {  // x is one already
+    return __ushort_as_bfloat16(uint16_t(__float_as_uint(x) >> 16));
+  }
 };
-template <> struct Groups<__half> {
-  static constexpr int kWords = 8;
+template <> struct Chunk<__half> {
+  static constexpr uint32_t kNone = 0xfc00fc00u;
   static __device__ __forceinline__ float max(const uint32_t* v) {
-    __half2 m = pair(v[0]);
-#pragma unroll
-    for (int i = 1; i < kWords; ++i) m = __hmax2_nan(m, pair(v[i]));
+    const __half2 m = __hmax2_nan(__hmax2_nan(pair(v[0]), pair(v[1])), __hmax2_nan(pair(v[2]), pair(v[3])));
     return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
   }
   static __device__ __forceinline__ float2 get(const uint32_t* v, int i) { return __half22float2(pair(v[i])); }
   static __device__ __forceinline__ __half2 pair(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
   static __device__ __forceinline__ __half narrow(float x) { return __float2half_rn(x); }
 };
-template <> struct Groups<float> {
-  static constexpr int kWords = 16;
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+template <> struct Chunk<float> {
+  static constexpr uint32_t kNone = 0xff800000u;
   static __device__ __forceinline__ float max(const uint32_t* v) {
-    float m = __uint_as_float(v[0]);
-#pragma unroll
-    for (int i = 1; i < kWords; ++i)
-      asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(m), "f"(__uint_as_float(v[i])));
-    return m;
+    return max_nan(max_nan(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                   max_nan(__uint_as_float(v[2]), __uint_as_float(v[3])));
   }
   static __device__ __forceinline__ float2 get(const uint32_t* v, int i) {
     return make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
@@ -120,9 +122,9 @@ template <> struct Groups<float> {
   static __device__ __forceinline__ float narrow(float x) { return x; }
 };
 
-__device__ __forceinline__ void load32(const void* p, uint32_t* v) {
-  asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
-               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7])
+__device__ __forceinline__ void load16(const void* p, uint32_t* v) {
+  asm volatile("ld.global.nc.L1::no_allocate.v4.b32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                : "l"(p));
 }
 
@@ -158,115 +160,42 @@ __device__ __forceinline__ float exp2_approx(float x) {
   return r;
 }
 
-// Sums relative to a reference ref: S = sum e^(z - ref), U = sum e^(z - ref) (z - ref).
+// Sums S and U whose reference moves by d: t becomes t + d.
 struct Sums {
-  float ref, s, u;
-  __device__ __forceinline__ void move_to(float to) {  // to > -inf
-    if (ref > -INFINITY) {
-      const float d = ref - to, w = exp2_approx(d * kLog2e);
-      u = w > 0.f ? (u + s * d) * w : 0.f;
-      s *= w;
-    }
-    ref = to;
-  }
-  __device__ __forceinline__ void add(const Sums& o) {  // o has the same reference, or none
-    if (o.ref > -INFINITY) {
-      s += o.s;
-      u += o.u;
-    }
+  float s, u;
+  __device__ __forceinline__ Sums moved(float d) const {
+    const float w = exp2_approx(d);
+    return w > 0.f ? Sums{s * w, (u + s * d) * w} : Sums{0.f, 0.f};
   }
 };
 
-constexpr float kRefSlack = 20.f;
+constexpr float kRefSlack = 29.f;
+constexpr float kLowest = -3.402823466e38f;
 
 struct LpShared {
-  uint64_t cand[kPicked * kGroup + kEdge];
-  float thread_max[kLpThreads];
-  uint16_t thread_group[kLpThreads];
-  uint16_t listed[kListed];
-  uint16_t picked[kPicked];
+  uint64_t cand[kPicked * kMaxGroup + kEdge];
+  uint64_t bucket[kBuckets];
+  uint64_t round[2][kLpWarps];
+  uint16_t listed[kListed], picked[kPicked];
   float wm[kLpWarps], ws[kLpWarps], wu[kLpWarps];
   // written by every block of the cluster into the first one's
   float part_m[kMaxCluster], part_s[kMaxCluster], part_u[kMaxCluster];
   int part_bad[kMaxCluster], part_found[kMaxCluster];
   uint64_t part_key[kMaxCluster][MTV_MAX_TOP];
-  float bound;
-  int bound_group, num_listed, num_cand;
+  uint64_t bound;
+  int num_listed, num_cand;
 };
 
-__device__ __forceinline__ uint32_t ordered(float x) {
-  const uint32_t b = __float_as_uint(x + 0.f);
-  return (b >> 31) ? ~b : (b | 0x80000000u);
-}
-
-// Warp 0: a bound (value, group) that at least k and at most kOwners of the
-// threads' (maximum, first group of it) pairs reach, in the order of larger
-// values and then lower groups; -inf and any group when fewer than k threads
-// have a maximum above -inf.  Bisection over the values' ordered bits, and
-// over the groups among equal values.
-__device__ __forceinline__ void select_bound(LpShared& sh, int k) {
-  const int lane = threadIdx.x;
-  constexpr int kPer = kLpThreads / 32;
-  uint32_t v[kPer];
-  uint32_t top = 0;
-#pragma unroll
-  for (int i = 0; i < kPer; ++i) {
-    v[i] = ordered(sh.thread_max[i * 32 + lane]);
-    top = v[i] > top ? v[i] : top;
-  }
-  top = __reduce_max_sync(0xffffffffu, top);
-  auto count_from = [&](uint32_t x) {
-    unsigned c = 0;
-#pragma unroll
-    for (int i = 0; i < kPer; ++i) c += v[i] >= x;
-    return int(__reduce_add_sync(0xffffffffu, c));
-  };
-  const uint32_t none = ordered(-INFINITY);
-  uint32_t lo = none + 1, hi = top;  // the bound's bits lie in [lo, hi]
-  int g = 0xffff, c = 0;
-  if (top <= none || (c = count_from(lo)) < k) {
-    lo = none;
-  } else {
-    // invariant: count_from(lo) >= k
-    while (lo < hi && c > kOwners) {
-      const uint32_t mid = lo + (hi - lo + 1) / 2;
-      const int cm = count_from(mid);
-      if (cm >= k) {
-        lo = mid;
-        c = cm;
-      } else {
-        hi = mid - 1;
-      }
-    }
-    if (c > kOwners) {  // equal values: the lowest groups among them
-      const int above = lo == 0xffffffffu ? 0 : count_from(lo + 1);
-      int g0 = 0, g1 = 0xffff;
-      uint16_t grp[kPer];
-#pragma unroll
-      for (int i = 0; i < kPer; ++i) grp[i] = sh.thread_group[i * 32 + lane];
-      while (g0 < g1) {
-        const int mid = (g0 + g1) / 2;
-        unsigned n = 0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) n += v[i] == lo && grp[i] <= mid;
-        if (above + int(__reduce_add_sync(0xffffffffu, n)) >= k) g1 = mid;
-        else g0 = mid + 1;
-      }
-      g = g0;
-    }
-  }
-  if (lane == 0) {
-    sh.bound = lo == none ? -INFINITY : __uint_as_float((lo >> 31) ? (lo & 0x7fffffffu) : ~lo);
-    sh.bound_group = g;
-  }
-}
+// Groups in the order of larger maxima and then lower groups: larger keys first.
+__device__ __forceinline__ uint64_t group_key(float m, int g) { return order_key(m, uint32_t(g)); }
 
 template <typename T>
-__global__ void __launch_bounds__(kLpThreads) logprob_rows_kernel(const LogprobArgs A, int blocks) {
+__global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const LogprobArgs A, int blocks) {
   extern __shared__ __align__(16) unsigned char dyn[];
   T* group_max = reinterpret_cast<T*>(dyn);
   __shared__ LpShared sh;
-  constexpr int kWords = Groups<T>::kWords;
+  constexpr int kChunks = 4;                       // of 16 bytes: a group's, and a thread's of a step
+  constexpr int kGroup = 64 / int(sizeof(T));      // logits a group
   const int tid = threadIdx.x, lane = tid & 31, w = tid >> 5;
   const int rank = blocks > 1 ? int(blockIdx.x % unsigned(blocks)) : 0;
   const int64_t r = blocks > 1 ? int64_t(blockIdx.x / unsigned(blocks)) : int64_t(blockIdx.x);
@@ -285,18 +214,21 @@ __global__ void __launch_bounds__(kLpThreads) logprob_rows_kernel(const LogprobA
     if (token >= 0 && token < A.vocab) token_x = to_float(x[token]);
   }
   // aligned groups [g0, g0 + n) of this block; logits before and after them
-  const int skew = int(reinterpret_cast<uintptr_t>(x) & 31) / int(sizeof(T));
-  const int head = min(skew ? 32 / int(sizeof(T)) - skew : 0, A.vocab);
+  const int skew = int(reinterpret_cast<uintptr_t>(x) & 63) / int(sizeof(T));
+  const int head = min(skew ? 64 / int(sizeof(T)) - skew : 0, A.vocab);
   const int all = (A.vocab - head) / kGroup;
   const int share = (all + blocks - 1) / blocks;
   const int g0 = min(rank * share, all), n = min(share, all - g0);
   const T* body = x + head + int64_t(g0) * kGroup;
 
-  Sums acc{-INFINITY, 0.f, 0.f};
-  float tmax = -INFINITY;
+  Sums acc{0.f, 0.f};
+  float ref = kLowest;
+  const float c2 = scale * kLog2e;
+  float tmax = -INFINITY, tnext = -INFINITY;  // largest and second largest group maximum
+  float worst = -INFINITY;  // NaN or +inf once a logit was
   int tgroup = 0xffff;
   bool bad = !usable_temperature(scale);
-  const uint64_t scale2 = pack2(scale, scale), log2e2 = pack2(kLog2e, kLog2e);
+  const uint64_t c22 = pack2(c2, c2);
   uint64_t s2 = 0, u2 = 0;
   auto fold = [&]() {
     const float2 a = unpack2(s2), b = unpack2(u2);
@@ -304,65 +236,94 @@ __global__ void __launch_bounds__(kLpThreads) logprob_rows_kernel(const LogprobA
     acc.u += b.x + b.y;
     s2 = u2 = 0;
   };
-  auto group = [&](const uint32_t* v, int g) {
-    const float m = Groups<T>::max(v);
-    group_max[g] = Groups<T>::narrow(m);
-    bad |= !(m < INFINITY);
-    if (m > tmax) {
-      tmax = m;
-      tgroup = g;
+  // A step of a warp is 32 neighbouring groups, as kChunks runs of 32 chunks: a
+  // lane loads chunk `lane` of each run.  A group's maximum is put together
+  // from the lanes that hold its chunks; lane l ends up with group own + step.
+  const int own = w * 32 + (lane % kChunks) * (32 / kChunks) + lane / kChunks;
+  auto process = [&](const uint32_t* v, int step) {
+    float c[kChunks];
+    float m = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+      c[i] = Chunk<T>::max(v + 4 * i);
+      m = max_nan(m, c[i]);
     }
-    const float z = m * scale;
-    if (!(z > -INFINITY)) return;
-    if (z > acc.ref + kRefSlack) {
+    worst = max_nan(worst, m);
+    // run r of the maxima goes to the lanes with lane % kChunks == r, halving the runs each time
+#pragma unroll
+    for (int h = kChunks / 2; h > 0; h >>= 1) {
+      const bool upper = (lane & h) != 0;
+#pragma unroll
+      for (int i = 0; i < h; ++i) {
+        const float other = __shfl_xor_sync(0xffffffffu, upper ? c[i] : c[i + h], h);
+        c[i] = fmaxf(upper ? c[i + h] : c[i], other);
+      }
+    }
+    const int g = own + step;
+    if (g < n) {
+      group_max[g] = Chunk<T>::narrow(c[0]);
+      tnext = fmaxf(tnext, fminf(c[0], tmax));
+      if (c[0] > tmax) {
+        tmax = c[0];
+        tgroup = g;
+      }
+    }
+    const float z = m * c2;
+    if (z > ref + kRefSlack) {
       fold();
-      acc.move_to(z);
+      if (ref > kLowest) acc = acc.moved(ref - z);
+      ref = z;
     }
-    const uint64_t ref2 = pack2(-acc.ref, -acc.ref);
+    const uint64_t ref2 = pack2(-ref, -ref);
     uint64_t ug = 0;
 #pragma unroll
     for (int i = 0; i < kGroup / 2; ++i) {
-      const float2 p = Groups<T>::get(v, i);
-      const uint64_t d = fma2(pack2(p.x, p.y), scale2, ref2);
-      const float2 t = unpack2(mul2(d, log2e2));
+      const float2 p = Chunk<T>::get(v, i);
+      const uint64_t t2 = fma2(pack2(p.x, p.y), c22, ref2);
+      const float2 t = unpack2(t2);
       const uint64_t e = pack2(exp2_approx(t.x), exp2_approx(t.y));
       s2 = add2(s2, e);
-      ug = fma2(e, d, ug);
+      ug = fma2(e, t2, ug);
     }
     const float2 h = unpack2(ug);
-    if (isnan(h.x + h.y)) {  // a logit at -inf, or so low that z is: 0 * -inf
+    if (isnan(h.x + h.y)) {  // 0 * -inf: a logit at -inf, or so low that t is
       ug = 0;
+      if (m > -INFINITY) {
 #pragma unroll
-      for (int i = 0; i < kGroup / 2; ++i) {
-        const float2 p = Groups<T>::get(v, i);
-        const float2 d = unpack2(fma2(pack2(p.x, p.y), scale2, ref2));
-        const float dx = fmaxf(d.x, -1000.f), dy = fmaxf(d.y, -1000.f);  // e^-1000 is 0
-        ug = fma2(pack2(exp2_approx(dx * kLog2e), exp2_approx(dy * kLog2e)), pack2(dx, dy), ug);
+        for (int i = 0; i < kGroup / 2; ++i) {
+          const float2 p = Chunk<T>::get(v, i);
+          const float2 t = unpack2(fma2(pack2(p.x, p.y), c22, ref2));
+          const float tx = fmaxf(t.x, -1000.f), ty = fmaxf(t.y, -1000.f);  // 2^-1000 is 0
+          ug = fma2(pack2(exp2_approx(tx), exp2_approx(ty)), pack2(tx, ty), ug);
+        }
       }
     }
     u2 = add2(u2, ug);
   };
-  constexpr int kBatch = kWords == 8 ? 4 : 2;  // groups in flight a thread
-  int g = tid;
-  for (; g + (kBatch - 1) * kLpThreads < n; g += kBatch * kLpThreads) {
-    uint32_t v[kBatch][kWords];
+  constexpr int kBatch = 1;  // steps in flight
+  constexpr int kChunkLogits = 16 / int(sizeof(T));
+#pragma unroll 1
+  for (int step = 0; w * 32 + step < n; step += kBatch * kLpThreads) {
+    uint32_t v[kBatch][4 * kChunks];
 #pragma unroll
     for (int b = 0; b < kBatch; ++b) {
-      const T* at = body + int64_t(g + b * kLpThreads) * kGroup;
+      const int from = w * 32 + step + b * kLpThreads;
 #pragma unroll
-      for (int q = 0; q < kWords; q += 8) load32(at + q * (kGroup / kWords), &v[b][q]);
+      for (int i = 0; i < kChunks; ++i) {
+        const int chunk = i * 32 + lane;  // of the step's 32 * kChunks
+        if (from + chunk / kChunks < n) {
+          load16(body + int64_t(from) * kGroup + chunk * kChunkLogits, &v[b][4 * i]);
+        } else {
+          v[b][4 * i] = v[b][4 * i + 1] = v[b][4 * i + 2] = v[b][4 * i + 3] = Chunk<T>::kNone;
+        }
+      }
     }
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) group(v[b], g + b * kLpThreads);
-  }
-  for (; g < n; g += kLpThreads) {
-    uint32_t v[kWords];
-    const T* at = body + int64_t(g) * kGroup;
-#pragma unroll
-    for (int q = 0; q < kWords; q += 8) load32(at + q * (kGroup / kWords), &v[q]);
-    group(v, g);
+    for (int b = 0; b < kBatch; ++b)
+      if (w * 32 + step + b * kLpThreads < n) process(v[b], step + b * kLpThreads);
   }
   fold();
+  bad |= !(worst < INFINITY);
   // the edges: thread tid < kEdge of the first block takes one logit
   const int tail0 = head + all * kGroup;
   float edge = -INFINITY;
@@ -372,162 +333,254 @@ __global__ void __launch_bounds__(kLpThreads) logprob_rows_kernel(const LogprobA
   if (edge_id >= 0) {
     edge = to_float(x[edge_id]);
     bad |= !(edge < INFINITY);
-    const float z = edge * scale;
-    if (z > -INFINITY && z < INFINITY) {
-      if (z > acc.ref + kRefSlack) acc.move_to(z);
-      const float d = fmaf(edge, scale, -acc.ref), e = exp2_approx(d * kLog2e);
-      acc.s += e;
-      acc.u += e > 0.f ? e * d : 0.f;
+    const float z = edge * c2;
+    if (z > ref + kRefSlack) {
+      if (ref > kLowest) acc = acc.moved(ref - z);
+      ref = z;
     }
+    const float t = fmaf(edge, c2, -ref), e = exp2_approx(t);
+    acc.s += e;
+    acc.u += e > 0.f ? e * t : 0.f;
   }
 
-  // the block's maximum and sums
+  // The block's maximum and the buckets' largest group keys.  A bucket is a few
+  // neighbouring threads: the k-th largest of 64 buckets' keys is reached by k
+  // groups at least, and by 1.4 k on average at k = 32.
   float m = fmaxf(tmax, edge);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
   if (lane == 0) sh.wm[w] = m;
-  sh.thread_max[tid] = tmax;
-  sh.thread_group[tid] = uint16_t(tgroup);
-  if (tid == 0) sh.num_listed = sh.num_cand = 0;
+  if (A.top_k > 0) {
+    // threads without a group above -inf rank last, each apart from the others
+    uint64_t key = tmax > -INFINITY ? group_key(tmax, tgroup) : group_key(-INFINITY, kMaxGroups + tid);
+#pragma unroll
+    for (int o = 1; o < kBucketThreads; o <<= 1) {
+      const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
+      key = other > key ? other : key;
+    }
+    if (tid % kBucketThreads == 0) sh.bucket[tid / kBucketThreads] = key;
+    if (tid == 0) sh.num_listed = sh.num_cand = 0;
+  }
   bad = __syncthreads_or(bad);
 #pragma unroll
   for (int i = 0; i < kLpWarps; ++i) m = fmaxf(m, sh.wm[i]);
-  // the reference of the results: one rounded product, so that one fused
-  // multiply-add gives z - zmax to half a step of the difference
-  float zmax = m * scale;
-  const bool sums = m > -INFINITY && !bad && fabsf(zmax) < INFINITY;
-  Sums total{zmax, 0.f, 0.f};
-  if (sums) {
-    if (acc.ref > -INFINITY) {
-      acc.move_to(zmax);
-      total.add(acc);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) {
-      total.s += __shfl_xor_sync(0xffffffffu, total.s, o);
-      total.u += __shfl_xor_sync(0xffffffffu, total.u, o);
-    }
-    if (lane == 0) {
-      sh.ws[w] = total.s;
-      sh.wu[w] = total.u;
+  // sums relative to the block's maximum: t = c (x - m)
+  Sums total{0.f, 0.f};
+  if (m > -INFINITY && !bad) {
+    if (fabsf(m * c2) < 0x1p30f) {
+      if (ref > kLowest) total = acc.moved(fmaf(-c2, m, ref));
+    } else {
+      // so far from 0 that a reference's rounding (2^-24 of it) is no longer a
+      // small t: once more, from differences to the maximum
+      for (int i = tid; i < n * kGroup; i += kLpThreads) {
+        const float t = (to_float(body[i]) - m) * c2, e = exp2_approx(t);
+        total.s += e;
+        total.u += e > 0.f ? e * t : 0.f;
+      }
+      if (edge_id >= 0) {
+        const float t = (edge - m) * c2, e = exp2_approx(t);
+        total.s += e;
+        total.u += e > 0.f ? e * t : 0.f;
+      }
     }
   }
-  if (A.top_k > 0 && w == 0) select_bound(sh, A.top_k);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    total.s += __shfl_xor_sync(0xffffffffu, total.s, o);
+    total.u += __shfl_xor_sync(0xffffffffu, total.u, o);
+  }
+  if (lane == 0) {
+    sh.ws[w] = total.s;
+    sh.wu[w] = total.u;
+  }
+  if (A.top_k > 0) {  // a bucket's threads count its rank
+    const uint64_t mine = sh.bucket[tid / kBucketThreads];
+    int above = 0;
+#pragma unroll
+    for (int j = 0; j < kBuckets; j += kBucketThreads) above += sh.bucket[j + tid % kBucketThreads] > mine;
+#pragma unroll
+    for (int o = 1; o < kBucketThreads; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+    if (above == A.top_k - 1 && tid % kBucketThreads == 0) sh.bound = mine;
+  }
   __syncthreads();
   total.s = total.u = 0.f;
-  if (sums) {
 #pragma unroll
-    for (int i = 0; i < kLpWarps; ++i) {
-      total.s += sh.ws[i];
-      total.u += sh.wu[i];
+  for (int i = 0; i < kLpWarps; ++i) {
+    total.s += sh.ws[i];
+    total.u += sh.wu[i];
+  }
+  LpShared* to = blocks > 1 ? cluster.map_shared_rank(&sh, 0) : &sh;
+  if (blocks > 1) {
+    cluster.barrier_wait();  // the first block is there
+    if (tid == 0) {
+      to->part_m[rank] = m;
+      to->part_s[rank] = total.s;
+      to->part_u[rank] = total.u;
+      to->part_bad[rank] = bad;
     }
   }
+  // what a single block knows of the row already, the first of several later
+  // m times the scale rounds; what that leaves goes into ln S, so that one
+  // fused multiply-add z - zmax, less ln S, is right to the roundings of both
+  float zmax, log_s, entropy;
+  auto finish = [&]() {
+    zmax = m * scale;
+    bad |= m > -INFINITY && !(fabsf(zmax) < INFINITY);
+    if (bad) {
+      log_s = entropy = zmax = NAN;
+    } else if (m == -INFINITY) {
+      log_s = -INFINITY;
+      entropy = 0.f;
+    } else {
+      const float l = logf(total.s);
+      log_s = l + fmaf(m, scale, -zmax);
+      entropy = l - kLn2 * (total.u / total.s);
+    }
+    if (tid == 0) {
+      A.stats[r] = zmax;
+      A.stats[A.num_rows + r] = log_s;
+      A.stats[2 * A.num_rows + r] = entropy;
+      uint32_t word = bad ? MTV_DEVERR_LOGITS : 0;
+      if (scores) {
+        float lp = 0.f;
+        if (token < -1 || token >= A.vocab) {
+          lp = NAN;
+          word |= MTV_DEVERR_TOKEN;
+        } else if (token >= 0) {
+          lp = token_x == -INFINITY && !bad ? -INFINITY : fmaf(token_x, scale, -zmax) - log_s;
+        }
+        A.logprobs[r] = lp;
+      }
+      if (word) set_err(A.err, word);
+    }
+  };
+  auto write_top = [&](int k, uint64_t key) {
+    A.top_tokens[k * A.num_rows + r] = int32_t(~uint32_t(key));
+    A.top_logprobs[k * A.num_rows + r] = fmaf(key_logit(key), scale, -zmax) - log_s;
+  };
+  auto write_none = [&](int from) {
+    for (int k = from + tid; k < A.top_k; k += kLpThreads) {
+      A.top_tokens[k * A.num_rows + r] = -1;
+      A.top_logprobs[k * A.num_rows + r] = bad ? NAN : -INFINITY;
+    }
+  };
+  if (blocks == 1) finish();
+  if (A.top_k == 0 && blocks == 1) return;
 
-  // the block's top k
+  // the block's top k: groups that reach the bound, their logits, their order
   int found = 0;
   if (A.top_k > 0 && !bad) {
-    const float bound = sh.bound;
-    const int bound_group = sh.bound_group;
-    auto reaches = [&](float v, int at) { return v > -INFINITY && (v > bound || (v == bound && at <= bound_group)); };
-    if (reaches(tmax, tgroup)) {
-      for (int at = tid; at < n; at += kLpThreads)
-        if (reaches(to_float(group_max[at]), at)) sh.listed[atomicAdd(&sh.num_listed, 1)] = uint16_t(at);
+    const uint64_t bound = sh.bound;
+    const float least = key_logit(bound);
+    auto list = [&](float v, int at) {
+      if (v > -INFINITY && group_key(v, at) >= bound) {
+        const int i = atomicAdd(&sh.num_listed, 1);
+        if (i < kListed) sh.listed[i] = uint16_t(at);
+      }
+    };
+    list(tmax, tgroup);
+    if (tnext > -INFINITY && tnext >= least) {  // rare: a second group of the thread
+      for (int at = own; at < n; at += kLpThreads)
+        if (at != tgroup) list(to_float(group_max[at]), at);
     }
     if (edge > -INFINITY) sh.cand[atomicAdd(&sh.num_cand, 1)] = order_key(edge, uint32_t(edge_id));
     __syncthreads();
-    int picked = sh.num_listed;
-    const uint16_t* list = sh.listed;
-    if (picked > kPicked) {  // few threads own many large groups: the first k by (maximum, group)
-      for (int i = tid; i < picked; i += kLpThreads) {
-        const uint64_t key = order_key(to_float(group_max[sh.listed[i]]), sh.listed[i]);
-        int above = 0;
-        for (int j = 0; j < picked; ++j) above += order_key(to_float(group_max[sh.listed[j]]), sh.listed[j]) > key;
-        if (above < A.top_k) sh.picked[above] = sh.listed[i];
+    const int listed = sh.num_listed;
+    const uint16_t* pick = sh.listed;
+    int picked = listed;
+    if (listed > kListed) {  // the large logits sit in few buckets, or many are equal: one search a rank
+      uint64_t below = ~uint64_t(0);
+      for (picked = 0; picked < A.top_k; ++picked) {
+        uint64_t best = 0;
+        for (int at = tid; at < n; at += kLpThreads) {
+          const uint64_t key = group_key(to_float(group_max[at]), at);
+          if (key < below && key > best) best = key;
+        }
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) {
+          const uint64_t other = __shfl_xor_sync(0xffffffffu, best, o);
+          best = other > best ? other : best;
+        }
+        if (lane == 0) sh.round[picked & 1][w] = best;
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < kLpWarps; ++i) best = sh.round[picked & 1][i] > best ? sh.round[picked & 1][i] : best;
+        if (best == 0 || key_logit(best) == -INFINITY) break;
+        below = best;
+        if (tid == 0) sh.picked[picked] = uint16_t(~uint32_t(best));
       }
+      pick = sh.picked;
       __syncthreads();
+    } else if (listed > kPicked) {  // the first k of them
+      for (int i = tid; i < listed; i += kLpThreads) {
+        const int at = sh.listed[i];
+        const uint64_t key = group_key(to_float(group_max[at]), at);
+        int above = 0;
+        for (int j = 0; j < listed; ++j) above += group_key(to_float(group_max[sh.listed[j]]), sh.listed[j]) > key;
+        if (above < A.top_k) sh.picked[above] = uint16_t(at);
+      }
       picked = A.top_k;
-      list = sh.picked;
+      pick = sh.picked;
+      __syncthreads();
     }
-    for (int i = tid; i < picked * kGroup; i += kLpThreads) {
-      const int id = head + (g0 + list[i / kGroup]) * kGroup + i % kGroup;
-      const float v = to_float(x[id]);
-      if (v >= bound && v > -INFINITY) sh.cand[atomicAdd(&sh.num_cand, 1)] = order_key(v, uint32_t(id));
+    for (int i0 = tid; i0 < picked * kGroup; i0 += 4 * kLpThreads) {  // four loads in flight
+      float v[4];
+      int id[4];
+#pragma unroll
+      for (int b = 0; b < 4; ++b) {
+        const int i = i0 + b * kLpThreads;
+        v[b] = -INFINITY;
+        if (i < picked * kGroup) {
+          id[b] = head + (g0 + pick[i / kGroup]) * kGroup + i % kGroup;
+          v[b] = to_float(x[id[b]]);
+        }
+      }
+#pragma unroll
+      for (int b = 0; b < 4; ++b)
+        if (v[b] >= least && v[b] > -INFINITY) sh.cand[atomicAdd(&sh.num_cand, 1)] = order_key(v[b], uint32_t(id[b]));
     }
     __syncthreads();
     found = sh.num_cand;
   }
-  LpShared* to = blocks > 1 ? cluster.map_shared_rank(&sh, 0) : &sh;
-  if (blocks > 1) cluster.barrier_wait();  // the first block is there
   if (A.top_k > 0) {
-    for (int i = tid; i < found; i += kLpThreads) {
-      const uint64_t key = sh.cand[i];
+    for (int i0 = 0; i0 < found; i0 += kLpThreads / 4) {  // four threads count a logit's rank
+      const int i = i0 + (tid >> 2);
+      const uint64_t key = i < found ? sh.cand[i] : 0;
       int above = 0;
-      for (int j = 0; j < found; ++j) above += sh.cand[j] > key;
-      if (above < A.top_k) to->part_key[rank][above] = key;
+      for (int j = tid & 3; j < found; j += 4) above += sh.cand[j] > key;
+      above += __shfl_xor_sync(0xffffffffu, above, 1);
+      above += __shfl_xor_sync(0xffffffffu, above, 2);
+      if ((tid & 3) == 0 && i < found && above < A.top_k) {
+        if (blocks == 1) write_top(above, key);
+        else to->part_key[rank][above] = key;
+      }
+    }
+    if (blocks == 1) {
+      write_none(min(found, A.top_k));
+      return;
     }
     for (int i = found + tid; i < A.top_k; i += kLpThreads) to->part_key[rank][i] = 0;
+    if (tid == 0) to->part_found[rank] = min(found, A.top_k);
   }
-  if (tid == 0) {
-    to->part_m[rank] = m;
-    to->part_s[rank] = total.s;
-    to->part_u[rank] = total.u;
-    to->part_bad[rank] = bad;
-    to->part_found[rank] = min(found, A.top_k);
-  }
-  if (blocks > 1) {
-    cluster.sync();
-    if (rank != 0) return;
-  } else {
-    __syncthreads();
-  }
+  cluster.sync();
+  if (rank != 0) return;
 
-  // the row
+  // the row, from its blocks' shares
   for (int i = 0; i < blocks; ++i) {
     m = fmaxf(m, sh.part_m[i]);
     bad |= sh.part_bad[i] != 0;
   }
-  zmax = m * scale;
-  bad |= m > -INFINITY && !(fabsf(zmax) < INFINITY);
-  float log_s, entropy;
-  if (bad) {
-    log_s = entropy = zmax = NAN;
-  } else if (m == -INFINITY) {
-    log_s = -INFINITY;
-    entropy = 0.f;
-  } else {
-    Sums row{zmax, 0.f, 0.f};
-    for (int i = 0; i < blocks; ++i) {
-      const float zi = sh.part_m[i] * scale;
-      if (zi > -INFINITY) {
-        Sums p{zi, sh.part_s[i], sh.part_u[i]};
-        p.move_to(zmax);
-        row.add(p);
-      }
-    }
-    log_s = logf(row.s);
-    entropy = log_s - row.u / row.s;
+  total = Sums{0.f, 0.f};
+  for (int i = 0; i < blocks && m > -INFINITY; ++i) {
+    const Sums p = Sums{sh.part_s[i], sh.part_u[i]}.moved((sh.part_m[i] - m) * c2);
+    total.s += p.s;
+    total.u += p.u;
   }
-  if (tid == 0) {
-    A.stats[r] = zmax;
-    A.stats[A.num_rows + r] = log_s;
-    A.stats[2 * A.num_rows + r] = entropy;
-    uint32_t word = bad ? MTV_DEVERR_LOGITS : 0;
-    if (scores) {
-      float lp = 0.f;
-      if (token < -1 || token >= A.vocab) {
-        lp = NAN;
-        word |= MTV_DEVERR_TOKEN;
-      } else if (token >= 0) {
-        lp = token_x == -INFINITY && !bad ? -INFINITY : fmaf(token_x, scale, -zmax) - log_s;
-      }
-      A.logprobs[r] = lp;
-    }
-    if (word) set_err(A.err, word);
-  }
+  finish();
   // ranks over the blocks' sorted lists; keys of different logits differ
-  for (int i = tid; i < A.top_k * blocks; i += kLpThreads) {
+  for (int i = tid; i < A.top_k * blocks && !bad; i += kLpThreads) {
     const int b = i / A.top_k, k = i - b * A.top_k;
-    const uint64_t key = bad ? 0 : sh.part_key[b][k];
+    const uint64_t key = sh.part_key[b][k];
     int above = k;
     for (int o = 0; o < blocks; ++o) {
       if (o == b) continue;
@@ -539,18 +592,12 @@ __global__ void __launch_bounds__(kLpThreads) logprob_rows_kernel(const LogprobA
       }
       above += lo;
     }
-    if (key != 0 && above < A.top_k) {
-      A.top_tokens[above * A.num_rows + r] = int32_t(~uint32_t(key));
-      A.top_logprobs[above * A.num_rows + r] = fmaf(key_logit(key), scale, -zmax) - log_s;
-    }
+    if (key != 0 && above < A.top_k) write_top(above, key);
   }
   if (A.top_k > 0) {
-    int have = 0;  // logits above -inf among the lists; the ranks behind them have none
+    int have = 0;  // logits above -inf; the ranks behind them have none
     for (int b = 0; b < blocks && !bad; ++b) have += sh.part_found[b];
-    for (int k = have + tid; k < A.top_k; k += kLpThreads) {
-      A.top_tokens[k * A.num_rows + r] = -1;
-      A.top_logprobs[k * A.num_rows + r] = bad ? NAN : -INFINITY;
-    }
+    write_none(have);
   }
 }
 
@@ -585,18 +632,18 @@ __global__ void __launch_bounds__(kLpThreads) logprob_tokens_kernel(const Logpro
 
 // Blocks a row: enough to give every SM work, as long as each keeps a few
 // groups a thread, and so many that a block's groups fit its shared memory.
-int blocks_per_row(int64_t rows, int vocab) {
-  const int groups = vocab / kGroup;
+int blocks_per_row(int64_t rows, int vocab, int size) {
+  const int groups = vocab / (64 / size);
   int b = 1;
-  while (b < kMaxCluster && (groups > b * kMaxGroups || (rows * b * 2 <= 304 && groups >= b * 2 * 128))) b *= 2;
+  while (b < kMaxCluster && (groups > b * kMaxGroups || (rows * b * 2 <= 304 && groups >= b * 2 * 64))) b *= 2;
   return b;
 }
 
 template <typename T>
 cudaError_t launch_logprobs(const LogprobArgs& A, cudaStream_t st) {
   if (A.num_rows > 0) {
-    const int blocks = blocks_per_row(A.num_rows, A.vocab);
-    const int share = (A.vocab / kGroup + blocks - 1) / blocks;
+    const int blocks = blocks_per_row(A.num_rows, A.vocab, int(sizeof(T)));
+    const int share = (A.vocab / (64 / int(sizeof(T))) + blocks - 1) / blocks;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(unsigned(A.num_rows) * unsigned(blocks));
     cfg.blockDim = dim3(kLpThreads);
