@@ -42,6 +42,170 @@ template <> __device__ __forceinline__ float from_float(float x) { return x; }
 // 64-bit fixed point (the multiplication's wrap drops the whole turns exactly),
 // of which the high 32 bits, signed, go to sincospi as half turns: the angle is
 // off by at most 2^-25 half turns from rounding them to fp32, at any position.
+// Each angle is computed once a token and serves all heads.
+//
+// What bounds it: for many tokens the bytes of the queries' rotary part, read
+// and written once (128-byte pieces of 1152-byte rows); for few the chain
+// position -> angle -> barrier -> store, so every load of the token, whether
+// it turns out valid or not, is issued before the first use of any.
+//
+// Vector form: a thread's unit is 4 or 8 pairs in two 16-byte pieces
+// (neighbours when interleaved, a half apart otherwise).  Its conditions
+// (16-byte alignment of every address, whole units a head) are checked by the
+// launch; the plain form below takes any strides and any even length, a pair
+// at a time.
+__device__ __forceinline__ float2 halves(uint32_t v, __nv_bfloat16) {
+  return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+}
+__device__ __forceinline__ float2 halves(uint32_t v, __half) {
+  return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+__device__ __forceinline__ uint32_t join(float x, float y, __nv_bfloat16) {
+  const __nv_bfloat162 r = __floats2bfloat162_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+__device__ __forceinline__ uint32_t join(float x, float y, __half) {
+  const __half2 r = __floats2half2_rn(x, y);
+  return *reinterpret_cast<const uint32_t*>(&r);
+}
+
+// 16 bytes as fp32 values and back.
+template <typename T> __device__ __forceinline__ void expand(const uint4& v, float* x) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) {
+      x[i] = __uint_as_float(w[i]);
+    } else {
+      const float2 p = halves(w[i], T());
+      x[2 * i] = p.x;
+      x[2 * i + 1] = p.y;
+    }
+  }
+}
+template <typename T> __device__ __forceinline__ uint4 pack(const float* x) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    if constexpr (sizeof(T) == 4) w[i] = __float_as_uint(x[i]);
+    else w[i] = join(x[2 * i], x[2 * i + 1], T());
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+// N fp32 values as bf16: 8 or 16 bytes.
+template <int N> __device__ __forceinline__ void store_bf16(__nv_bfloat16* to, const float* x) {
+  uint32_t w[N / 2];
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) w[i] = join(x[2 * i], x[2 * i + 1], __nv_bfloat16());
+  if constexpr (N == 8) *reinterpret_cast<uint4*>(to) = make_uint4(w[0], w[1], w[2], w[3]);
+  else *reinterpret_cast<uint2*>(to) = make_uint2(w[0], w[1]);
+}
+
+template <typename T, bool kHalf>
+__global__ void __launch_bounds__(kRopeThreads) rope_write_vec_kernel(const RopeArgs A) {
+  constexpr int V = 16 / int(sizeof(T));             // values of 16 bytes: pairs a unit
+  constexpr int kItems = sizeof(T) == 4 ? 4 : 2;     // units in flight a thread
+  constexpr int kLatent = kDLat / (kRopeThreads / 2);  // 8 latent values each for half of the threads
+  __shared__ __align__(16) float cos_s[MTV_MAX_ROPE_DIM / 2], sin_s[MTV_MAX_ROPE_DIM / 2];
+  const int64_t t = blockIdx.x;
+  const int tid = threadIdx.x, pairs = A.rope_dim / 2, units = pairs / V;
+  const int second = kHalf ? pairs : V;
+  auto first = [&](int u) { return kHalf ? u * V : 2 * u * V; };
+
+  const int total = A.q_in ? A.num_heads * units : 0;
+  const T* q_in = static_cast<const T*>(A.q_in) + t * A.q_in_tok;
+  T* q_out = static_cast<T*>(A.q_out) + t * A.q_out_tok;
+  uint4 qa[kItems], qb[kItems];
+  auto load_q = [&](int base) {
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int x = base + i * kRopeThreads;
+      if (x < total) {
+        const int h = x / units, d = first(x - h * units);
+        qa[i] = *reinterpret_cast<const uint4*>(q_in + h * A.q_in_head + d);
+        qb[i] = *reinterpret_cast<const uint4*>(q_in + h * A.q_in_head + d + second);
+      }
+    }
+  };
+  load_q(tid);
+  uint4 la = make_uint4(0, 0, 0, 0), lb = la;  // the latent part, or a unit of the key part
+  int64_t slot = -1;
+  const bool latent = A.pool && tid < kRopeThreads / 2;
+  const bool key = A.pool && tid >= kRopeThreads / 2 && tid - kRopeThreads / 2 < units;
+  const int key_unit = tid - kRopeThreads / 2;
+  if (A.pool) slot = A.out_cache_loc[t];
+  if (latent) {
+    const T* c = static_cast<const T*>(A.c_in) + t * A.c_tok + tid * kLatent;
+    la = *reinterpret_cast<const uint4*>(c);
+    if (V == 4) lb = *reinterpret_cast<const uint4*>(c + 4);
+  } else if (key) {
+    const T* k = static_cast<const T*>(A.k_in) + t * A.k_tok + first(key_unit);
+    la = *reinterpret_cast<const uint4*>(k);
+    lb = *reinterpret_cast<const uint4*>(k + second);
+  }
+  const int64_t valid = A.num_valid ? *A.num_valid : INT64_MAX;
+  const uint64_t pos = uint64_t(A.positions[t]);
+  for (int i = tid; i < pairs; i += kRopeThreads) {
+    float s, c;
+    sincospif(float(int32_t((pos * A.turns[i]) >> 32)) * 0x1p-31f, &s, &c);
+    cos_s[i] = c * A.amplitude;
+    sin_s[i] = (A.inverse ? -s : s) * A.amplitude;
+  }
+  __syncthreads();
+  if (t >= valid) return;
+
+  // pairs u * V .. of a unit; interleaved ones alternate through both registers
+  auto turn = [&](const uint4& a, const uint4& b, int u, float* y) {
+    float x[2 * V], c[V], s[V];
+    expand<T>(a, x);
+    expand<T>(b, x + V);
+#pragma unroll
+    for (int i = 0; i < V; i += 4) {
+      const float4 cc = *reinterpret_cast<const float4*>(&cos_s[u * V + i]);
+      const float4 ss = *reinterpret_cast<const float4*>(&sin_s[u * V + i]);
+      c[i] = cc.x, c[i + 1] = cc.y, c[i + 2] = cc.z, c[i + 3] = cc.w;
+      s[i] = ss.x, s[i + 1] = ss.y, s[i + 2] = ss.z, s[i + 3] = ss.w;
+    }
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+      const int j = kHalf ? i : 2 * i, k = kHalf ? i + V : 2 * i + 1;
+      y[j] = x[j] * c[i] - x[k] * s[i];
+      y[k] = x[j] * s[i] + x[k] * c[i];
+    }
+  };
+  for (int base = tid; base < total; base += kItems * kRopeThreads) {
+    if (base != tid) load_q(base);
+#pragma unroll
+    for (int i = 0; i < kItems; ++i) {
+      const int x = base + i * kRopeThreads;
+      if (x < total) {
+        const int h = x / units, u = x - h * units, d = first(u);
+        float y[2 * V];
+        turn(qa[i], qb[i], u, y);
+        *reinterpret_cast<uint4*>(q_out + h * A.q_out_head + d) = pack<T>(y);
+        *reinterpret_cast<uint4*>(q_out + h * A.q_out_head + d + second) = pack<T>(y + V);
+      }
+    }
+  }
+  if (!A.pool) return;
+  if (slot < 0 || slot >= A.num_slots) {
+    if (tid == 0 && A.err) atomicOr(A.err, MTV_DEVERR_SLOT_RANGE);
+    return;
+  }
+  __nv_bfloat16* row = A.pool + slot * kDQK;
+  if (latent) {
+    float x[2 * V];
+    expand<T>(la, x);
+    if (V == 4) expand<T>(lb, x + 4);
+    store_bf16<kLatent>(row + tid * kLatent, x);
+  } else if (key) {
+    float y[2 * V];
+    turn(la, lb, key_unit, y);
+    store_bf16<V>(row + kDLat + first(key_unit), y);
+    store_bf16<V>(row + kDLat + first(key_unit) + second, y + V);
+  }
+}
+
 template <typename T, bool kHalf>
 __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeArgs A) {
   __shared__ float cos_s[MTV_MAX_ROPE_DIM / 2], sin_s[MTV_MAX_ROPE_DIM / 2];
@@ -95,12 +259,25 @@ __global__ void __launch_bounds__(kRopeThreads) rope_write_kernel(const RopeArgs
   }
 }
 
+// Whether every address that the vector form touches is 16-byte aligned.
+template <typename T> bool vector_form(const RopeArgs& A) {
+  constexpr int64_t v = 16 / int64_t(sizeof(T));
+  uint64_t bits = 0;
+  if (A.q_in)
+    bits |= reinterpret_cast<uintptr_t>(A.q_in) | reinterpret_cast<uintptr_t>(A.q_out) |
+            uint64_t((A.q_in_tok | A.q_in_head | A.q_out_tok | A.q_out_head) % v != 0);
+  if (A.pool)
+    bits |= reinterpret_cast<uintptr_t>(A.k_in) | reinterpret_cast<uintptr_t>(A.c_in) |
+            uint64_t((A.k_tok | A.c_tok) % v != 0);
+  return (bits & 15) == 0 && A.rope_dim % (2 * v) == 0 && int64_t(A.num_heads) * A.rope_dim < INT32_MAX / 2;
+}
+
 template <typename T>
 cudaError_t launch_rope(const RopeArgs& A, int layout, int64_t tokens, cudaStream_t st) {
-  if (layout == MTV_ROPE_HALF)
-    rope_write_kernel<T, true><<<unsigned(tokens), kRopeThreads, 0, st>>>(A);
-  else
-    rope_write_kernel<T, false><<<unsigned(tokens), kRopeThreads, 0, st>>>(A);
+  const bool half = layout == MTV_ROPE_HALF, vec = vector_form<T>(A);
+  auto kernel = vec ? (half ? rope_write_vec_kernel<T, true> : rope_write_vec_kernel<T, false>)
+                    : (half ? rope_write_kernel<T, true> : rope_write_kernel<T, false>);
+  kernel<<<unsigned(tokens), kRopeThreads, 0, st>>>(A);
   return cudaGetLastError();
 }
 
@@ -175,6 +352,10 @@ extern "C" int mla_rope_write(const uint64_t* turns, int rope_dim, float amplitu
   }
   if (num_tokens == 0 || (!kv_pool && (!q_in || num_heads == 0))) return MTV_OK;
   if (!turns || !positions || (kv_pool && (!k_in || !c_in || !out_cache_loc))) return MTV_E_NULL_POINTER;
+  const uintptr_t size = dtype == MTV_DTYPE_FP32 ? 4 : 2;
+  if ((reinterpret_cast<uintptr_t>(q_in) | reinterpret_cast<uintptr_t>(q_out) | reinterpret_cast<uintptr_t>(k_in) |
+       reinterpret_cast<uintptr_t>(c_in)) & (size - 1))
+    return MTV_E_BAD_ARGUMENT;
   const RopeArgs A{turns,  positions, num_valid, q_in, q_out, k_in, c_in, out_cache_loc,
                    static_cast<__nv_bfloat16*>(kv_pool), err, q_in_tok_stride, q_in_head_stride, q_out_tok_stride,
                    q_out_head_stride, k_tok_stride, c_tok_stride, num_slots, amplitude, rope_dim, num_heads, inverse};
