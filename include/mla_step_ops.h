@@ -83,9 +83,8 @@ extern "C" {
  *                free_capacity (pages past it are lost).  MTV_DEVERR_INDPTR:
  *                lens[r] < -1.  A flagged row is left as it is.
  *
- * A page belongs to one row.  One thread-block cluster does the call, so the
- * updates in place need no memory besides these buffers; two calls on the same
- * buffers have to be ordered by the caller.
+ * A page belongs to one row.  The updates in place need no memory besides these
+ * buffers; two calls on the same buffers have to be ordered by the caller.
  */
 int mla_page_table_update(const int32_t* lens, int num_rows, int page_size, int32_t* page_table,
                           int64_t table_stride, int64_t max_pages, int32_t* held, int32_t* free_pages,

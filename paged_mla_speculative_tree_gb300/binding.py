@@ -352,6 +352,11 @@ def tree_group_prefix(group_indptr, num_groups: int, max_group_prefix: int, kv_i
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
+# The current stream's handle without building a Stream object, where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
+    (lambda device: torch.cuda.current_stream(device).cuda_stream)
+
+
 class _Args:
     """Device addresses of one call's tensors, which have to share a device;
     the call is made on that device and, by default, on its current stream."""
@@ -360,44 +365,53 @@ class _Args:
     def __init__(self):
         self.device = None
 
-    def strided(self, t, dtype, name):
-        """Address of a tensor whose strides the call takes."""
-        if t.dtype != dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    def _bind(self, t, name):
         device = t.get_device()
-        if device != self.device:
-            if device < 0:
-                raise TypeError(f"{name} must be a CUDA tensor")
-            if self.device is not None:
-                raise ValueError(f"{name} is on another device")
-            self.device = device
+        if device < 0:
+            raise TypeError(f"{name} must be a CUDA tensor")
+        if self.device is not None:
+            raise ValueError(f"{name} is on another device")
+        self.device = device
+
+    def strided(self, t, dtype, name, shape=None):
+        """Address of a tensor whose strides the call takes."""
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != self.device:
+            self._bind(t, name)
+        if shape is not None and t.shape != shape:
+            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
         return t.data_ptr()
 
     def dense(self, t, dtype, name, shape=None):
         """Address of a contiguous tensor (None stays NULL)."""
         if t is None:
             return None
-        p = self.strided(t, dtype, name)
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+        if t.get_device() != self.device:
+            self._bind(t, name)
         if not t.is_contiguous():
             raise ValueError(f"{name} must be contiguous")
         if shape is not None and t.shape != shape:
             raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        return p
+        return t.data_ptr()
 
-    def call(self, fn, what, stream, check, *args):
+    def call(self, fn, stream, check, *args):
+        device = self.device
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        if isinstance(stream, torch.cuda.Stream):
-            if stream.device_index != self.device:
-                raise ValueError(f"{what}: the stream is on another device than the tensors")
+            stream = _raw_stream(device)
+        elif isinstance(stream, torch.cuda.Stream):
+            if stream.device_index != device:
+                raise ValueError("the stream is on another device than the tensors")
             stream = stream.cuda_stream
-        if self.device == torch.cuda.current_device():
+        if device == torch.cuda.current_device():
             rc = fn(*args, stream)
         else:
-            with torch.cuda.device(self.device):
+            with torch.cuda.device(device):
                 rc = fn(*args, stream)
         if check and rc != MTV_OK:
-            raise MtvError(rc, what)
+            raise MtvError(rc, fn.__name__)
         return rc
 
 
@@ -417,7 +431,7 @@ def page_table_update(lens, page_size: int, page_table, held, free_pages, num_fr
             page_table.stride(0) if rows > 1 else max_pages, max_pages, a.dense(held, torch.int32, "held", (rows,)),
             a.dense(free_pages, torch.int32, "free_pages"), free_pages.numel(),
             a.dense(num_free, torch.int32, "num_free"), a.dense(err, torch.int32, "err"))
-    return a.call(load().mla_page_table_update, "mla_page_table_update", stream, check, *args)
+    return a.call(load().mla_page_table_update, stream, check, *args)
 
 
 def slot_map_build(page_table, prefix_lens, tree_sizes, page_size: int, kv_indptr, kv_indices, qo_indptr,
@@ -447,7 +461,7 @@ def slot_map_build(page_table, prefix_lens, tree_sizes, page_size: int, kv_indpt
             a.dense(qo_indptr, torch.int64, "qo_indptr", (bs + 1,)),
             a.dense(out_cache_loc, torch.int64, "out_cache_loc"), a.dense(positions, torch.int64, "positions"),
             q_capacity, a.dense(err, torch.int32, "err"))
-    return a.call(load().mla_slot_map_build, "mla_slot_map_build", stream, check, *args)
+    return a.call(load().mla_slot_map_build, stream, check, *args)
 
 
 def rope_freqs(rope_dim: int, base: float, scaling: RopeScaling | None = None):
@@ -486,20 +500,17 @@ def rope_write(turns, positions, layout: int = ROPE_INTERLEAVED, amplitude: floa
     tp = a.dense(turns, torch.int64, "turns")
     pp = a.dense(positions, torch.int64, "positions")
 
-    def part(t, name, shape):
-        p = a.strided(t, dtype, name)
-        if t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        if t.stride(-1) != 1:
-            raise ValueError(f"{name} must be dense in its last dimension")
-        return p
-
     q_args = (None, 0, 0, None, 0, 0, 0)
     if q_in is not None:
-        heads = q_in.shape[1] if q_in.dim() == 3 else -1
+        if q_in.dim() != 3:
+            raise ValueError("q_in must be [tokens, heads, rope_dim]")
+        heads = q_in.shape[1]
         shape = (tokens, heads, rope_dim)
-        q_args = (part(q_in, "q_in", shape), q_in.stride(0), q_in.stride(1), part(q_out, "q_out", shape),
-                  q_out.stride(0), q_out.stride(1), heads)
+        qi, qo = q_in.stride(), q_out.stride()
+        q_args = (a.strided(q_in, dtype, "q_in", shape), qi[0], qi[1], a.strided(q_out, dtype, "q_out", shape), qo[0],
+                  qo[1], heads)
+        if qi[2] != 1 or qo[2] != 1:
+            raise ValueError("q_in and q_out must be dense in their last dimension")
     kv_args = (None, 0, None, 0, None, None, 0)
     if kv_pool is not None or c_in is not None or k_in is not None or out_cache_loc is not None:
         if kv_pool is None or c_in is None or k_in is None or out_cache_loc is None:
@@ -507,12 +518,15 @@ def rope_write(turns, positions, layout: int = ROPE_INTERLEAVED, amplitude: floa
         slots = kv_pool.shape[0]
         if slots == 0:
             raise ValueError("kv_pool is empty")
-        kv_args = (part(k_in, "k_in", (tokens, 64)), k_in.stride(0), part(c_in, "c_in", (tokens, 512)), c_in.stride(0),
-                   a.dense(out_cache_loc, torch.int64, "out_cache_loc", (tokens,)),
+        kp, cp = a.strided(k_in, dtype, "k_in", (tokens, 64)), a.strided(c_in, dtype, "c_in", (tokens, 512))
+        ks, cs = k_in.stride(), c_in.stride()
+        if ks[1] != 1 or cs[1] != 1:
+            raise ValueError("k_in and c_in must be dense in their last dimension")
+        kv_args = (kp, ks[0], cp, cs[0], a.dense(out_cache_loc, torch.int64, "out_cache_loc", (tokens,)),
                    a.dense(kv_pool, torch.bfloat16, "kv_pool", (slots, 576)), slots)
     if num_valid is not None and num_valid.numel() != 1:
         raise ValueError("num_valid must hold one element")
-    return a.call(load().mla_rope_write, "mla_rope_write", stream, check, tp, rope_dim, amplitude, layout, int(inverse),
+    return a.call(load().mla_rope_write, stream, check, tp, rope_dim, amplitude, layout, int(inverse),
                   pp, tokens, a.dense(num_valid, torch.int64, "num_valid"), code, *q_args, *kv_args,
                   a.dense(err, torch.int32, "err"))
 
@@ -540,7 +554,7 @@ def token_logprobs(logits, stats, tokens=None, logprobs=None, top_tokens=None, t
             a.dense(logprobs, torch.float32, "logprobs", (n,)), a.dense(stats, torch.float32, "stats", (3, rows)), k,
             a.dense(top_tokens, torch.int32, "top_tokens", (k, rows)),
             a.dense(top_logprobs, torch.float32, "top_logprobs", (k, rows)), a.dense(err, torch.int32, "err"))
-    return a.call(load().mla_token_logprobs, "mla_token_logprobs", stream, check, *args)
+    return a.call(load().mla_token_logprobs, stream, check, *args)
 
 
 class MlaTreeVerify:

@@ -1,7 +1,6 @@
 // Page tables and slot maps of the paged latent pool, built on the GPU from
 // request lengths: the buffers that the verify kernels take their offsets
 // from ("The Final Solder Joint" -- "The Investigation" gives their types).
-#include <cooperative_groups.h>
 #include <stdint.h>
 
 #include "mla_step_ops.h"
@@ -10,7 +9,8 @@
 namespace mtv {
 namespace {
 
-namespace cg = cooperative_groups;
+__device__ __forceinline__ void grid_dependency_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void grid_launch_dependents() { asm volatile("griddepcontrol.launch_dependents;"); }
 
 __device__ __forceinline__ void set_err(uint32_t* err, uint32_t bits) {
   if (err) atomicOr(err, bits);
@@ -34,29 +34,38 @@ __device__ __forceinline__ uint32_t fast_div(uint32_t x, FastDiv f) {
   return uint32_t((uint64_t(x) * f.mul) >> f.shift);
 }
 
-// Inclusive sum over the block of one 64-bit value a thread, in thread order.
-// part: shared, one entry a warp.  Ends with every thread past the last read.
+// Inclusive sums over the block of one or two 64-bit values a thread, in
+// thread order.  part: shared, an entry a warp for each.  Ends with every
+// thread past the last read.
 template <int kThreads>
-__device__ __forceinline__ uint64_t block_inclusive_sum(uint64_t v, uint64_t* part, uint64_t* total) {
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  if (lane == 31) part[w] = v;
-  __syncthreads();
+__device__ __forceinline__ void block_inclusive_sum(uint64_t* a, uint64_t* b, uint64_t* part, uint64_t* a_total,
+                                                    uint64_t* b_total) {
   constexpr int kWarps = kThreads / 32;
-  uint64_t s = lane < kWarps ? part[lane] : 0;
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5;
+  auto warp_sum = [&](uint64_t v) {
 #pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t u = __shfl_up_sync(0xffffffffu, s, o);
-    if (lane >= o) s += u;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t u = __shfl_up_sync(0xffffffffu, v, o);
+      if (lane >= o) v += u;
+    }
+    return v;
+  };
+  *a = warp_sum(*a);
+  if (lane == 31) part[w] = *a;
+  if (b) {
+    *b = warp_sum(*b);
+    if (lane == 31) part[kWarps + w] = *b;
   }
-  const uint64_t before = __shfl_sync(0xffffffffu, s, w > 0 ? w - 1 : 0);
-  *total = __shfl_sync(0xffffffffu, s, kWarps - 1);
   __syncthreads();
-  return v + (w > 0 ? before : 0);
+  auto before = [&](const uint64_t* p, uint64_t* total) {
+    const uint64_t s = warp_sum(lane < kWarps ? p[lane] : 0);
+    *total = __shfl_sync(0xffffffffu, s, kWarps - 1);
+    const uint64_t left = __shfl_sync(0xffffffffu, s, w > 0 ? w - 1 : 0);
+    return w > 0 ? left : 0;
+  };
+  *a += before(part, a_total);
+  if (b) *b += before(part + kWarps, b_total);
+  __syncthreads();
 }
 
 // Largest r in [lo, hi) with off[r] <= x (off non-decreasing, off[lo] <= x).
@@ -77,10 +86,17 @@ __device__ __forceinline__ int find_row(const uint32_t* off, int lo, int hi, uin
 // free_pages[F - 1 - (y - R)].  Released entries x >= G stay on the stack.  So
 // every page moves once, reads and writes never meet (a row releases or grows,
 // not both; stack reads lie below F, writes at or above), and only held and
-// num_free are updated in place: one cluster does the call, every block scans
-// all rows itself, and the two are written after the cluster's barrier.
+// num_free are updated in place: every block scans all rows itself, and the
+// two are written by one more block, a programmatic dependent of the grid whose
+// own scan is done by the time the grid is.  (One cluster for the whole call,
+// with its barrier in place of the second launch, took 9.6 us in place of 8.6
+// for two calls on 256 rows, and 33 in place of 14 us where 1 M pages move.)
 // ---------------------------------------------------------------------------
 constexpr int kPageThreads = 1024;
+constexpr int kRun = 512;
+constexpr int kFewRows = 4;   // of a run that is copied row by row
+constexpr int kSearches = 4;  // entries a lane has in flight otherwise
+constexpr int64_t kPageBlocks = 152;  // one an SM
 
 struct PageArgs {
   const int32_t* lens;
@@ -93,15 +109,17 @@ struct PageArgs {
   int32_t num_rows, page_size, max_pages;
 };
 
-__global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs A) {
+// kState false: a grid moves the pages.  kState true: one block behind it writes
+// held and num_free.
+template <bool kState> __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs A) {
   extern __shared__ uint32_t sm[];
   uint32_t* rel_off = sm;                          // [num_rows + 1]
   uint32_t* grow_off = rel_off + A.num_rows + 1;   // [num_rows + 1]
   uint32_t* base = grow_off + A.num_rows + 1;      // [num_rows]: min(need, held)
   __shared__ uint64_t part[kPageThreads / 32];
-  cg::cluster_group cluster = cg::this_cluster();
-  const int rank = int(cluster.block_rank()), blocks = int(cluster.num_blocks());
+  const int rank = int(blockIdx.x), blocks = int(gridDim.x);
   const int tid = threadIdx.x;
+  if (!kState) grid_launch_dependents();
   const int64_t F = *A.num_free;
   const bool stack_ok = F >= 0 && F <= A.free_capacity;
   uint32_t bad = stack_ok ? 0 : MTV_DEVERR_PAGES;
@@ -127,8 +145,9 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
       }
       base[r] = uint32_t(min(need, held));
     }
-    uint64_t total;
-    const uint64_t incl = block_inclusive_sum<kPageThreads>((uint64_t(rel) << 32) | grow, part, &total) + carry;
+    uint64_t incl = (uint64_t(rel) << 32) | grow, total;
+    block_inclusive_sum<kPageThreads>(&incl, nullptr, part, &total, nullptr);
+    incl += carry;
     carry += total;
     if (r < A.num_rows) {
       rel_off[r + 1] = uint32_t(incl >> 32);
@@ -145,26 +164,104 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
   }
   if (F + R - G > A.free_capacity) bad |= MTV_DEVERR_PAGES;
 
-  if (stack_ok) {
-    const int64_t step = int64_t(blocks) * kPageThreads;
-    for (int64_t y = int64_t(rank) * kPageThreads + tid; y < G; y += step) {
-      const int r = find_row(grow_off, 0, A.num_rows, uint32_t(y));
-      int32_t page;
-      if (y < R) {
-        const int s = find_row(rel_off, 0, A.num_rows, uint32_t(y));
-        page = A.table[s * A.stride + base[s] + (y - rel_off[s])];
-      } else {
-        page = A.free_pages[F - 1 - (y - R)];
+  if (!kState && stack_ok) {
+    // A warp moves runs of 32 or 512 entries.  A run inside a few rows, with
+    // all its pages from the stack (or to it), is copied row by row with up to
+    // 16 loads a lane in flight; any other one searches each entry's row.
+    const int lane = tid & 31;
+    const int64_t warp = int64_t(rank) * (kPageThreads / 32) + (tid >> 5);
+    const int64_t warps = int64_t(blocks) * (kPageThreads / 32);
+    auto copy = [&](int32_t* to, int to_step, const int32_t* from, int from_step, int64_t lo, int64_t hi) {
+      for (int64_t z0 = lo; z0 < hi; z0 += kRun) {  // to[to_step * z] = from[from_step * z]
+        int32_t page[kRun / 32];
+#pragma unroll
+        for (int i = 0; i < kRun / 32; ++i) {
+          const int64_t z = z0 + i * 32 + lane;
+          if (z < hi) page[i] = from[from_step * z];
+        }
+#pragma unroll
+        for (int i = 0; i < kRun / 32; ++i) {
+          const int64_t z = z0 + i * 32 + lane;
+          if (z < hi) to[to_step * z] = page[i];
+        }
       }
-      A.table[r * A.stride + base[r] + (y - grow_off[r])] = page;
+    };
+    const int64_t grow_run = G > warps * 64 ? kRun : 32, rel_run = R - G > warps * 64 ? kRun : 32;
+    for (int64_t y0 = warp * grow_run; y0 < G; y0 += warps * grow_run) {
+      const int64_t y1 = min(y0 + grow_run, G);
+      int r0 = 0, r1 = A.num_rows - 1;
+      if (grow_run == kRun) {
+        r0 = find_row(grow_off, 0, A.num_rows, uint32_t(y0));
+        r1 = find_row(grow_off, r0, A.num_rows, uint32_t(y1 - 1));
+      }
+      if (grow_run == kRun && y0 >= R && r1 - r0 < kFewRows) {
+        for (int r = r0; r <= r1; ++r)
+          copy(A.table + r * A.stride + (int64_t(base[r]) - grow_off[r]), 1, A.free_pages + (F - 1 + R), -1,
+               max(y0, int64_t(grow_off[r])), min(y1, int64_t(grow_off[r + 1])));
+        continue;
+      }
+      for (int64_t y = y0 + lane; y < y1; y += 32 * kSearches) {
+        const int32_t* from[kSearches];
+        int32_t* to[kSearches];
+        int32_t page[kSearches];
+#pragma unroll
+        for (int i = 0; i < kSearches; ++i) {
+          const uint32_t z = uint32_t(y) + i * 32;
+          from[i] = nullptr;
+          if (z < y1) {
+            const int r = find_row(grow_off, r0, r1 + 1, z);
+            to[i] = A.table + r * A.stride + base[r] + (z - grow_off[r]);
+            if (z < R) {
+              const int s = find_row(rel_off, 0, A.num_rows, z);
+              from[i] = A.table + s * A.stride + base[s] + (z - rel_off[s]);
+            } else {
+              from[i] = A.free_pages + (F - 1 - (z - R));
+            }
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kSearches; ++i)
+          if (from[i]) page[i] = *from[i];
+#pragma unroll
+        for (int i = 0; i < kSearches; ++i)
+          if (from[i]) *to[i] = page[i];
+      }
     }
-    for (int64_t x = G + int64_t(rank) * kPageThreads + tid; x < R; x += step) {
-      const int s = find_row(rel_off, 0, A.num_rows, uint32_t(x));
-      const int64_t at = F + R - 1 - x;
-      if (at < A.free_capacity) A.free_pages[at] = A.table[s * A.stride + base[s] + (x - rel_off[s])];
+    const int64_t top = F + R - 1;  // released entry x goes to top - x
+    for (int64_t x0 = G + warp * rel_run; x0 < R; x0 += warps * rel_run) {
+      const int64_t x1 = min(x0 + rel_run, R);
+      int s0 = 0, s1 = A.num_rows - 1;
+      if (rel_run == kRun) {
+        s0 = find_row(rel_off, 0, A.num_rows, uint32_t(x0));
+        s1 = find_row(rel_off, s0, A.num_rows, uint32_t(x1 - 1));
+      }
+      const int64_t lo = max(x0, top - A.free_capacity + 1);  // (those before it would pass the capacity)
+      if (rel_run == kRun && s1 - s0 < kFewRows) {
+        for (int s = s0; s <= s1; ++s)
+          copy(A.free_pages + top, -1, A.table + s * A.stride + (int64_t(base[s]) - rel_off[s]), 1,
+               max(lo, int64_t(rel_off[s])), min(x1, int64_t(rel_off[s + 1])));
+        continue;
+      }
+      for (int64_t x = x0 + lane; x < x1; x += 32 * kSearches) {
+        int32_t page[kSearches];
+#pragma unroll
+        for (int i = 0; i < kSearches; ++i) {
+          const uint32_t z = uint32_t(x) + i * 32;
+          if (z >= lo && z < x1) {
+            const int s = find_row(rel_off, s0, s1 + 1, z);
+            page[i] = A.table[s * A.stride + base[s] + (z - rel_off[s])];
+          }
+        }
+#pragma unroll
+        for (int i = 0; i < kSearches; ++i) {
+          const uint32_t z = uint32_t(x) + i * 32;
+          if (z >= lo && z < x1) A.free_pages[top - z] = page[i];
+        }
+      }
     }
   }
-  cluster.sync();  // every block has read held, num_free and the released entries
+  if (!kState) return;
+  grid_dependency_wait();  // every block of the moves has read held and num_free
   if (stack_ok) {
     for (int r = rank * kPageThreads + tid; r < A.num_rows; r += blocks * kPageThreads) {
       const uint32_t rel = rel_off[r + 1] - rel_off[r], grow = grow_off[r + 1] - grow_off[r];
@@ -173,7 +270,7 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
     }
     if (rank == 0 && tid == 0) *A.num_free = int32_t(min(F + R - G, A.free_capacity));
   }
-  if (rank == 0 && bad) set_err(A.err, bad);
+  if (bad) set_err(A.err, bad);
 }
 
 // ---------------------------------------------------------------------------
@@ -182,6 +279,10 @@ __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs
 // and every gridDim-th request's tree.
 // ---------------------------------------------------------------------------
 constexpr int kMapThreads = 512;
+constexpr int kPairs = 4;        // keys a lane searches at a time
+constexpr int kMaxSteps = 32;    // of 64 keys, in a run
+constexpr int kFewRequests = 4;  // of a run that is written request by request
+constexpr int kMapBlocks = 304;  // two on each of 152 SMs
 constexpr uint32_t kMaxSum = 0x7fffffffu;
 
 struct MapArgs {
@@ -217,11 +318,12 @@ __device__ __forceinline__ int64_t slot_of(const MapArgs& A, int64_t row, uint32
   return int64_t(id) * A.page.d + (j - pg * A.page.d);
 }
 
-__global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const MapArgs A) {
+__global__ void __launch_bounds__(kMapThreads, 2) slot_map_kernel(const MapArgs A) {
   extern __shared__ uint32_t sm[];
   uint32_t* kv_off = sm;                // [bs + 1]
   uint32_t* q_off = kv_off + A.bs + 1;  // [bs + 1]
-  __shared__ uint64_t part[kMapThreads / 32];
+  int32_t* row_of = reinterpret_cast<int32_t*>(q_off + A.bs + 1);  // [bs]
+  __shared__ uint64_t part[2 * kMapThreads / 32];
   __shared__ int up[2][kMapThreads], dep[2][kMapThreads];
   const int tid = threadIdx.x;
   uint32_t bad = 0;
@@ -234,13 +336,15 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const MapArgs A) 
     if (r < A.bs) {
       p = A.prefix[r];
       n = A.tree ? A.tree[r] : 0;
+      row_of[r] = A.rows ? A.rows[r] : r;
       if (p < 0 || n < 0) bad |= MTV_DEVERR_INDPTR;
     }
-    uint64_t total;
-    const uint64_t a = block_inclusive_sum<kMapThreads>(uint64_t(max(p, 0)), part, &total) + kv_carry;
-    kv_carry += total;
-    const uint64_t b = block_inclusive_sum<kMapThreads>(uint64_t(max(n, 0)), part, &total) + q_carry;
-    q_carry += total;
+    uint64_t a = uint64_t(max(p, 0)), b = uint64_t(max(n, 0)), a_total, b_total;
+    block_inclusive_sum<kMapThreads>(&a, &b, part, &a_total, &b_total);
+    a += kv_carry;
+    b += q_carry;
+    kv_carry += a_total;
+    q_carry += b_total;
     if (r < A.bs) {
       kv_off[r + 1] = uint32_t(a < kMaxSum ? a : kMaxSum);
       q_off[r + 1] = uint32_t(b < kMaxSum ? b : kMaxSum);
@@ -259,11 +363,12 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const MapArgs A) 
 
   // trees: slots of their tokens, and positions from their depths
   if (A.out_cache_loc || A.positions) {
-    for (int r = blockIdx.x; r < A.bs; r += gridDim.x) {
+    // (the last blocks first: the prefix keys' remainder falls to the first ones)
+    for (int r = gridDim.x - 1 - blockIdx.x; r < A.bs; r += gridDim.x) {
       const int64_t q0 = q_off[r];
       const int64_t n = min(int64_t(q_off[r + 1]), A.q_capacity) - q0;
       const uint32_t p = kv_off[r + 1] - kv_off[r];
-      const int64_t row = A.rows ? A.rows[r] : r;
+      const int64_t row = row_of[r];
       for (int64_t t0 = 0; t0 < n; t0 += kMapThreads) {
         const int64_t t = t0 + tid;
         const bool live = t < n;
@@ -312,14 +417,69 @@ __global__ void __launch_bounds__(kMapThreads) slot_map_kernel(const MapArgs A) 
     }
   }
 
-  // prefix keys by output position
+  // Prefix keys by output position: a warp writes runs of 64 to 2048 keys.
+  // A run inside a few requests goes request by request, two neighbouring keys
+  // a lane and step, its row and pages checked as a whole; any other one (of
+  // many short requests) searches each key's request.
   if (A.kv_indices) {
+    const int lane = tid & 31;
     const int64_t total = min(int64_t(kv_off[A.bs]), A.kv_capacity);
-    const int64_t step = int64_t(gridDim.x) * kMapThreads;
-    for (int64_t y = int64_t(blockIdx.x) * kMapThreads + tid; y < total; y += step) {
-      const int r = find_row(kv_off, 0, A.bs, uint32_t(y));
-      const int64_t row = A.rows ? A.rows[r] : r;
-      A.kv_indices[y] = slot_of(A, row, uint32_t(y) - kv_off[r], &bad);
+    const uint32_t limit = uint32_t(min(A.num_pages, int64_t(1) << 31));  // of an entry; negative ones wrap past it
+    // runs short enough to give every warp one, of 64 to 2048 keys
+    const int run = 64 * int(min(max(total / (64 * int64_t(gridDim.x) * (kMapThreads / 32)), int64_t(1)), int64_t(kMaxSteps)));
+    const int64_t step = int64_t(gridDim.x) * (kMapThreads / 32) * run;
+    for (int64_t y0 = (int64_t(blockIdx.x) * (kMapThreads / 32) + (tid >> 5)) * run; y0 < total; y0 += step) {
+      const int64_t y1 = min(y0 + run, total);
+      const int r0 = find_row(kv_off, 0, A.bs, uint32_t(y0));
+      const int r1 = find_row(kv_off, r0, A.bs, uint32_t(y1 - 1));
+      if (r1 - r0 >= kFewRequests) {
+        for (int64_t y = y0 + lane; y < y1; y += 32 * kPairs) {
+          int64_t slot[kPairs];
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i) {
+            const int64_t z = y + i * 32;
+            if (z < y1) {
+              const int r = find_row(kv_off, r0, r1 + 1, uint32_t(z));
+              slot[i] = slot_of(A, row_of[r], uint32_t(z) - kv_off[r], &bad);
+            }
+          }
+#pragma unroll
+          for (int i = 0; i < kPairs; ++i)
+            if (y + i * 32 < y1) A.kv_indices[y + i * 32] = slot[i];
+        }
+        continue;
+      }
+      for (int r = r0; r <= r1; ++r) {
+        const int64_t lo = max(y0, int64_t(kv_off[r])), hi = min(y1, int64_t(kv_off[r + 1]));
+        if (lo >= hi) continue;
+        const int64_t row = row_of[r];
+        const uint32_t j0 = uint32_t(lo) - kv_off[r], keys = uint32_t(hi - lo);  // tokens [j0, j0 + keys)
+        if (row < 0 || row >= A.num_rows || int64_t(fast_div(j0 + keys - 1, A.page)) >= A.max_pages) {
+          for (int64_t y = lo + lane; y < hi; y += 32)
+            A.kv_indices[y] = slot_of(A, row, uint32_t(y) - kv_off[r], &bad);
+          continue;
+        }
+        const int32_t* pages = A.table + row * A.stride;
+        int64_t* to = A.kv_indices + lo;
+        // a lane's pair starts on 16 bytes: the segment's first one may lack its first key
+        const int shift = int(reinterpret_cast<uintptr_t>(to) >> 3) & 1;
+        const int steps = (int(keys) + shift + 63) / 64;
+#pragma unroll 4
+        for (int i = 0; i < steps; ++i) {
+          const int k = i * 64 + lane * 2 - shift;
+          if (k < int(keys)) {
+            const uint32_t j = j0 + uint32_t(max(k, 0)), a = fast_div(j, A.page), off = j - a * A.page.d;
+            const bool turns = off + 1 == A.page.d, both = k >= 0 && k + 1 < int(keys);
+            const int32_t id = __ldg(pages + a), next = turns && both ? __ldg(pages + a + 1) : id;
+            const bool ok = uint32_t(id) < limit, next_ok = uint32_t(next) < limit;
+            if (!ok || !next_ok) bad |= MTV_DEVERR_PAGES;
+            const int64_t x = ok ? int64_t(id) * A.page.d + off : -1;
+            const int64_t y = next_ok ? int64_t(next) * A.page.d + (turns ? 0 : off + 1) : -1;
+            if (both) *reinterpret_cast<longlong2*>(to + k) = make_longlong2(x, y);
+            else to[max(k, 0)] = x;
+          }
+        }
+      }
     }
   }
   if (bad) set_err(A.err, bad);
@@ -356,20 +516,25 @@ extern "C" int mla_page_table_update(const int32_t* lens, int num_rows, int page
   const PageArgs A{lens,  page_table,   held,          free_pages, num_free,  err,
                    table_stride, free_capacity, num_rows,   page_size, int32_t(max_pages)};
   const size_t smem = (3 * size_t(num_rows) + 2) * 4;
-  cudaError_t e = allow_smem(page_table_kernel, smem);
+  cudaError_t e = allow_smem(page_table_kernel<false>, smem);
+  if (e == cudaSuccess) e = allow_smem(page_table_kernel<true>, smem);
   if (e != cudaSuccess) return launch_code(e);
-  const unsigned blocks = int64_t(num_rows) * max_pages > 8192 ? 8 : 1;
+  // blocks for at most one entry a thread, as far as that goes
+  const int64_t blocks = (int64_t(num_rows) * max_pages + kPageThreads - 1) / kPageThreads;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(blocks);
+  cfg.gridDim = dim3(unsigned(blocks < 1 ? 1 : blocks > kPageBlocks ? kPageBlocks : blocks));
   cfg.blockDim = dim3(kPageThreads);
   cfg.dynamicSmemBytes = smem;
   cfg.stream = static_cast<cudaStream_t>(stream);
+  e = cudaLaunchKernelEx(&cfg, page_table_kernel<false>, A);
+  if (e != cudaSuccess) return launch_code(e);
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim = {blocks, 1, 1};
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  return launch_code(cudaLaunchKernelEx(&cfg, page_table_kernel, A));
+  cfg.gridDim = dim3(1);
+  return launch_code(cudaLaunchKernelEx(&cfg, page_table_kernel<true>, A));
 }
 
 extern "C" int mla_slot_map_build(const int32_t* page_table, int64_t table_stride, int64_t num_rows,
@@ -388,12 +553,12 @@ extern "C" int mla_slot_map_build(const int32_t* page_table, int64_t table_strid
   const MapArgs A{page_table, rows,         prefix_lens, tree_sizes, parents,   kv_indptr, kv_indices,
                   qo_indptr,  out_cache_loc, positions,   err,        table_stride, num_rows,  max_pages,
                   num_pages,  kv_capacity,   q_capacity,  make_fast_div(uint32_t(page_size)), bs};
-  const size_t smem = 2 * (size_t(bs) + 1) * 4;
+  const size_t smem = (3 * size_t(bs) + 2) * 4;
   cudaError_t e = allow_smem(slot_map_kernel, smem);
   if (e != cudaSuccess) return launch_code(e);
-  int64_t blocks = kv_indices ? (kv_capacity + kMapThreads - 1) / kMapThreads : 0;
+  int64_t blocks = kv_indices ? (kv_capacity + 64 * (kMapThreads / 32) - 1) / (64 * (kMapThreads / 32)) : 0;
   if (blocks < bs) blocks = bs;
-  if (blocks > 608) blocks = 608;
+  if (blocks > kMapBlocks) blocks = kMapBlocks;
   if (blocks < 1) blocks = 1;
   slot_map_kernel<<<unsigned(blocks), kMapThreads, smem, static_cast<cudaStream_t>(stream)>>>(A);
   return launch_code(cudaSuccess);
