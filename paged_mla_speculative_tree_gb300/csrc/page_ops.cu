@@ -87,16 +87,18 @@ __device__ __forceinline__ int find_row(const uint32_t* off, int lo, int hi, uin
 // every page moves once, reads and writes never meet (a row releases or grows,
 // not both; stack reads lie below F, writes at or above), and only held and
 // num_free are updated in place: every block scans all rows itself, and the
-// two are written by one more block, a programmatic dependent of the grid whose
-// own scan is done by the time the grid is.  (One cluster for the whole call,
-// with its barrier in place of the second launch, took 9.6 us in place of 8.6
-// for two calls on 256 rows, and 33 in place of 14 us where 1 M pages move.)
+// two are written at the end -- by the one block of a small table, or by one
+// more block behind a grid, its programmatic dependent, whose own scan is done
+// by the time the grid is.  (One cluster of 16 blocks with its barrier in
+// place of the second launch took 33 us where the grid takes 10, for 1 M pages
+// in and out.)
 // ---------------------------------------------------------------------------
-constexpr int kPageThreads = 1024;
+constexpr int kPageThreads = 512;
 constexpr int kRun = 512;
 constexpr int kFewRows = 4;   // of a run that is copied row by row
 constexpr int kSearches = 4;  // entries a lane has in flight otherwise
-constexpr int64_t kPageBlocks = 152;  // one an SM
+constexpr int64_t kPageBlocks = 152;         // of the grid: one an SM
+constexpr int64_t kBlockEntries = 1 << 14;  // tables that one block does: one launch, at 4 us
 
 struct PageArgs {
   const int32_t* lens;
@@ -109,9 +111,13 @@ struct PageArgs {
   int32_t num_rows, page_size, max_pages;
 };
 
-// kState false: a grid moves the pages.  kState true: one block behind it writes
-// held and num_free.
-template <bool kState> __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs A) {
+enum PageMode {
+  kAll,    // one block does the call
+  kMoves,  // a grid moves the pages ...
+  kState,  // ... and one block behind it writes held and num_free
+};
+
+template <int kMode> __global__ void __launch_bounds__(kPageThreads) page_table_kernel(const PageArgs A) {
   extern __shared__ uint32_t sm[];
   uint32_t* rel_off = sm;                          // [num_rows + 1]
   uint32_t* grow_off = rel_off + A.num_rows + 1;   // [num_rows + 1]
@@ -119,7 +125,7 @@ template <bool kState> __global__ void __launch_bounds__(kPageThreads) page_tabl
   __shared__ uint64_t part[kPageThreads / 32];
   const int rank = int(blockIdx.x), blocks = int(gridDim.x);
   const int tid = threadIdx.x;
-  if (!kState) grid_launch_dependents();
+  if (kMode == kMoves) grid_launch_dependents();
   const int64_t F = *A.num_free;
   const bool stack_ok = F >= 0 && F <= A.free_capacity;
   uint32_t bad = stack_ok ? 0 : MTV_DEVERR_PAGES;
@@ -164,7 +170,7 @@ template <bool kState> __global__ void __launch_bounds__(kPageThreads) page_tabl
   }
   if (F + R - G > A.free_capacity) bad |= MTV_DEVERR_PAGES;
 
-  if (!kState && stack_ok) {
+  if (kMode != kState && stack_ok) {
     // A warp moves runs of 32 or 512 entries.  A run inside a few rows, with
     // all its pages from the stack (or to it), is copied row by row with up to
     // 16 loads a lane in flight; any other one searches each entry's row.
@@ -260,8 +266,10 @@ template <bool kState> __global__ void __launch_bounds__(kPageThreads) page_tabl
       }
     }
   }
-  if (!kState) return;
-  grid_dependency_wait();  // every block of the moves has read held and num_free
+  if (kMode == kMoves) return;
+  // every thread or block of the moves has read held and num_free
+  if (kMode == kAll) __syncthreads();
+  else grid_dependency_wait();
   if (stack_ok) {
     for (int r = rank * kPageThreads + tid; r < A.num_rows; r += blocks * kPageThreads) {
       const uint32_t rel = rel_off[r + 1] - rel_off[r], grow = grow_off[r + 1] - grow_off[r];
@@ -516,25 +524,32 @@ extern "C" int mla_page_table_update(const int32_t* lens, int num_rows, int page
   const PageArgs A{lens,  page_table,   held,          free_pages, num_free,  err,
                    table_stride, free_capacity, num_rows,   page_size, int32_t(max_pages)};
   const size_t smem = (3 * size_t(num_rows) + 2) * 4;
-  cudaError_t e = allow_smem(page_table_kernel<false>, smem);
-  if (e == cudaSuccess) e = allow_smem(page_table_kernel<true>, smem);
+  const int64_t entries = int64_t(num_rows) * max_pages;
+  cudaStream_t st = static_cast<cudaStream_t>(stream);
+  if (entries <= kBlockEntries) {
+    const cudaError_t e = allow_smem(page_table_kernel<kAll>, smem);
+    if (e != cudaSuccess) return launch_code(e);
+    page_table_kernel<kAll><<<1, kPageThreads, smem, st>>>(A);
+    return launch_code(cudaSuccess);
+  }
+  cudaError_t e = allow_smem(page_table_kernel<kMoves>, smem);
+  if (e == cudaSuccess) e = allow_smem(page_table_kernel<kState>, smem);
   if (e != cudaSuccess) return launch_code(e);
-  // blocks for at most one entry a thread, as far as that goes
-  const int64_t blocks = (int64_t(num_rows) * max_pages + kPageThreads - 1) / kPageThreads;
+  const int64_t blocks = (entries + kPageThreads - 1) / kPageThreads;
+  page_table_kernel<kMoves><<<unsigned(blocks < kPageBlocks ? blocks : kPageBlocks), kPageThreads, smem, st>>>(A);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return launch_code(e);
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(unsigned(blocks < 1 ? 1 : blocks > kPageBlocks ? kPageBlocks : blocks));
+  cfg.gridDim = dim3(1);
   cfg.blockDim = dim3(kPageThreads);
   cfg.dynamicSmemBytes = smem;
-  cfg.stream = static_cast<cudaStream_t>(stream);
-  e = cudaLaunchKernelEx(&cfg, page_table_kernel<false>, A);
-  if (e != cudaSuccess) return launch_code(e);
+  cfg.stream = st;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  cfg.gridDim = dim3(1);
-  return launch_code(cudaLaunchKernelEx(&cfg, page_table_kernel<true>, A));
+  return launch_code(cudaLaunchKernelEx(&cfg, page_table_kernel<kState>, A));
 }
 
 extern "C" int mla_slot_map_build(const int32_t* page_table, int64_t table_stride, int64_t num_rows,
