@@ -79,13 +79,23 @@ constexpr int kBuckets = 64;
 constexpr int kBucketThreads = kLpThreads / kBuckets;
 constexpr int kMaxCluster = 8;
 
-// 16 bytes of logits in four registers.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float r;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+  return r;
+}
+
+// 16 bytes of logits in four registers.  Maxima stay in one register of the
+// logits' type (two of them for 16-bit types) until one value is needed.
 template <typename T> struct Chunk;
 template <> struct Chunk<__nv_bfloat16> {
   static constexpr uint32_t kNone = 0xff80ff80u;  // -inf
-  static __device__ __forceinline__ float max(const uint32_t* v) {
-    const __nv_bfloat162 m = __hmax2_nan(__hmax2_nan(pair(v[0]), pair(v[1])), __hmax2_nan(pair(v[2]), pair(v[3])));
-    return __bfloat162float(__hmax_nan(__low2bfloat16(m), __high2bfloat16(m)));
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    const __nv_bfloat162 m = __hmax2_nan(pair(a), pair(b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  static __device__ __forceinline__ float value(uint32_t m) {
+    return max_nan(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
   }
   static __device__ __forceinline__ float2 get(const uint32_t* v, int i) {
     return make_float2(__uint_as_float(v[i] << 16), __uint_as_float(v[i] & 0xffff0000u));
@@ -97,25 +107,24 @@ template <> struct Chunk<__nv_bfloat16> {
 };
 template <> struct Chunk<__half> {
   static constexpr uint32_t kNone = 0xfc00fc00u;
-  static __device__ __forceinline__ float max(const uint32_t* v) {
-    const __half2 m = __hmax2_nan(__hmax2_nan(pair(v[0]), pair(v[1])), __hmax2_nan(pair(v[2]), pair(v[3])));
-    return __half2float(__hmax_nan(__low2half(m), __high2half(m)));
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    const __half2 m = __hmax2_nan(pair(a), pair(b));
+    return *reinterpret_cast<const uint32_t*>(&m);
+  }
+  static __device__ __forceinline__ float value(uint32_t m) {
+    const float2 p = __half22float2(pair(m));
+    return max_nan(p.x, p.y);
   }
   static __device__ __forceinline__ float2 get(const uint32_t* v, int i) { return __half22float2(pair(v[i])); }
   static __device__ __forceinline__ __half2 pair(uint32_t x) { return *reinterpret_cast<__half2*>(&x); }
   static __device__ __forceinline__ __half narrow(float x) { return __float2half_rn(x); }
 };
-__device__ __forceinline__ float max_nan(float a, float b) {
-  float r;
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
-  return r;
-}
 template <> struct Chunk<float> {
   static constexpr uint32_t kNone = 0xff800000u;
-  static __device__ __forceinline__ float max(const uint32_t* v) {
-    return max_nan(max_nan(__uint_as_float(v[0]), __uint_as_float(v[1])),
-                   max_nan(__uint_as_float(v[2]), __uint_as_float(v[3])));
+  static __device__ __forceinline__ uint32_t larger(uint32_t a, uint32_t b) {
+    return __float_as_uint(max_nan(__uint_as_float(a), __uint_as_float(b)));
   }
+  static __device__ __forceinline__ float value(uint32_t m) { return __uint_as_float(m); }
   static __device__ __forceinline__ float2 get(const uint32_t* v, int i) {
     return make_float2(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]));
   }
@@ -241,13 +250,11 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
   // from the lanes that hold its chunks; lane l ends up with group own + step.
   const int own = w * 32 + (lane % kChunks) * (32 / kChunks) + lane / kChunks;
   auto process = [&](const uint32_t* v, int step) {
-    float c[kChunks];
-    float m = -INFINITY;
+    uint32_t c[kChunks];
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-      c[i] = Chunk<T>::max(v + 4 * i);
-      m = max_nan(m, c[i]);
-    }
+    for (int i = 0; i < kChunks; ++i)
+      c[i] = Chunk<T>::larger(Chunk<T>::larger(v[4 * i], v[4 * i + 1]), Chunk<T>::larger(v[4 * i + 2], v[4 * i + 3]));
+    const float m = Chunk<T>::value(Chunk<T>::larger(Chunk<T>::larger(c[0], c[1]), Chunk<T>::larger(c[2], c[3])));
     worst = max_nan(worst, m);
     // run r of the maxima goes to the lanes with lane % kChunks == r, halving the runs each time
 #pragma unroll
@@ -255,16 +262,17 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
       const bool upper = (lane & h) != 0;
 #pragma unroll
       for (int i = 0; i < h; ++i) {
-        const float other = __shfl_xor_sync(0xffffffffu, upper ? c[i] : c[i + h], h);
-        c[i] = fmaxf(upper ? c[i + h] : c[i], other);
+        const uint32_t other = __shfl_xor_sync(0xffffffffu, upper ? c[i] : c[i + h], h);
+        c[i] = Chunk<T>::larger(upper ? c[i + h] : c[i], other);
       }
     }
+    const float gm = Chunk<T>::value(c[0]);
     const int g = own + step;
     if (g < n) {
-      group_max[g] = Chunk<T>::narrow(c[0]);
-      tnext = fmaxf(tnext, fminf(c[0], tmax));
-      if (c[0] > tmax) {
-        tmax = c[0];
+      group_max[g] = Chunk<T>::narrow(gm);
+      tnext = fmaxf(tnext, fminf(gm, tmax));
+      if (gm > tmax) {
+        tmax = gm;
         tgroup = g;
       }
     }
@@ -300,27 +308,23 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
     }
     u2 = add2(u2, ug);
   };
-  constexpr int kBatch = 1;  // steps in flight
   constexpr int kChunkLogits = 16 / int(sizeof(T));
 #pragma unroll 1
-  for (int step = 0; w * 32 + step < n; step += kBatch * kLpThreads) {
-    uint32_t v[kBatch][4 * kChunks];
+  for (int step = 0; w * 32 + step < n; step += kLpThreads) {
+    const int from = w * 32 + step;
+    const T* at = body + int64_t(from) * kGroup + lane * kChunkLogits;
+    uint32_t v[4 * kChunks];
+    if (from + 32 <= n) {
 #pragma unroll
-    for (int b = 0; b < kBatch; ++b) {
-      const int from = w * 32 + step + b * kLpThreads;
+      for (int i = 0; i < kChunks; ++i) load16(at + i * 32 * kChunkLogits, v + 4 * i);
+    } else {
 #pragma unroll
       for (int i = 0; i < kChunks; ++i) {
-        const int chunk = i * 32 + lane;  // of the step's 32 * kChunks
-        if (from + chunk / kChunks < n) {
-          load16(body + int64_t(from) * kGroup + chunk * kChunkLogits, &v[b][4 * i]);
-        } else {
-          v[b][4 * i] = v[b][4 * i + 1] = v[b][4 * i + 2] = v[b][4 * i + 3] = Chunk<T>::kNone;
-        }
+        if (from + (i * 32 + lane) / kChunks < n) load16(at + i * 32 * kChunkLogits, v + 4 * i);
+        else v[4 * i] = v[4 * i + 1] = v[4 * i + 2] = v[4 * i + 3] = Chunk<T>::kNone;
       }
     }
-#pragma unroll
-    for (int b = 0; b < kBatch; ++b)
-      if (w * 32 + step + b * kLpThreads < n) process(v[b], step + b * kLpThreads);
+    process(v, step);
   }
   fold();
   bad |= !(worst < INFINITY);
