@@ -150,6 +150,51 @@ def test_pages_capture_and_replay():
     p.expect(table, held, free)
 
 
+@pytest.mark.parametrize("rows,per", [(900, 40), (1, 30000)])
+def test_pages_of_a_large_table_capture_and_replay(rows, per):
+    """Over 16384 entries: a grid of moves with the state written behind it."""
+    _, table, held, free = page_state(rows, rows, per, 2, fill=0.4)
+    lens = [h * 2 for h in held]
+    p, up, down = Pages(table, held, free), i32([n + per // 2 for n in lens]), i32([max(0, n - per // 3) for n in lens])
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            for v in (up, down, up):
+                pkg.page_table_update(v, 2, p.table, p.held, p.free, p.num, p.err)
+    for _ in range(2):
+        graph.replay()
+        for v in (up, down, up):
+            table, held, free, flagged = S.page_table_update(v.tolist(), 2, table, held, free)
+            assert not flagged
+    p.expect(table, held, free)
+
+
+def test_pages_of_rows_without_entries():
+    p = Pages([[1], [2]], [0, 0], [7, 8])
+    empty = torch.empty((2, 0), dtype=torch.int32, device=DEV)
+    pkg.page_table_update(i32([0, -1]), 4, empty, p.held, p.free, p.num, p.err)
+    p.expect([[1], [2]], [0, 0], [7, 8])
+    pkg.page_table_update(i32([0, 1]), 4, empty, p.held, p.free, p.num, p.err)
+    p.expect([[1], [2]], [0, 0], [7, 8], binding.DEVERR_PAGES)
+
+
+def test_two_updates_at_once_on_two_streams():
+    states = [page_state(50 + k, 300, 90, 1, fill=0.5) for k in range(2)]
+    pages = [Pages(*st[1:]) for st in states]
+    lens = [[int(x) for x in st[0].integers(0, 91, 300)] for st in states]
+    dev = [i32(v) for v in lens]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for k in range(2):
+            pkg.page_table_update(dev[k], 1, pages[k].table, pages[k].held, pages[k].free, pages[k].num, pages[k].err,
+                                  stream=streams[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        pages[k].expect(*S.page_table_update(lens[k], 1, *states[k][1:])[:3])
+
+
 # ---------------------------------------------------------------- slot maps
 
 def build_slots(table, page, prefix, tree, rows=None, parents=None, kv_cap=None, q_cap=None, num_pages=None, pad=5,
@@ -222,6 +267,41 @@ def test_slot_maps_without_rows_trees_or_outputs():
     empty = torch.empty(0, dtype=torch.int32, device=DEV)
     pkg.slot_map_build(i32(table), empty, empty, 8, kvp[:1], i64([1]), qop[:1], i64([1]), num_pages=9)
     assert int(kvp[0]) == 0 and int(qop[0]) == 0
+
+
+@pytest.mark.parametrize("bs,max_p,page", [(3, 5000, 16), (700, 9, 4), (20, 130, 1), (2, 70000, 64)])
+def test_slot_maps_into_odd_addresses(bs, max_p, page):
+    """kv_indices 8 bytes past a 16-byte boundary, its neighbours untouched."""
+    table, rows, prefix, tree, _ = slot_case(bs + max_p, bs, max_p, 3, page)
+    want = S.slot_map(table, page, rows, prefix, tree, None)
+    buf = torch.full((sum(prefix) + 2,), -4, dtype=torch.int64, device=DEV)
+    kvp, qop, loc = i32([0] * (bs + 1)), i64([0] * (bs + 1)), torch.empty(sum(tree) + 1, dtype=torch.int64, device=DEV)[1:]
+    pkg.slot_map_build(i32(table), i32(prefix), i32(tree), page, kvp, buf[1:-1], qop, loc, rows=i32(rows), num_pages=1 << 20)
+    np.testing.assert_array_equal(buf[1:-1].cpu().numpy(), want[1])
+    np.testing.assert_array_equal(loc.cpu().numpy(), want[3])
+    assert int(buf[0]) == -4 and int(buf[-1]) == -4
+
+
+def test_slot_maps_capture_and_replay_with_new_lengths():
+    table, rows, _, _, _ = slot_case(31, 6, 400, 20, 16)
+    p, n, t, r = i32([0] * 6), i32([0] * 6), i32(table), i32(rows)
+    o = dict(kv_indptr=i32([0] * 7), kv_indices=torch.full((2400,), -4, dtype=torch.int64, device=DEV), qo_indptr=i64([0] * 7),
+             out_cache_loc=torch.full((120,), -4, dtype=torch.int64, device=DEV))
+    s = torch.cuda.Stream()
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            pkg.slot_map_build(t, p, n, 16, *o.values(), rows=r, num_pages=10000)
+    rng = np.random.default_rng(8)
+    for _ in range(3):
+        prefix, tree = [int(x) for x in rng.integers(0, 401, 6)], [int(x) for x in rng.integers(0, 21, 6)]
+        p.copy_(i32(prefix))
+        n.copy_(i32(tree))
+        for v in (o["kv_indices"], o["out_cache_loc"]):
+            v.fill_(-4)
+        graph.replay()
+        torch.cuda.synchronize()
+        check_slots({k: v.cpu().numpy() for k, v in o.items()}, S.slot_map(table, 16, rows, prefix, tree, None)[:4])
 
 
 @pytest.mark.parametrize("shape", ["chain", "star", "deep"])
@@ -584,6 +664,43 @@ def test_logprobs_are_repeatable_and_capture(rows):
         torch.cuda.synchronize()
         for a, b in zip(*outs):
             assert torch.equal(a, b)
+
+
+def test_two_calls_at_once_on_two_streams():
+    """Rows and their tokens' kernel on two streams, each on its own buffers."""
+    x = [make_logits(21 + k, 200, 20011, torch.bfloat16) for k in range(2)]
+    trow = i32([(7 * i) % 200 for i in range(500)])
+    tokens = i32([(131 * i) % 20011 for i in range(500)])
+    new = lambda: [torch.zeros((3, 200), device=DEV), torch.zeros(500, device=DEV),  # noqa: E731
+                   torch.zeros((4, 200), dtype=torch.int32, device=DEV), torch.zeros((4, 200), device=DEV)]
+    want, got = [new(), new()], [new(), new()]
+    for k in range(2):
+        pkg.token_logprobs(x[k], want[k][0], tokens, *want[k][1:], token_rows=trow)
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for k in range(2):
+            pkg.token_logprobs(x[k], got[k][0], tokens, *got[k][1:], token_rows=trow, stream=streams[k])
+    torch.cuda.synchronize()
+    for k in range(2):
+        for a, b in zip(want[k], got[k]):
+            assert torch.equal(a, b)
+
+
+def test_a_call_runs_on_its_tensors_device(monkeypatch):
+    """Another current device: the call enters the tensors' one (device 0 here)."""
+    x = make_logits(30, 2, 300, torch.float32)
+    a, b = torch.zeros((3, 2), device=DEV), torch.zeros((3, 2), device=DEV)
+    pkg.token_logprobs(x, a)
+    entered = []
+    real = torch.cuda.device
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    monkeypatch.setattr(torch.cuda, "device", lambda d: entered.append(d) or real(0))
+    pkg.token_logprobs(x, b)
+    monkeypatch.undo()
+    assert entered == [0] and torch.equal(a, b)
+    with pytest.raises(ValueError, match="one element"):
+        pkg.rope_write(i64([1]), i64([0]), q_in=x.view(2, 1, 300)[:1, :, :2], q_out=x.view(2, 1, 300)[:1, :, :2], num_valid=i64([1, 1]))
 
 
 # ------------------------------------------------------------- the whole step
