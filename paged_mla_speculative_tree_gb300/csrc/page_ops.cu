@@ -16,22 +16,24 @@ __device__ __forceinline__ void set_err(uint32_t* err, uint32_t bits) {
   if (err) atomicOr(err, bits);
 }
 
-// Division by a host-known divisor d >= 1 of numerators below 2^31:
-// floor(x / d) = x * ceil(2^(31+s) / d) >> (31 + s) with 2^s >= d, since the
-// product is too large by less than 2^31 * 2^s / 2^(31+s) = 1 (in units of 1/d).
+// Division by a host-known divisor d of numerators below 2^31: with 2^s >= d,
+// s >= 1, floor(x / d) = x * ceil(2^(31+s) / d) >> (31 + s), since the product
+// is too large by less than 2^31 * 2^s / 2^(31+s) = 1 (in units of 1/d); the
+// high word of the product, shifted by s - 1.  mul == 0 stands for d == 1.
 struct FastDiv {
   uint32_t d, mul, shift;
 };
 
 FastDiv make_fast_div(uint32_t d) {
-  uint32_t s = 0;
+  if (d == 1) return FastDiv{1, 0, 0};
+  uint32_t s = 1;
   while ((uint64_t(1) << s) < d) ++s;
   const uint64_t m = ((uint64_t(1) << (31 + s)) + d - 1) / d;
-  return FastDiv{d, uint32_t(m), 31 + s};
+  return FastDiv{d, uint32_t(m), s - 1};
 }
 
 __device__ __forceinline__ uint32_t fast_div(uint32_t x, FastDiv f) {
-  return uint32_t((uint64_t(x) * f.mul) >> f.shift);
+  return f.mul ? __umulhi(x, f.mul) >> f.shift : x;
 }
 
 // Inclusive sums over the block of one or two 64-bit values a thread, in
