@@ -282,7 +282,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
     const float z = m * c2;
     if (z > ref + kRefSlack) {
       fold();
-      if (ref > kLowest) acc = acc.moved(ref - z);
+      acc = acc.moved(ref - z);
       ref = z;
     }
     const uint64_t ref2 = pack2(-ref, -ref);
@@ -342,7 +342,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
     bad |= !(edge < INFINITY);
     const float z = edge * c2;
     if (z > ref + kRefSlack) {
-      if (ref > kLowest) acc = acc.moved(ref - z);
+      acc = acc.moved(ref - z);
       ref = z;
     }
     const float t = fmaf(edge, c2, -ref), e = exp2_approx(t);
@@ -375,7 +375,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
   Sums total{0.f, 0.f};
   if (m > -INFINITY && !bad) {
     if (fabsf(m * c2) < 0x1p30f) {
-      if (ref > kLowest) total = acc.moved(fmaf(-c2, m, ref));
+      total = acc.moved(fmaf(-c2, m, ref));
     } else {
       // so far from 0 that a reference's rounding (2^-24 of it) is no longer a
       // small t: once more, from differences to the maximum
@@ -426,7 +426,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
       to->part_bad[rank] = bad;
     }
   }
-  // what a single block knows of the row already, the first of several later
+  // What a single block knows of the row already, the first of several later:
   // m times the scale rounds; what that leaves goes into ln S, so that one
   // fused multiply-add z - zmax, less ln S, is right to the roundings of both
   float zmax, log_s, entropy;

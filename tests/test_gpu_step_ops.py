@@ -601,6 +601,20 @@ def test_logprobs_flag_bad_rows_alone(dtype, vocab):
         check_logprobs(z, [0, 0], inv=torch.tensor([2.0, 2.0], device=DEV), k=2, err=binding.DEVERR_LOGITS)
 
 
+@pytest.mark.parametrize("vocab", [33, 40000])
+def test_logprobs_masked_with_the_lowest_value_at_a_scale_of_one_bit(vocab):
+    """c = log2(e) / temperature rounds to 1, so that a mask of fp32's lowest
+    value scales to exactly the starting reference of the sums."""
+    inv = np.float32(math.log(2.0))
+    step = np.spacing(inv)
+    inv = next(v for v in (inv, inv + step, inv - step, inv + 2 * step) if v * np.float32(1.4426950408889634) == np.float32(1))
+    x = make_logits(8, 3, vocab, torch.float32).contiguous()
+    x[0, :vocab // 2] = torch.finfo(torch.float32).min  # before the live ones
+    x[1, vocab // 2:] = torch.finfo(torch.float32).min
+    x[2, 3:] = torch.finfo(torch.float32).min
+    check_logprobs(x, [vocab - 1, 0, 1], inv=torch.full((3,), float(inv), device=DEV), k=5)
+
+
 def test_logprobs_far_from_zero_keep_their_differences():
     """Logits around 20000: log probabilities come from differences, not from a large ln sum."""
     x = (make_logits(5, 4, 5000, torch.float32) + 20000.0).contiguous()
