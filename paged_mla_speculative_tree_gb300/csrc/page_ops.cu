@@ -3,6 +3,8 @@
 // from ("The Final Solder Joint" -- "The Investigation" gives their types).
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "mla_step_ops.h"
 #include "mtv_internal.cuh"
 
@@ -287,14 +289,16 @@ template <int kMode> __global__ void __launch_bounds__(kPageThreads) page_table_
 // Slot maps.  Every block scans all request lengths into shared memory (a few
 // KB out of L2), then takes its share of the prefix keys by output position
 // and every gridDim-th request's tree.  Bound by the 8 bytes stored a key:
-// 256 x (131,072 + 64) in pages of 64 takes 47.5 us (5.7 TB/s), 4 x (5,760 +
-// 16) takes 4.1 us of launch, scan and depths.
+// 256 x (131,072 + 64) in pages of 64 takes 47.5 us (5.7 TB/s, of which 4 us
+// are scan and trees; bare stores in this order take 41 to 43), 4 x (5,760 +
+// 16) takes 3.9 us of launch, scan and depths.
 // ---------------------------------------------------------------------------
-constexpr int kMapThreads = 512;
+constexpr int kMapThreads = 256;
 constexpr int kPairs = 4;        // keys a lane searches at a time
+constexpr int kUnroll = 4;       // steps with their loads in flight together
 constexpr int kMaxSteps = 32;    // of 64 keys, in a run
 constexpr int kFewRequests = 4;  // of a run that is written request by request
-constexpr int kMapBlocks = 304;  // two on each of 152 SMs
+constexpr int kMapBlocks = 608;  // four on each of 152 SMs
 constexpr uint32_t kMaxSum = 0x7fffffffu;
 
 struct MapArgs {
@@ -330,7 +334,48 @@ __device__ __forceinline__ int64_t slot_of(const MapArgs& A, int64_t row, uint32
   return int64_t(id) * A.page.d + (j - pg * A.page.d);
 }
 
-__global__ void __launch_bounds__(kMapThreads, 2) slot_map_kernel(const MapArgs A) {
+// A lane's pairs of keys in steps of 64 keys a warp, from token j on: slots of
+// tokens j + 64 i and the next one.  kInside: both always lie in one page.
+// Returns whether an entry was no page (its slots are then wrong).
+template <bool kInside>
+__device__ __forceinline__ bool write_steps(longlong2* out, const int32_t* pages, uint32_t j, int steps, FastDiv page,
+                                            uint32_t limit) {
+  const int32_t d = int32_t(page.d);
+  bool none = false;
+  auto batch = [&](auto count) {
+    constexpr int kCount = decltype(count)::value;
+    uint32_t at[kCount];
+    int32_t id[kCount], next[kCount];
+#pragma unroll
+    for (int u = 0; u < kCount; ++u) {
+      at[u] = fast_div(j + u * 64, page);
+      id[u] = __ldg(pages + at[u]);
+      // the second key may start the next page
+      if (!kInside) next[u] = j + u * 64 + 1 == (at[u] + 1) * page.d ? __ldg(pages + at[u] + 1) : -1;
+    }
+#pragma unroll
+    for (int u = 0; u < kCount; ++u) {
+      none |= uint32_t(id[u]) >= limit;
+      const int64_t x = int64_t(id[u] - int32_t(at[u])) * d + (j + u * 64);  // id d + j mod d
+      int64_t y = x + 1;
+      if (!kInside && j + u * 64 + 1 == (at[u] + 1) * page.d) {
+        none |= uint32_t(next[u]) >= limit;
+        y = int64_t(next[u]) * d;
+      }
+      out[u * 32] = make_longlong2(x, y);
+    }
+    out += kCount * 32;
+    j += kCount * 64;
+  };
+  int i = 0;
+#pragma unroll 1
+  for (; i + kUnroll <= steps; i += kUnroll) batch(std::integral_constant<int, kUnroll>());
+#pragma unroll 1
+  for (; i < steps; ++i) batch(std::integral_constant<int, 1>());
+  return none;
+}
+
+__global__ void __launch_bounds__(kMapThreads, 4) slot_map_kernel(const MapArgs A) {
   extern __shared__ uint32_t sm[];
   uint32_t* kv_off = sm;                // [bs + 1]
   uint32_t* q_off = kv_off + A.bs + 1;  // [bs + 1]
@@ -430,9 +475,9 @@ __global__ void __launch_bounds__(kMapThreads, 2) slot_map_kernel(const MapArgs 
   }
 
   // Prefix keys by output position: a warp writes runs of 64 to 2048 keys.
-  // A run inside a few requests goes request by request, two neighbouring keys
-  // a lane and step, its row and pages checked as a whole; any other one (of
-  // many short requests) searches each key's request.
+  // A run inside a few requests goes request by request, its row and pages
+  // checked as a whole, in steps of two neighbouring keys a lane (16 bytes);
+  // any other one (of many short requests) searches each key's request.
   if (A.kv_indices) {
     const int lane = tid & 31;
     const int64_t total = min(int64_t(kv_off[A.bs]), A.kv_capacity);
@@ -473,23 +518,22 @@ __global__ void __launch_bounds__(kMapThreads, 2) slot_map_kernel(const MapArgs 
         }
         const int32_t* pages = A.table + row * A.stride;
         int64_t* to = A.kv_indices + lo;
-        // a lane's pair starts on 16 bytes: the segment's first one may lack its first key
-        const int shift = int(reinterpret_cast<uintptr_t>(to) >> 3) & 1;
-        const int steps = (int(keys) + shift + 63) / 64;
-#pragma unroll 4
-        for (int i = 0; i < steps; ++i) {
-          const int k = i * 64 + lane * 2 - shift;
-          if (k < int(keys)) {
-            const uint32_t j = j0 + uint32_t(max(k, 0)), a = fast_div(j, A.page), off = j - a * A.page.d;
-            const bool turns = off + 1 == A.page.d, both = k >= 0 && k + 1 < int(keys);
-            const int32_t id = __ldg(pages + a), next = turns && both ? __ldg(pages + a + 1) : id;
-            const bool ok = uint32_t(id) < limit, next_ok = uint32_t(next) < limit;
-            if (!ok || !next_ok) bad |= MTV_DEVERR_PAGES;
-            const int64_t x = ok ? int64_t(id) * A.page.d + off : -1;
-            const int64_t y = next_ok ? int64_t(next) * A.page.d + (turns ? 0 : off + 1) : -1;
-            if (both) *reinterpret_cast<longlong2*>(to + k) = make_longlong2(x, y);
-            else to[max(k, 0)] = x;
-          }
+        const int count = int(keys), shift = int(reinterpret_cast<uintptr_t>(to) >> 3) & 1;
+        const int whole = (count - shift) / 64;  // steps of 64 keys on 16-byte boundaries
+        const uint32_t d = A.page.d;
+        auto one = [&](int k) { to[k] = slot_of(A, row, j0 + uint32_t(k), &bad); };
+        longlong2* out = reinterpret_cast<longlong2*>(to + shift) + lane;
+        const uint32_t j = j0 + uint32_t(shift) + 2 * lane;
+        bool none = false;  // an entry that is no page
+        if (d % 2 == 0 && (j0 + uint32_t(shift)) % 2 == 0)
+          none = write_steps<true>(out, pages, j, whole, A.page, limit);
+        else
+          none = write_steps<false>(out, pages, j, whole, A.page, limit);
+        if (__any_sync(0xffffffffu, none)) {
+          for (int k = lane; k < count; k += 32) one(k);
+        } else {
+          if (shift && lane == 0) one(0);
+          for (int k = shift + whole * 64 + lane; k < count; k += 32) one(k);
         }
       }
     }
