@@ -355,64 +355,72 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 # The current stream's handle without building a Stream object, where torch has it.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or \
     (lambda device: torch.cuda.current_stream(device).cuda_stream)
+_I32, _I64, _F32, _BF16 = torch.int32, torch.int64, torch.float32, torch.bfloat16
 
 
-class _Args:
-    """Device addresses of one call's tensors, which have to share a device;
-    the call is made on that device and, by default, on its current stream."""
-    __slots__ = ("device",)
+def _device_of(t, name):
+    device = t.get_device()
+    if device < 0:
+        raise TypeError(f"{name} must be a CUDA tensor")
+    return device
 
-    def __init__(self):
-        self.device = None
 
-    def _bind(self, t, name):
-        device = t.get_device()
-        if device < 0:
-            raise TypeError(f"{name} must be a CUDA tensor")
-        if self.device is not None:
-            raise ValueError(f"{name} is on another device")
-        self.device = device
+def _refuse(t, dtype, device, name):
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if _device_of(t, name) != device:
+        raise ValueError(f"{name} is on another device")
+    raise ValueError(f"{name} must be contiguous")
 
-    def strided(self, t, dtype, name, shape=None):
-        """Address of a tensor whose strides the call takes."""
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.get_device() != self.device:
-            self._bind(t, name)
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        return t.data_ptr()
 
-    def dense(self, t, dtype, name, shape=None):
-        """Address of a contiguous tensor (None stays NULL)."""
-        if t is None:
-            return None
-        if t.dtype is not dtype:
-            raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
-        if t.get_device() != self.device:
-            self._bind(t, name)
-        if not t.is_contiguous():
-            raise ValueError(f"{name} must be contiguous")
-        if shape is not None and t.shape != shape:
-            raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
-        return t.data_ptr()
+def _dense(t, dtype, device, name, count=None):
+    """Address of a contiguous tensor of ``count`` elements on ``device`` (None stays NULL)."""
+    if t is None:
+        return None
+    if t.dtype is not dtype or t.get_device() != device or not t.is_contiguous():
+        _refuse(t, dtype, device, name)
+    if count is not None and t.numel() != count:
+        raise ValueError(f"{name} must hold {count} elements, got {t.numel()}")
+    return t.data_ptr()
 
-    def call(self, fn, stream, check, *args):
-        device = self.device
-        if stream is None:
-            stream = _raw_stream(device)
-        elif isinstance(stream, torch.cuda.Stream):
-            if stream.device_index != device:
-                raise ValueError("the stream is on another device than the tensors")
-            stream = stream.cuda_stream
-        if device == torch.cuda.current_device():
+
+def _strided(t, dtype, device, name, shape):
+    """Address of a tensor of this shape whose strides the call takes."""
+    if t.dtype is not dtype or t.get_device() != device:
+        _refuse(t, dtype, device, name)
+    if t.shape != shape:
+        raise ValueError(f"{name} must be {list(shape)}, got {list(t.shape)}")
+    return t.data_ptr()
+
+
+def _table(page_table):
+    """(address, row stride, rows, entries a row, device) of a page table."""
+    shape, stride = page_table.shape, page_table.stride()
+    if len(shape) != 2 or (shape[1] > 1 and stride[1] != 1):
+        raise ValueError("page_table must be [rows, max_pages] with dense rows")
+    rows, max_pages = shape
+    device = _device_of(page_table, "page_table")
+    if page_table.dtype is not _I32:
+        _refuse(page_table, _I32, device, "page_table")
+    return page_table.data_ptr(), stride[0] if rows > 1 else max_pages, rows, max_pages, device
+
+
+def _call(fn, device, stream, check, *args):
+    """Makes the call on the tensors' device and, by default, its current stream."""
+    if stream is None:
+        stream = _raw_stream(device)
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != device:
+            raise ValueError("the stream is on another device than the tensors")
+        stream = stream.cuda_stream
+    if device == torch.cuda.current_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
             rc = fn(*args, stream)
-        else:
-            with torch.cuda.device(device):
-                rc = fn(*args, stream)
-        if check and rc != MTV_OK:
-            raise MtvError(rc, fn.__name__)
-        return rc
+    if check and rc != MTV_OK:
+        raise MtvError(rc, fn.__name__)
+    return rc
 
 
 def page_table_update(lens, page_size: int, page_table, held, free_pages, num_free, err=None, stream=None,
@@ -420,18 +428,13 @@ def page_table_update(lens, page_size: int, page_table, held, free_pages, num_fr
     """Enqueues the growing and shrinking of every row of ``page_table``
     [rows, max_pages] to ``lens`` tokens, from and to the ``free_pages`` stack
     (see the header)."""
-    a = _Args()
-    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be [rows, max_pages] with dense rows")
-    rows, max_pages = page_table.shape
     if num_free.numel() != 1:
         raise ValueError("num_free must hold one element")
-    lp = a.dense(lens, torch.int32, "lens", (rows,))
-    args = (lp, rows, page_size, a.strided(page_table, torch.int32, "page_table"),
-            page_table.stride(0) if rows > 1 else max_pages, max_pages, a.dense(held, torch.int32, "held", (rows,)),
-            a.dense(free_pages, torch.int32, "free_pages"), free_pages.numel(),
-            a.dense(num_free, torch.int32, "num_free"), a.dense(err, torch.int32, "err"))
-    return a.call(load().mla_page_table_update, stream, check, *args)
+    table, stride, rows, max_pages, device = _table(page_table)
+    return _call(load().mla_page_table_update, device, stream, check, _dense(lens, _I32, device, "lens", rows), rows,
+                 page_size, table, stride, max_pages, _dense(held, _I32, device, "held", rows),
+                 _dense(free_pages, _I32, device, "free_pages"), free_pages.numel(),
+                 _dense(num_free, _I32, device, "num_free"), _dense(err, _I32, device, "err"))
 
 
 def slot_map_build(page_table, prefix_lens, tree_sizes, page_size: int, kv_indptr, kv_indices, qo_indptr,
@@ -441,27 +444,21 @@ def slot_map_build(page_table, prefix_lens, tree_sizes, page_size: int, kv_indpt
     ``out_cache_loc`` and ``positions`` from a page table [rows, max_pages] and
     request lengths (see the header).  The outputs' element counts are their
     capacities; ``num_pages`` bounds the page table's entries."""
-    a = _Args()
-    if page_table.dim() != 2 or (page_table.shape[1] > 1 and page_table.stride(1) != 1):
-        raise ValueError("page_table must be [rows, max_pages] with dense rows")
     if num_pages is None:
         raise ValueError("num_pages is needed: the pages of the pool")
-    num_rows, max_pages = page_table.shape
     bs = prefix_lens.numel()
-    if rows is None and bs > num_rows:
+    if rows is None and bs > page_table.shape[0]:
         raise ValueError("more requests than rows of page_table")
-    q = [t for t in (out_cache_loc, positions, parents) if t is not None]
-    q_capacity = min(t.numel() for t in q) if q else 0
-    args = (a.strided(page_table, torch.int32, "page_table"), page_table.stride(0) if num_rows > 1 else max_pages,
-            num_rows, max_pages, num_pages, page_size, a.dense(rows, torch.int32, "rows", (bs,)),
-            a.dense(prefix_lens, torch.int32, "prefix_lens", (bs,)),
-            a.dense(tree_sizes, torch.int32, "tree_sizes", (bs,)), a.dense(parents, torch.int32, "parents"), bs,
-            a.dense(kv_indptr, torch.int32, "kv_indptr", (bs + 1,)), a.dense(kv_indices, torch.int64, "kv_indices"),
-            kv_indices.numel() if kv_indices is not None else 0,
-            a.dense(qo_indptr, torch.int64, "qo_indptr", (bs + 1,)),
-            a.dense(out_cache_loc, torch.int64, "out_cache_loc"), a.dense(positions, torch.int64, "positions"),
-            q_capacity, a.dense(err, torch.int32, "err"))
-    return a.call(load().mla_slot_map_build, stream, check, *args)
+    table, stride, num_rows, max_pages, device = _table(page_table)
+    q_capacity = [t.numel() for t in (out_cache_loc, positions, parents) if t is not None]
+    return _call(load().mla_slot_map_build, device, stream, check, table, stride, num_rows, max_pages, num_pages, page_size,
+                 _dense(rows, _I32, device, "rows", bs), _dense(prefix_lens, _I32, device, "prefix_lens"),
+                 _dense(tree_sizes, _I32, device, "tree_sizes", bs), _dense(parents, _I32, device, "parents"), bs,
+                 _dense(kv_indptr, _I32, device, "kv_indptr", bs + 1), _dense(kv_indices, _I64, device, "kv_indices"),
+                 kv_indices.numel() if kv_indices is not None else 0,
+                 _dense(qo_indptr, _I64, device, "qo_indptr", bs + 1),
+                 _dense(out_cache_loc, _I64, device, "out_cache_loc"), _dense(positions, _I64, device, "positions"),
+                 min(q_capacity) if q_capacity else 0, _dense(err, _I32, device, "err"))
 
 
 def rope_freqs(rope_dim: int, base: float, scaling: RopeScaling | None = None):
@@ -485,8 +482,6 @@ def rope_write(turns, positions, layout: int = ROPE_INTERLEAVED, amplitude: floa
     dimension; ``q_out`` may be ``q_in``), and the write of every token's
     latent row (``c_in`` [tokens, 512] and the rotated ``k_in`` [tokens, 64])
     into ``kv_pool`` at ``out_cache_loc``.  Either half may be left out."""
-    a = _Args()
-    tokens, rope_dim = positions.numel(), 2 * turns.numel()
     if (q_in is None) != (q_out is None):
         raise ValueError("q_in and q_out go together")
     some = q_in if q_in is not None else c_in
@@ -496,39 +491,37 @@ def rope_write(turns, positions, layout: int = ROPE_INTERLEAVED, amplitude: floa
     code = _DTYPES.get(dtype)
     if code is None:
         raise TypeError(f"{dtype} is not one of {list(_DTYPES)}")
-
-    tp = a.dense(turns, torch.int64, "turns")
-    pp = a.dense(positions, torch.int64, "positions")
-
-    q_args = (None, 0, 0, None, 0, 0, 0)
+    if num_valid is not None and num_valid.numel() != 1:
+        raise ValueError("num_valid must hold one element")
+    device = _device_of(some, "q_in" if q_in is not None else "c_in")
+    tokens, rope_dim = positions.numel(), 2 * turns.numel()
+    qi = qo = kp = cp = lp = pool = None
+    qi_tok = qi_head = qo_tok = qo_head = heads = k_tok = c_tok = slots = 0
     if q_in is not None:
         if q_in.dim() != 3:
             raise ValueError("q_in must be [tokens, heads, rope_dim]")
         heads = q_in.shape[1]
         shape = (tokens, heads, rope_dim)
-        qi, qo = q_in.stride(), q_out.stride()
-        q_args = (a.strided(q_in, dtype, "q_in", shape), qi[0], qi[1], a.strided(q_out, dtype, "q_out", shape), qo[0],
-                  qo[1], heads)
-        if qi[2] != 1 or qo[2] != 1:
+        qi, qo = _strided(q_in, dtype, device, "q_in", shape), _strided(q_out, dtype, device, "q_out", shape)
+        (qi_tok, qi_head, qi_dim), (qo_tok, qo_head, qo_dim) = q_in.stride(), q_out.stride()
+        if qi_dim != 1 or qo_dim != 1:
             raise ValueError("q_in and q_out must be dense in their last dimension")
-    kv_args = (None, 0, None, 0, None, None, 0)
     if kv_pool is not None or c_in is not None or k_in is not None or out_cache_loc is not None:
         if kv_pool is None or c_in is None or k_in is None or out_cache_loc is None:
             raise ValueError("kv_pool, c_in, k_in and out_cache_loc go together")
         slots = kv_pool.shape[0]
         if slots == 0:
             raise ValueError("kv_pool is empty")
-        kp, cp = a.strided(k_in, dtype, "k_in", (tokens, 64)), a.strided(c_in, dtype, "c_in", (tokens, 512))
-        ks, cs = k_in.stride(), c_in.stride()
-        if ks[1] != 1 or cs[1] != 1:
+        kp, cp = _strided(k_in, dtype, device, "k_in", (tokens, 64)), _strided(c_in, dtype, device, "c_in", (tokens, 512))
+        (k_tok, k_dim), (c_tok, c_dim) = k_in.stride(), c_in.stride()
+        if k_dim != 1 or c_dim != 1:
             raise ValueError("k_in and c_in must be dense in their last dimension")
-        kv_args = (kp, ks[0], cp, cs[0], a.dense(out_cache_loc, torch.int64, "out_cache_loc", (tokens,)),
-                   a.dense(kv_pool, torch.bfloat16, "kv_pool", (slots, 576)), slots)
-    if num_valid is not None and num_valid.numel() != 1:
-        raise ValueError("num_valid must hold one element")
-    return a.call(load().mla_rope_write, stream, check, tp, rope_dim, amplitude, layout, int(inverse),
-                  pp, tokens, a.dense(num_valid, torch.int64, "num_valid"), code, *q_args, *kv_args,
-                  a.dense(err, torch.int32, "err"))
+        lp = _dense(out_cache_loc, _I64, device, "out_cache_loc", tokens)
+        pool = _dense(kv_pool, _BF16, device, "kv_pool", 576 * slots)
+    return _call(load().mla_rope_write, device, stream, check, _dense(turns, _I64, device, "turns"), rope_dim, amplitude,
+                 layout, 1 if inverse else 0, _dense(positions, _I64, device, "positions"), tokens,
+                 _dense(num_valid, _I64, device, "num_valid"), code, qi, qi_tok, qi_head, qo, qo_tok, qo_head, heads,
+                 kp, k_tok, cp, c_tok, lp, pool, slots, _dense(err, _I32, device, "err"))
 
 
 def token_logprobs(logits, stats, tokens=None, logprobs=None, top_tokens=None, top_logprobs=None, token_rows=None,
@@ -537,24 +530,24 @@ def token_logprobs(logits, stats, tokens=None, logprobs=None, top_tokens=None, t
     token i under row i), the rows' ``stats`` [3, rows] (scaled maximum, ln of
     the sum relative to it, entropy) and their top alternatives [k, rows], from
     ``logits`` [rows, vocab] with dense rows (see the header)."""
-    a = _Args()
     code = _DTYPES.get(logits.dtype)
     if code is None:
         raise TypeError(f"logits must be one of {list(_DTYPES)}, got {logits.dtype}")
-    if logits.dim() != 2 or (logits.shape[1] > 1 and logits.stride(1) != 1):
+    if logits.dim() != 2:
         raise ValueError("logits must be [rows, vocab] with dense rows")
-    rows, vocab = logits.shape
+    (rows, vocab), (row_stride, entry) = logits.shape, logits.stride()
+    if vocab > 1 and entry != 1:
+        raise ValueError("logits must be [rows, vocab] with dense rows")
     if (tokens is None) != (logprobs is None) or (top_tokens is None) != (top_logprobs is None):
         raise ValueError("tokens and logprobs go together, and so do top_tokens and top_logprobs")
+    device = _device_of(logits, "logits")
     n = tokens.numel() if tokens is not None else 0
     k = top_tokens.shape[0] if top_tokens is not None else 0
-    args = (a.strided(logits, logits.dtype, "logits"), code, rows, vocab, logits.stride(0),
-            a.dense(inv_temperature, torch.float32, "inv_temperature", (rows,)),
-            a.dense(tokens, torch.int32, "tokens", (n,)), a.dense(token_rows, torch.int32, "token_rows", (n,)), n,
-            a.dense(logprobs, torch.float32, "logprobs", (n,)), a.dense(stats, torch.float32, "stats", (3, rows)), k,
-            a.dense(top_tokens, torch.int32, "top_tokens", (k, rows)),
-            a.dense(top_logprobs, torch.float32, "top_logprobs", (k, rows)), a.dense(err, torch.int32, "err"))
-    return a.call(load().mla_token_logprobs, stream, check, *args)
+    return _call(load().mla_token_logprobs, device, stream, check, logits.data_ptr(), code, rows, vocab, row_stride,
+                 _dense(inv_temperature, _F32, device, "inv_temperature", rows), _dense(tokens, _I32, device, "tokens"),
+                 _dense(token_rows, _I32, device, "token_rows", n), n, _dense(logprobs, _F32, device, "logprobs", n),
+                 _dense(stats, _F32, device, "stats", 3 * rows), k, _dense(top_tokens, _I32, device, "top_tokens", k * rows),
+                 _dense(top_logprobs, _F32, device, "top_logprobs", k * rows), _dense(err, _I32, device, "err"))
 
 
 class MlaTreeVerify:
