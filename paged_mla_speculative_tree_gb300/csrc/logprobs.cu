@@ -637,12 +637,21 @@ __global__ void __launch_bounds__(kLpThreads) logprob_tokens_kernel(const Logpro
   A.logprobs[i] = lp;
 }
 
-// Blocks a row: enough to give every SM work, as long as each keeps a few
-// groups a thread, and so many that a block's groups fit its shared memory.
+// Blocks a row: doubled while a block's groups do not fit its shared memory,
+// and while there are SMs for more blocks and each keeps enough of the row to
+// pay for the cluster and one more top k.  Measured (us; blocks 1, 2, 4, 8):
+//   8 x 32,000 bf16      5.6   6.0   5.9   6.3      64 x 131,072 bf16   16.0  11.8  10.0  11.5
+//   8 x 131,072 bf16    12.6   9.9   8.1   7.8     152 x 131,072 bf16   18.5  14.7  19.1  24.1
+//   1 x 64,000 bf16      7.9   7.3   6.7   7.1     304 x 131,072 bf16   21.4  19.9  29.1  39.8
+//   8 x 131,072 fp32    17.2  12.5   9.2   8.6     304 x 32,000 bf16     9.1  11.5  19.0  32.0
 int blocks_per_row(int64_t rows, int vocab, int size) {
   const int groups = vocab / (64 / size);
   int b = 1;
-  while (b < kMaxCluster && (groups > b * kMaxGroups || (rows * b * 2 <= 304 && groups >= b * 2 * 64))) b *= 2;
+  for (; b < kMaxCluster; b *= 2) {
+    const int share = vocab * size / (2 * b);  // bytes a block with twice as many
+    const int64_t most = share >= 128 * 1024 ? 608 : share >= 48 * 1024 ? 304 : share >= 32000 && b > 1 ? 152 : 0;
+    if (groups <= b * kMaxGroups && rows * b * 2 > most) break;
+  }
   return b;
 }
 
