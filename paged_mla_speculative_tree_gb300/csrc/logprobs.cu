@@ -71,7 +71,7 @@ __device__ __forceinline__ bool usable_temperature(float s) { return s > 0.f && 
 // blocks: 225 and 208 us, 1,024 rows 59 and 57 in place of 53); then issue
 // slots, about 6 instructions a logit with the fp32 work in pairs (f32x2) and
 // one MUFU exponential each.  The top k adds 2 us to a wave of blocks and
-// 2.4 us to the latency of few rows (8 x 32,000: 6.1 us).
+// 1.7 us to the latency of few rows (8 x 32,000: 5.6 us).
 // ---------------------------------------------------------------------------
 constexpr int kMaxGroups = 8192;      // groups a block: their maxima fill 16 or 32 KB
 constexpr int kListed = 256;          // groups that may reach the bound before they are searched by rank
@@ -154,11 +154,6 @@ __device__ __forceinline__ float2 unpack2(uint64_t v) {
 __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
   uint64_t r;
   asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
-  return r;
-}
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-  uint64_t r;
-  asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
   return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
