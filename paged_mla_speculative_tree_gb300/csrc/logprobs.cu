@@ -78,6 +78,8 @@ constexpr int kListed = 256;          // groups that may reach the bound before 
 constexpr int kPicked = MTV_MAX_TOP;  // groups read again at most
 constexpr int kMaxGroup = 32;         // logits a group at most
 constexpr int kEdge = 64;             // logits before and after the aligned groups, under 32 each
+constexpr int kCand = kPicked * kMaxGroup + kEdge;  // logits found at most
+constexpr int kFewCand = 128;         // 4 MTV_MAX_TOP: found from 64 buckets of 4 threads with one logit each
 constexpr int kBuckets = 64;
 constexpr int kBucketThreads = kLpThreads / kBuckets;
 constexpr int kMaxCluster = 8;
@@ -180,7 +182,7 @@ constexpr float kRefSlack = 29.f;
 constexpr float kLowest = -3.402823466e38f;
 
 struct LpShared {
-  uint64_t cand[kPicked * kMaxGroup + kEdge];
+  uint64_t cand[kCand];
   uint64_t bucket[kBuckets];
   uint64_t round[2][kLpWarps];
   uint16_t listed[kListed], picked[kPicked];
@@ -348,19 +350,31 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
   // The block's maximum and the buckets' largest group keys.  A bucket is a few
   // neighbouring threads: the k-th largest of 64 buckets' keys is reached by k
   // groups at least, and by 1.4 k on average at k = 32.
-  float m = fmaxf(tmax, edge);
-#pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-  if (lane == 0) sh.wm[w] = m;
-  if (A.top_k > 0) {
-    // threads without a group above -inf rank last, each apart from the others
-    uint64_t key = tmax > -INFINITY ? group_key(tmax, tgroup) : group_key(-INFINITY, kMaxGroups + tid);
+  auto fill_bucket = [&](uint64_t key) {  // the largest of a bucket's threads' keys
 #pragma unroll
     for (int o = 1; o < kBucketThreads; o <<= 1) {
       const uint64_t other = __shfl_xor_sync(0xffffffffu, key, o);
       key = other > key ? other : key;
     }
     if (tid % kBucketThreads == 0) sh.bucket[tid / kBucketThreads] = key;
+  };
+  auto find_bound = [&]() {  // the k-th largest bucket: a bucket's threads count its rank
+    const uint64_t mine = sh.bucket[tid / kBucketThreads];
+    int above = 0;
+#pragma unroll
+    for (int j = 0; j < kBuckets; j += kBucketThreads) above += sh.bucket[j + tid % kBucketThreads] > mine;
+#pragma unroll
+    for (int o = 1; o < kBucketThreads; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
+    if (above == A.top_k - 1 && tid % kBucketThreads == 0) sh.bound = mine;
+  };
+  float m = fmaxf(tmax, edge);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  if (lane == 0) sh.wm[w] = m;
+  if (A.top_k > 0) {
+    // threads without a group above -inf rank last, each apart from the others
+    const uint64_t key = tmax > -INFINITY ? group_key(tmax, tgroup) : group_key(-INFINITY, kMaxGroups + tid);
+    fill_bucket(key);
     if (tid == 0) sh.num_listed = sh.num_cand = 0;
   }
   bad = __syncthreads_or(bad);
@@ -395,15 +409,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
     sh.ws[w] = total.s;
     sh.wu[w] = total.u;
   }
-  if (A.top_k > 0) {  // a bucket's threads count its rank
-    const uint64_t mine = sh.bucket[tid / kBucketThreads];
-    int above = 0;
-#pragma unroll
-    for (int j = 0; j < kBuckets; j += kBucketThreads) above += sh.bucket[j + tid % kBucketThreads] > mine;
-#pragma unroll
-    for (int o = 1; o < kBucketThreads; o <<= 1) above += __shfl_xor_sync(0xffffffffu, above, o);
-    if (above == A.top_k - 1 && tid % kBucketThreads == 0) sh.bound = mine;
-  }
+  if (A.top_k > 0) find_bound();
   __syncthreads();
   total.s = total.u = 0.f;
 #pragma unroll
@@ -543,6 +549,29 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
     }
     __syncthreads();
     found = sh.num_cand;
+    // Many logits of few groups (a small vocabulary, a mask that leaves little):
+    // the bound once more, over the logits.  k buckets of 4 threads with c logits
+    // each leave 128 c of over 256 (c - 1) at most, so this ends.
+    while (found > kFewCand) {
+      uint64_t mine[(kCand + kLpThreads - 1) / kLpThreads], best = 0;
+#pragma unroll
+      for (int q = 0; q < (kCand + kLpThreads - 1) / kLpThreads; ++q) {
+        const int i = tid + q * kLpThreads;
+        mine[q] = i < found ? sh.cand[i] : 0;
+        best = mine[q] > best ? mine[q] : best;
+      }
+      fill_bucket(best);
+      __syncthreads();
+      find_bound();
+      if (tid == 0) sh.num_cand = 0;
+      __syncthreads();
+      const uint64_t at_least = sh.bound;
+#pragma unroll
+      for (int q = 0; q < (kCand + kLpThreads - 1) / kLpThreads; ++q)
+        if (mine[q] != 0 && mine[q] >= at_least) sh.cand[atomicAdd(&sh.num_cand, 1)] = mine[q];
+      __syncthreads();
+      found = sh.num_cand;
+    }
   }
   if (A.top_k > 0) {
     for (int i0 = 0; i0 < found; i0 += kLpThreads / 4) {  // four threads count a logit's rank
