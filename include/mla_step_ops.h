@@ -200,7 +200,8 @@ int mla_rope_freqs(int rope_dim, double base, const mtv_rope_scaling_t* scaling,
  * positions      device, int64 [num_tokens].
  * num_tokens     host: rows of the buffers.
  * num_valid      device, int64 [1], or NULL: only tokens below it are done
- *                (a padded batch: pass qo_indptr + bs).
+ *                (a padded batch: pass qo_indptr + bs).  The others' inputs may
+ *                be read, but nothing of theirs is written.
  * dtype          MTV_DTYPE_* of q_in, q_out, k_in and c_in.
  * q_in, q_out    device, or both NULL to leave the queries out; element d < rope_dim of head h
  *                of token t at t * tok_stride + h * head_stride + d (strides in
