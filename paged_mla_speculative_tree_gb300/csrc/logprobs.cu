@@ -233,6 +233,9 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
   Sums acc{0.f, 0.f};
   float ref = kLowest;
   const float c2 = scale * kLog2e;
+  // a difference of logits in powers of two; scale * log2(e) passes fp32's range
+  // before scale does, and a difference of 0 has to stay 0
+  auto powers = [&](float d) { return c2 < INFINITY ? d * c2 : d * scale * kLog2e; };
   float tmax = -INFINITY, tnext = -INFINITY;  // largest and second largest group maximum
   float worst = -INFINITY;  // NaN or +inf once a logit was
   int tgroup = 0xffff;
@@ -387,14 +390,14 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
       total = acc.moved(fmaf(-c2, m, ref));
     } else {
       // so far from 0 that a reference's rounding (2^-24 of it) is no longer a
-      // small t: once more, from differences to the maximum
+      // small t, or c2 is no number: once more, from differences to the maximum
       for (int i = tid; i < n * kGroup; i += kLpThreads) {
-        const float t = (to_float(body[i]) - m) * c2, e = exp2_approx(t);
+        const float t = powers(to_float(body[i]) - m), e = exp2_approx(t);
         total.s += e;
         total.u += e > 0.f ? e * t : 0.f;
       }
       if (edge_id >= 0) {
-        const float t = (edge - m) * c2, e = exp2_approx(t);
+        const float t = powers(edge - m), e = exp2_approx(t);
         total.s += e;
         total.u += e > 0.f ? e * t : 0.f;
       }
@@ -603,7 +606,7 @@ __global__ void __launch_bounds__(kLpThreads, 4) logprob_rows_kernel(const Logpr
   }
   total = Sums{0.f, 0.f};
   for (int i = 0; i < blocks && m > -INFINITY; ++i) {
-    const Sums p = Sums{sh.part_s[i], sh.part_u[i]}.moved((sh.part_m[i] - m) * c2);
+    const Sums p = Sums{sh.part_s[i], sh.part_u[i]}.moved(powers(sh.part_m[i] - m));
     total.s += p.s;
     total.u += p.u;
   }

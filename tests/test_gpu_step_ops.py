@@ -622,6 +622,39 @@ def test_logprobs_far_from_zero_keep_their_differences():
     check_logprobs(-x - 30000.0, [0, 1, 2, 3], inv=torch.tensor([0.7, 1.0, 1.9, 3.0], device=DEV), k=8)
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("vocab", [9, 3001, 150001])
+@pytest.mark.parametrize("inv", [2.3e38, 2.4e38, 3.4028234663852886e38])
+def test_logprobs_at_the_largest_temperatures(dtype, vocab, inv):
+    """inv_temperature * log2(e) passes fp32's range from 2.3587e38 on, while z
+    keeps inside it.  The largest logits are powers of two, so that z's maximum
+    is exact; one row in one block, in several (150001), or in its edges (9)."""
+    dt, low = TYPES[dtype], -math.inf
+    rows = []
+
+    def row(fill):
+        rows.append(torch.full((vocab,), fill, dtype=dt))
+        return rows[-1]
+
+    row(-2.0 ** -7)[vocab // 2] = 0.0         # all mass on one token
+    row(0.0)                                  # uniform, in every block
+    r = row(-0.5)
+    r[0], r[vocab - 1] = -2.0 ** -7, -2.0 ** -7  # two equal ones below 0, in two blocks
+    row(low)[vocab - 1] = 0.0
+    r = row(-1.0)
+    r[1], r[vocab // 3], r[vocab - 2] = 0.0, -2.0 ** -126, -2.0 ** -127  # z of 0, -2.8 and -1.4 (fp16: three of 0)
+    row(low)
+    x = torch.stack(rows).to(DEV)
+    scale = torch.full((len(rows),), inv, device=DEV)
+    check_logprobs(x, [vocab // 2] * len(rows), inv=scale, k=3)
+    check_logprobs(x, [0, 1, 0, vocab - 1, vocab - 2, 0, -1], [0, 1, 2, 3, 4, 5, 0], scale, 20)
+    y = torch.full((1, vocab), -0.5, dtype=dt, device=DEV)
+    y[0, vocab // 3] = -0.01                  # z's maximum rounds: its rest is in ln S, and goes out again
+    got, word = run_logprobs(y, [vocab // 3], inv=scale[:1], k=1)
+    assert word == 0 and got["top_tokens"].tolist() == [[vocab // 3]] and got["logprobs"].tolist() == [0.0]
+    assert got["top_logprobs"].tolist() == [[0.0]] and got["stats"][2].tolist() == [0.0] and np.isfinite(got["stats"]).all()
+
+
 def test_logprobs_bad_tokens_and_rows():
     x = make_logits(6, 3, 100, torch.bfloat16)
     check_logprobs(x, [100, -2, 5, -1, 7, 7], [0, 1, 3, 2, -1, 2], err=binding.DEVERR_TOKEN)
