@@ -535,6 +535,7 @@ __global__ void __launch_bounds__(kMapThreads, 4) slot_map_kernel(const MapArgs 
         else
           none = write_steps<false>(out, pages, j, whole, A.page, limit);
         if (__any_sync(0xffffffffu, none)) {
+          __syncwarp();  // other lanes have stored to these addresses: a vote orders no memory
           for (int k = lane; k < count; k += 32) one(k);
         } else {
           if (shift && lane == 0) one(0);

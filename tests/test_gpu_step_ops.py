@@ -335,6 +335,47 @@ def test_slot_maps_flag_bad_input():
     assert err == binding.DEVERR_PARENT and got["positions"][:4].tolist() == [2, 2, 3, 2]
 
 
+@pytest.mark.parametrize("page", [1, 2, 7, 64])
+@pytest.mark.parametrize("where", ["first", "middle", "last"])
+@pytest.mark.parametrize("odd", [0, 1])
+def test_slots_of_a_bad_entry_in_a_long_run(page, where, odd):
+    """Runs of up to 32 steps of 64 keys: one entry that is no page (negative, or
+    past the pool) gives -1 for its own tokens, and its neighbours keep theirs."""
+    prefix, num_pages = [5000, 3, 40000, 1111], 1 << 20
+    per = -(-max(prefix) // page)
+    table = np.random.default_rng(page).integers(0, num_pages, (4, per))
+    flagged = table.copy()
+    for r, p in enumerate(prefix):
+        last = (p - 1) // page
+        at = {"first": 0, "middle": last // 2, "last": last}[where]
+        table[r, at], flagged[r, at] = (-1 - r if r % 2 else num_pages + r), -1
+    j = [np.arange(p) for p in prefix]
+    want = np.concatenate([np.where(flagged[r, x // page] < 0, -1, flagged[r, x // page] * page + x % page) for r, x in enumerate(j)])
+    out = torch.full((sum(prefix) + 4,), -4, dtype=torch.int64, device=DEV)
+    kvp, qop, err = i32([0] * 5), i64([0] * 5), err_word()
+    for _ in range(3):
+        out.fill_(-4)
+        pkg.slot_map_build(i32(table.tolist()), i32(prefix), None, page, kvp, out[odd:odd + sum(prefix)], qop, None,
+                           num_pages=num_pages, err=err)
+        got = out.cpu().numpy()
+        np.testing.assert_array_equal(got[odd:odd + sum(prefix)], want)
+        assert (got[:odd] == -4).all() and (got[odd + sum(prefix):] == -4).all() and int(err) == binding.DEVERR_PAGES
+
+
+@pytest.mark.parametrize("page", [1, 3, 16])
+def test_slots_of_a_prefix_past_its_row(page):
+    """A prefix of several thousand tokens, its table row three pages short."""
+    prefix = [2500, 4000, 4001]
+    per = -(-4000 // page) - 3
+    table = np.random.default_rng(page).permutation(3 * per).reshape(3, per)
+    slot = lambda r, j: int(table[r, j // page]) * page + j % page if j < per * page else -1  # noqa: E731
+    out = torch.full((sum(prefix),), -4, dtype=torch.int64, device=DEV)
+    kvp, qop, err = i32([0] * 4), i64([0] * 4), err_word()
+    pkg.slot_map_build(i32(table.tolist()), i32(prefix), None, page, kvp, out, qop, None, num_pages=3 * per, err=err)
+    assert out.tolist() == [slot(r, j) for r, p in enumerate(prefix) for j in range(p)]
+    assert int(err) == binding.DEVERR_PAGES
+
+
 def test_slot_maps_past_a_capacity():
     table, rows, prefix, tree, parents = slot_case(12, 5, 200, 30, 16)
     want = S.slot_map(table, 16, rows, prefix, tree, parents)
