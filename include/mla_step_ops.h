@@ -13,9 +13,14 @@
  * CUDA device pointer; buffers are caller-owned; nothing allocates or
  * synchronises, so every call may be captured in a CUDA graph; no call keeps
  * state of its own, so calls on different buffers may overlap on different
- * streams; the return value is MTV_OK (0) or a negative MTV_E* code (nothing
- * is launched then).  `err` (device, may be NULL) is a sticky 32-bit word the
- * kernels OR MTV_DEVERR_* bits into; data-dependent problems never trap.
+ * streams and come from different host threads; the return value is MTV_OK (0)
+ * or a negative MTV_E* code.  Nothing is launched then, with one exception:
+ * MTV_E_CUDA of a call that takes two kernels, when the first was launched and
+ * the second refused.  mla_page_table_update of more than 16,384 entries has
+ * then moved pages without writing held and num_free, so that its buffers no
+ * longer describe each other; mla_token_logprobs with token_rows has written
+ * everything but logprobs.  `err` (device, may be NULL) is a sticky 32-bit word
+ * the kernels OR MTV_DEVERR_* bits into; data-dependent problems never trap.
  */
 #ifndef MLA_STEP_OPS_H_
 #define MLA_STEP_OPS_H_

@@ -547,11 +547,16 @@ __global__ void __launch_bounds__(kMapThreads, 4) slot_map_kernel(const MapArgs 
   if (bad) set_err(A.err, bad);
 }
 
-// Dynamic shared memory above 48 KB has to be allowed for a kernel first.
+// Dynamic shared memory above 48 KB has to be allowed for a kernel first.  The
+// limit belongs to the process and not to the call, so it is the one that the
+// largest call needs: a call's own bytes would lower it for another host
+// thread's call, or for a graph that is still to be instantiated.
+constexpr size_t step_smem(size_t requests) { return (3 * requests + 2) * 4; }
+
 template <typename K>
 cudaError_t allow_smem(K kernel, size_t bytes) {
   if (bytes <= 40 * 1024) return cudaSuccess;  // static arrays come on top
-  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(bytes));
+  return cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(step_smem(MTV_MAX_REQUESTS)));
 }
 
 int launch_code(cudaError_t e) {
@@ -577,7 +582,7 @@ extern "C" int mla_page_table_update(const int32_t* lens, int num_rows, int page
     return MTV_E_NULL_POINTER;
   const PageArgs A{lens,  page_table,   held,          free_pages, num_free,  err,
                    table_stride, free_capacity, num_rows,   page_size, int32_t(max_pages)};
-  const size_t smem = (3 * size_t(num_rows) + 2) * 4;
+  const size_t smem = step_smem(size_t(num_rows));
   const int64_t entries = int64_t(num_rows) * max_pages;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   if (entries <= kBlockEntries) {
@@ -622,7 +627,7 @@ extern "C" int mla_slot_map_build(const int32_t* page_table, int64_t table_strid
   const MapArgs A{page_table, rows,         prefix_lens, tree_sizes, parents,   kv_indptr, kv_indices,
                   qo_indptr,  out_cache_loc, positions,   err,        table_stride, num_rows,  max_pages,
                   num_pages,  kv_capacity,   q_capacity,  make_fast_div(uint32_t(page_size)), bs};
-  const size_t smem = (3 * size_t(bs) + 2) * 4;
+  const size_t smem = step_smem(size_t(bs));
   cudaError_t e = allow_smem(slot_map_kernel, smem);
   if (e != cudaSuccess) return launch_code(e);
   int64_t blocks = kv_indices ? (kv_capacity + 64 * (kMapThreads / 32) - 1) / (64 * (kMapThreads / 32)) : 0;

@@ -791,6 +791,72 @@ def test_a_call_runs_on_its_tensors_device(monkeypatch):
         pkg.rope_write(i64([1]), i64([0]), q_in=x.view(2, 1, 300)[:1, :, :2], q_out=x.view(2, 1, 300)[:1, :, :2], num_valid=i64([1, 1]))
 
 
+def test_calls_of_several_host_threads():
+    """Calls of 8192 and of 4000 requests from four threads that share nothing:
+    what one call asks of the device (its shared memory) bounds no other's."""
+    import threading
+    lib, work = binding.load(), []
+    for k, (rows, per) in enumerate([(8192, 3), (4000, 5)] * 2):
+        rng, table, held, free = page_state(70 + k, rows, per, 4)
+        p = Pages(table, held, free)
+        prefix = [int(x) for x in rng.integers(0, 4 * per - 1, rows)]
+        full = rng.permutation(rows * per).reshape(rows, per).tolist()
+        keep = [i32([h * 4 + 4 for h in held]), i32([h * 4 for h in held]), i32(full), i32(prefix), i32([1] * rows)]
+        out = [i32([0] * (rows + 1)), i64([0] * sum(prefix)), i64([0] * (rows + 1)), i64([0] * rows), i64([0] * rows)]
+        stream, at = torch.cuda.Stream(), lambda t: t.data_ptr()
+        update = lambda lens: (lib.mla_page_table_update, (  # noqa: E731
+            at(lens), rows, 4, at(p.table), per, per, at(p.held), at(p.free), p.free.numel(), at(p.num), at(p.err),
+            stream.cuda_stream))
+        build = (lib.mla_slot_map_build, (
+            at(keep[2]), per, rows, per, rows * per, 4, None, at(keep[3]), at(keep[4]), None, rows, at(out[0]), at(out[1]),
+            out[1].numel(), at(out[2]), at(out[3]), at(out[4]), rows, at(p.err), stream.cuda_stream))
+        work.append(dict(p=p, held=held, free=free, keep=keep, out=out, stream=stream, codes=set(),
+                         calls=[update(keep[0]), update(keep[1]), build],
+                         want=S.slot_map(full, 4, range(rows), prefix, [1] * rows, None)))
+    torch.cuda.synchronize()
+    start = threading.Barrier(len(work))
+
+    def run(w):
+        torch.cuda.set_device(0)
+        start.wait()
+        for _ in range(1000):
+            for fn, args in w["calls"]:
+                w["codes"].add(fn(*args))
+
+    threads = [threading.Thread(target=run, args=(w,)) for w in work]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    for w in work:
+        assert w["codes"] == {0}
+        for got, want in zip(w["out"], w["want"]):
+            np.testing.assert_array_equal(got.cpu().numpy(), want)
+        p, held, free = w["p"], w["held"], w["free"]
+        assert p.held.tolist() == held and p.free[:len(free)].tolist() == free and int(p.err) == 0
+
+
+def test_large_and_medium_calls_in_one_graph():
+    """8192 rows, then 4000: the graph is instantiated after both."""
+    sets = []
+    for k, (rows, per) in enumerate([(8192, 3), (4000, 5)]):
+        _, table, held, free = page_state(90 + k, rows, per, 4)
+        sets.append((Pages(table, held, free), i32([4 * per] * rows), (table, held, free), [4 * per] * rows))
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=s):
+            for p, lens, _, _ in sets:
+                pkg.page_table_update(lens, 4, p.table, p.held, p.free, p.num, p.err)
+    graph.replay()
+    for p, _, state, lens in sets:
+        t2, h2, f2, flagged = S.page_table_update(lens, 4, *state)
+        assert not flagged
+        p.expect(t2, h2, f2)
+
+
 # ------------------------------------------------------------- the whole step
 
 def test_a_serving_step_end_to_end():
