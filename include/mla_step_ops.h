@@ -125,7 +125,8 @@ int mla_page_table_update(const int32_t* lens, int num_rows, int page_size, int3
  * out_cache_loc  device, int64 [q_capacity] output, or NULL to leave it out.
  * positions      device, int64 [q_capacity] output, or NULL to leave it out.
  * err            device uint32 or NULL.  MTV_DEVERR_INDPTR: a negative length
- *                (taken as 0), sums past 2^31 - 1 (held there) or past a
+ *                (taken as 0), sums past 2^31 - 1 (the offsets are held there;
+ *                slots and positions go by the request's own length) or past a
  *                capacity (the offsets are published, nothing is written past
  *                the capacity: mla_tree_verify_run skips such a request).
  *                MTV_DEVERR_PAGES: a token past its row's max_pages, a row

@@ -429,7 +429,9 @@ __global__ void __launch_bounds__(kMapThreads, 4) slot_map_kernel(const MapArgs 
     for (int r = gridDim.x - 1 - blockIdx.x; r < A.bs; r += gridDim.x) {
       const int64_t q0 = q_off[r];
       const int64_t n = min(int64_t(q_off[r + 1]), A.q_capacity) - q0;
-      const uint32_t p = kv_off[r + 1] - kv_off[r];
+      // (sums that are held have lost the prefix's length, and with a shorter one
+      // the tree's slots would be those of cached tokens)
+      const uint32_t p = kv_carry > kMaxSum ? uint32_t(max(A.prefix[r], 0)) : kv_off[r + 1] - kv_off[r];
       const int64_t row = row_of[r];
       for (int64_t t0 = 0; t0 < n; t0 += kMapThreads) {
         const int64_t t = t0 + tid;

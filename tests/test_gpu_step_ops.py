@@ -388,6 +388,25 @@ def test_slot_maps_past_a_capacity():
     assert err & binding.DEVERR_INDPTR and got["kv_indptr"].tolist() == [0] + [2 ** 31 - 1] * 3
 
 
+@pytest.mark.parametrize("prefix", [[2 ** 31 - 1, 5, 2 ** 30, 20], [2 ** 30, 2 ** 30 + 100, 9, 33], [3, 2 ** 31 - 1, 0, 17]])
+@pytest.mark.parametrize("with_keys", [True, False])
+def test_slots_of_trees_behind_sums_past_32_bits(prefix, with_keys):
+    """kv_indptr is held at 2^31 - 1; every tree keeps its own prefix length: its
+    slots lie behind its prefix (or are none), never on a prefix's tokens."""
+    page, tree, parents = 16, [2, 3, 1, 4], [[-1, 0], [-1, 0, 0], [-1], [-1, 0, 1, 0]]
+    table = np.random.default_rng(3).permutation(4 * 3).reshape(4, 3)
+    depth = [[0, 1], [0, 1, 1], [0], [0, 1, 2, 1]]
+    kvp, qop, loc, pos, err = i32([0] * 5), i64([0] * 5), i64([-4] * 12), i64([-4] * 12), err_word()
+    kvi = torch.full((8,), -4, dtype=torch.int64, device=DEV) if with_keys else None
+    pkg.slot_map_build(i32(table.tolist()), i32(prefix), i32(tree), page, kvp, kvi, qop, loc, pos,
+                       parents=i32([x for p in parents for x in p] + [-1, -1]), num_pages=12, err=err)
+    slot = lambda r, j: int(table[r][j // page]) * page + j % page if j < 3 * page else -1  # noqa: E731
+    assert loc.tolist() == [slot(r, p + t) for r, p in enumerate(prefix) for t in range(tree[r])] + [-4, -4]
+    assert pos.tolist() == [p + d for r, p in enumerate(prefix) for d in depth[r]] + [-4, -4]
+    assert kvp.tolist() == [0] + [min(int(n), 2 ** 31 - 1) for n in np.cumsum(prefix)]
+    assert qop.tolist() == [0, 2, 5, 6, 10] and int(err) == binding.DEVERR_INDPTR | binding.DEVERR_PAGES
+
+
 def test_slots_past_32_bits_in_bytes_and_far_pages():
     table = [[2 ** 31 - 1, 0, 2 ** 30]]
     got, err = build_slots(table, 1000, [2500], [3], [0], [[-1, 0, 1]], num_pages=2 ** 31)
