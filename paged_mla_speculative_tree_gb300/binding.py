@@ -540,9 +540,14 @@ def token_logprobs(logits, stats, tokens=None, logprobs=None, top_tokens=None, t
         raise ValueError("logits must be [rows, vocab] with dense rows")
     if (tokens is None) != (logprobs is None) or (top_tokens is None) != (top_logprobs is None):
         raise ValueError("tokens and logprobs go together, and so do top_tokens and top_logprobs")
-    device = _device_of(logits, "logits")
     n = tokens.numel() if tokens is not None else 0
     k = top_tokens.shape[0] if top_tokens is not None else 0
+    # as many elements in another order ([rows, 3], [rows, k]) would be filled wrongly; flat ones are fine
+    if stats.dim() > 1 and stats.shape[0] != 3:
+        raise ValueError(f"stats must be [3, rows], got {list(stats.shape)}")
+    if k and top_logprobs.dim() > 1 and top_logprobs.shape[0] != k:
+        raise ValueError(f"top_logprobs must be [{k}, rows] as top_tokens, got {list(top_logprobs.shape)}")
+    device = _device_of(logits, "logits")
     return _call(load().mla_token_logprobs, device, stream, check, logits.data_ptr(), code, rows, vocab, row_stride,
                  _dense(inv_temperature, _F32, device, "inv_temperature", rows), _dense(tokens, _I32, device, "tokens"),
                  _dense(token_rows, _I32, device, "token_rows", n), n, _dense(logprobs, _F32, device, "logprobs", n),

@@ -220,3 +220,15 @@ def test_binding_refuses_host_tensors_types_and_shapes():
         pkg.token_logprobs(f32(2, 9), f32(3, 2), tokens=i32(2))
     with pytest.raises(TypeError, match="CUDA"):
         pkg.token_logprobs(f32(2, 9), f32(3, 2))
+
+
+def test_binding_refuses_log_probability_outputs_in_another_order():
+    logits, f32 = torch.zeros((5, 9)), lambda *s: torch.zeros(s)  # noqa: E731
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)  # noqa: E731
+    with pytest.raises(ValueError, match=r"stats must be \[3, rows\]"):
+        pkg.token_logprobs(logits, f32(5, 3))
+    with pytest.raises(ValueError, match=r"top_logprobs must be \[2, rows\]"):
+        pkg.token_logprobs(logits, f32(3, 5), top_tokens=i32(2, 5), top_logprobs=f32(5, 2))
+    for stats, top in [(f32(3, 5), f32(2, 5)), (f32(15), f32(10))]:  # up to the device, which is the host here
+        with pytest.raises(TypeError, match="CUDA"):
+            pkg.token_logprobs(logits, stats, top_tokens=i32(2, 5), top_logprobs=top)
