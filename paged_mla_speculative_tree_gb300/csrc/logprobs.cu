@@ -697,11 +697,9 @@ cudaError_t launch_logprobs(const LogprobArgs& A, cudaStream_t st) {
     attr[0].val.clusterDim = {unsigned(blocks), 1, 1};
     cfg.attrs = attr;
     cfg.numAttrs = blocks > 1 ? 1 : 0;
-    if (sizeof(LpShared) + cfg.dynamicSmemBytes > 48 * 1024) {
-      const cudaError_t e = cudaFuncSetAttribute(logprob_rows_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 int(cfg.dynamicSmemBytes));
-      if (e != cudaSuccess) return e;
-    }
+    // within the 48 KB that need no leave (a block's groups: MTV_MAX_VOCAB over 8 blocks at most)
+    static_assert(sizeof(LpShared) + kMaxGroups * sizeof(float) <= 48 * 1024);
+    static_assert(MTV_MAX_VOCAB / (64 / sizeof(T)) <= kMaxGroups * kMaxCluster);
     const cudaError_t e = cudaLaunchKernelEx(&cfg, logprob_rows_kernel<T>, A, blocks);
     if (e != cudaSuccess) return e;
   }
