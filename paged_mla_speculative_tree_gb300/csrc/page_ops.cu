@@ -129,7 +129,6 @@ template <int kMode> __global__ void __launch_bounds__(kPageThreads) page_table_
   uint32_t* grow_off = rel_off + A.num_rows + 1;   // [num_rows + 1]
   uint32_t* base = grow_off + A.num_rows + 1;      // [num_rows]: min(need, held)
   __shared__ uint64_t part[kPageThreads / 32];
-  const int rank = int(blockIdx.x), blocks = int(gridDim.x);
   const int tid = threadIdx.x;
   if (kMode == kMoves) grid_launch_dependents();
   const int64_t F = *A.num_free;
@@ -181,8 +180,8 @@ template <int kMode> __global__ void __launch_bounds__(kPageThreads) page_table_
     // all its pages from the stack (or to it), is copied row by row with up to
     // 16 loads a lane in flight; any other one searches each entry's row.
     const int lane = tid & 31;
-    const int64_t warp = int64_t(rank) * (kPageThreads / 32) + (tid >> 5);
-    const int64_t warps = int64_t(blocks) * (kPageThreads / 32);
+    const int64_t warp = int64_t(blockIdx.x) * (kPageThreads / 32) + (tid >> 5);
+    const int64_t warps = int64_t(gridDim.x) * (kPageThreads / 32);
     auto copy = [&](int32_t* to, int to_step, const int32_t* from, int from_step, int64_t lo, int64_t hi) {
       for (int64_t z0 = lo; z0 < hi; z0 += kRun) {  // to[to_step * z] = from[from_step * z]
         int32_t page[kRun / 32];
@@ -277,12 +276,12 @@ template <int kMode> __global__ void __launch_bounds__(kPageThreads) page_table_
   if (kMode == kAll) __syncthreads();
   else grid_dependency_wait();
   if (stack_ok) {
-    for (int r = rank * kPageThreads + tid; r < A.num_rows; r += blocks * kPageThreads) {
+    for (int r = tid; r < A.num_rows; r += kPageThreads) {  // (one block is left)
       const uint32_t rel = rel_off[r + 1] - rel_off[r], grow = grow_off[r + 1] - grow_off[r];
       if (rel) A.held[r] = int32_t(base[r]);
       else if (grow && int64_t(grow_off[r + 1]) <= G) A.held[r] = int32_t(base[r] + grow);
     }
-    if (rank == 0 && tid == 0) *A.num_free = int32_t(min(F + R - G, A.free_capacity));
+    if (tid == 0) *A.num_free = int32_t(min(F + R - G, A.free_capacity));
   }
   if (bad) set_err(A.err, bad);
 }
