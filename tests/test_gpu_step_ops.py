@@ -715,6 +715,56 @@ def test_logprobs_at_the_largest_temperatures(dtype, vocab, inv):
     assert got["top_logprobs"].tolist() == [[0.0]] and got["stats"][2].tolist() == [0.0] and np.isfinite(got["stats"]).all()
 
 
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("skip", [0, 1])
+@pytest.mark.parametrize("k", [32, 5, 1])
+def test_logprobs_whose_large_logits_sit_in_few_threads(dtype, skip, k):
+    """Fewer threads hold the large logits than ranks are asked for, in
+    thousands of groups of 64 bytes: one search a rank.  Distinct values, equal
+    ones, and the same behind a mask; rows at an odd address too."""
+    dt, vocab = TYPES[dtype], 1 << 20
+    buf = torch.zeros((4, vocab + skip), dtype=dt, device=DEV)
+    x = buf[:, skip:]
+    per = 64 // x.element_size()
+    i = torch.arange(vocab, device=DEV)
+    for r in range(4):
+        head = (-(x[r].data_ptr() % 64) % 64) // x.element_size()
+        res = torch.div(i - head, per, rounding_mode="floor") % 256
+        # k - 1 buckets of four neighbouring threads (a block holds a multiple of 256 groups)
+        few = (res // 32) * 8 + res % 8 < k - 1
+        g = torch.Generator(device=DEV).manual_seed(40 + r)
+        value = torch.rand((vocab,), generator=g, device=DEV) * (8 if r != 2 else 0) + 4
+        low = torch.full_like(value, -math.inf) if r == 3 else torch.rand((vocab,), generator=g, device=DEV) * -8
+        x[r] = torch.where(few, value, low).to(dt)
+    x[3, vocab // 2] = -3.0  # (for k == 1 the only one left)
+    check_logprobs(x, [0, vocab - 1, vocab // 3, vocab // 2], k=k)
+
+
+@pytest.mark.parametrize("dtype", list(TYPES))
+@pytest.mark.parametrize("vocab", [61, 5000, 131072, 1 << 20])
+@pytest.mark.parametrize("skip", [0, 1, 31])
+def test_logprobs_count_every_logit_once(dtype, vocab, skip):
+    """Logits of 0 and -inf alone: S is a whole number below 2^24, so that every
+    sum of it is exact, and ln S is within fp32's rounding and logf's 1 ulp."""
+    buf = torch.full((3, vocab + skip + 5), 9.0, dtype=TYPES[dtype], device=DEV)
+    x = buf[:, skip:skip + vocab]
+    x[0] = 0.0
+    x[1] = -math.inf
+    ends = min(vocab // 2, 40)  # the logits before and after the aligned ones, and a few more
+    x[1, :ends] = 0.0
+    x[1, vocab - ends + 1:] = 0.0
+    x[2] = 0.0
+    x[2, ::3] = -math.inf
+    counts = [vocab, 2 * ends - 1, vocab - (vocab + 2) // 3]
+    got, err = run_logprobs(x, [1, 1, 1], k=1)
+    want = np.log(np.array(counts, dtype=np.float64))
+    assert err == 0 and got["stats"][0].tolist() == [0.0] * 3
+    assert np.abs(got["stats"][1] - want).max() <= 2.0 ** -22 * want.max()  # 2^-24 of ln S and an ulp of it, twice over
+    missing = want - np.log(np.array(counts, dtype=np.float64) - 1)
+    assert missing[1] > 2.0 ** -22 * want.max()  # one end left out would be seen
+    np.testing.assert_allclose(got["stats"][2], want, atol=2.0 ** -21 * want.max())
+
+
 def test_logprobs_bad_tokens_and_rows():
     x = make_logits(6, 3, 100, torch.bfloat16)
     check_logprobs(x, [100, -2, 5, -1, 7, 7], [0, 1, 3, 2, -1, 2], err=binding.DEVERR_TOKEN)
