@@ -671,6 +671,10 @@ __global__ void __launch_bounds__(kLpThreads) logprob_tokens_kernel(const Logpro
 //   8 x 131,072 bf16    12.6   9.9   8.1   7.8     152 x 131,072 bf16   18.5  14.7  19.1  24.1
 //   1 x 64,000 bf16      7.9   7.3   6.7   7.1     304 x 131,072 bf16   21.4  19.9  29.1  39.8
 //   8 x 131,072 fp32    17.2  12.5   9.2   8.6     304 x 32,000 bf16     9.1  11.5  19.0  32.0
+// The bounds on a block's bytes are those of measured sizes, with no margin:
+// 128 KB is 131,072 bf16 in two, 32,000 bytes 64,000 bf16 in four.  A little
+// less, 129,280 bf16 say, falls to the rule's other side (one block a row from
+// 153 rows on, in place of two), of which nothing has been measured.
 int blocks_per_row(int64_t rows, int vocab, int size) {
   const int groups = vocab / (64 / size);
   int b = 1;

@@ -102,8 +102,9 @@ constexpr int kRun = 512;     // entries (runs of 32 throughout: 34 us in place 
 constexpr int kFewRows = 4;   // of a run that is copied row by row (every entry searched: 14.6 us)
 constexpr int kSearches = 4;  // entries a lane has in flight otherwise
 constexpr int64_t kPageBlocks = 152;  // of the grid: one an SM
-// Tables that one block does, for one launch in place of two: 256 rows up and
-// back, called from Python, 12 us against 15; in a graph 8.9 against 7.9.
+// Tables that one block does, for one launch in place of two.  Measured on one
+// table of 256 rows (5,888 entries), up and back: 12 us against 15 called from
+// Python, which is why; 8.9 against 7.9 in a graph, where the grid would win.
 constexpr int64_t kBlockEntries = 1 << 14;
 
 struct PageArgs {
