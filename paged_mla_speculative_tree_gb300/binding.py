@@ -78,7 +78,7 @@ SYMBOLS = ("mla_tree_verify_plan", "mla_tree_verify_choose_nsplit", "mla_tree_ve
            "mla_tree_verify_clear_device_error", "mla_tree_verify_read_device_error",
            "mla_tree_verify_run_static", "mla_tree_verify_read_static_device_error", "mla_tree_mask_build", "mla_tree_accept", "mla_kv_defrag",
            "mla_tree_group_prefix", "mla_page_table_update", "mla_slot_map_build", "mla_rope_freqs", "mla_rope_write",
-           "mla_token_logprobs")
+           "mla_token_logprobs", "mla_head_product", "mla_prefill_workspace", "mla_prefill_run", "mla_norm_rope_write")
 
 
 def library_path() -> str:
@@ -137,6 +137,17 @@ def load(path: str | None = None):
     lib.mla_rope_write.restype = I32
     lib.mla_token_logprobs.argtypes = [P, I32, I64, I32, I64, P, P, P, I64, P, P, I32, P, P, P, P]
     lib.mla_token_logprobs.restype = I32
+    F32 = ctypes.c_float
+    lib.mla_head_product.argtypes = [P, I64, I64, P, I64, I64, I64, P, I64, I64, I64, I32, I32, I32, I32, P]
+    lib.mla_head_product.restype = I32
+    lib.mla_prefill_workspace.argtypes = [I32, I32, I64, I64, I64, I32, ctypes.POINTER(I32), ctypes.POINTER(U64)]
+    lib.mla_prefill_workspace.restype = I32
+    lib.mla_prefill_run.argtypes = [P, I64, I64, P, I64, I64, P, I64, P, I64, I64, P, P, I32, I64, I64, I64, I64, I32,
+                                    I32, F32, I32, P, I64, I64, P, I32, P, U64, P, P]
+    lib.mla_prefill_run.restype = I32
+    lib.mla_norm_rope_write.argtypes = [P, I32, F32, I32, P, I64, P, I32, F32, P, I64, I64, I32, I32, P, P, I64, I64, P,
+                                        I64, I64, P, I64, P, P, I64, P, P, I64, P, P]
+    lib.mla_norm_rope_write.restype = I32
     if path == library_path():
         _lib = lib
     return lib
@@ -350,6 +361,7 @@ def tree_group_prefix(group_indptr, num_groups: int, max_group_prefix: int, kv_i
 
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+_HALF_TYPES = (torch.bfloat16, torch.float16)
 
 
 # The current stream's handle without building a Stream object, where torch has it.
@@ -553,6 +565,169 @@ def token_logprobs(logits, stats, tokens=None, logprobs=None, top_tokens=None, t
                  _dense(token_rows, _I32, device, "token_rows", n), n, _dense(logprobs, _F32, device, "logprobs", n),
                  _dense(stats, _F32, device, "stats", 3 * rows), k, _dense(top_tokens, _I32, device, "top_tokens", k * rows),
                  _dense(top_logprobs, _F32, device, "top_logprobs", k * rows), _dense(err, _I32, device, "err"))
+
+
+def _heads(t, dtype, device, name, shape):
+    """(address, token stride, head stride) of a [tokens, heads, dim] view dense in its last dimension."""
+    at = _strided(t, dtype, device, name, shape)
+    tok, head, inner = t.stride()
+    if inner != 1 and shape[2] > 1:
+        raise ValueError(f"{name} must be dense in its last dimension")
+    return at, tok, head
+
+
+def _code_of(t, name, types):
+    if t.dtype not in types:
+        raise TypeError(f"{name} must be one of {list(types)}, got {t.dtype}")
+    return _DTYPES[t.dtype]
+
+
+def head_product(x, w, out, stream=None, check: bool = True) -> int:
+    """Enqueues ``out[t, h] = x[t, h] @ w[h]`` of ``x`` [tokens, heads, k], ``w``
+    [heads, k, n] and ``out`` [tokens, heads, n], bf16 or fp16: the products of
+    latent attention's absorbed and expanded forms (see the header).  ``x`` and
+    ``out`` are views of any strides with a dense last dimension (an expanded
+    head dimension of ``x`` gives every head the same rows), ``w`` one of any."""
+    code = _code_of(x, "x", _HALF_TYPES)
+    if x.dim() != 3 or w.dim() != 3:
+        raise ValueError("x must be [tokens, heads, k] and w [heads, k, n]")
+    tokens, heads, k_dim = x.shape
+    n_dim = w.shape[2]
+    device = _device_of(x, "x")
+    xp, x_tok, x_head = _heads(x, x.dtype, device, "x", (tokens, heads, k_dim))
+    wp = _strided(w, x.dtype, device, "w", (heads, k_dim, n_dim))
+    op, out_tok, out_head = _heads(out, x.dtype, device, "out", (tokens, heads, n_dim))
+    return _call(load().mla_head_product, device, stream, check, xp, x_tok, x_head, wp, *w.stride(), op, out_tok, out_head,
+                 tokens, heads, k_dim, n_dim, code)
+
+
+def prefill_workspace(num_sms: int, bs: int, max_q: int, max_kv: int, num_q: int, num_heads: int):
+    """(split count, workspace bytes) of ``prefill_run`` for batches within these bounds (host only)."""
+    nsplit, size = ctypes.c_int(0), ctypes.c_uint64(0)
+    rc = load().mla_prefill_workspace(int(num_sms), int(bs), int(max_q), int(max_kv), int(num_q), int(num_heads),
+                                      ctypes.byref(nsplit), ctypes.byref(size))
+    if rc != MTV_OK:
+        raise MtvError(rc, "mla_prefill_workspace")
+    return int(nsplit.value), int(size.value)
+
+
+def prefill_run(q, k_nope, k_rope, v, qo_indptr, kv_indptr, max_q: int, max_kv: int, scale: float, out, lse=None,
+                causal: bool = True, nsplit: int = 1, workspace=None, err=None, stream=None, check: bool = True) -> int:
+    """Enqueues attention of ``q`` [rows, heads, 192] over ``k_nope`` [keys,
+    heads, 128] with ``k_rope`` [keys, 64] behind it, and ``v`` [keys, heads,
+    128], into ``out`` [rows, heads, 128] and ``lse`` [rows, heads] (see the
+    header).  Requests are runs of rows and keys by ``qo_indptr`` and
+    ``kv_indptr``, at most ``max_q`` and ``max_kv`` long."""
+    dtype, code = q.dtype, _code_of(q, "q", _HALF_TYPES)
+    if q.dim() != 3 or k_nope.dim() != 3:
+        raise ValueError("q must be [rows, heads, 192] and k_nope [keys, heads, 128]")
+    device = _device_of(q, "q")
+    num_q, heads = q.shape[:2]
+    num_kv = k_nope.shape[0]
+    bs = qo_indptr.numel() - 1
+    if bs < 0:
+        raise ValueError("qo_indptr must hold one element more than there are requests")
+    qp, q_tok, q_head = _heads(q, dtype, device, "q", (num_q, heads, 192))
+    kp, k_tok, k_head = _heads(k_nope, dtype, device, "k_nope", (num_kv, heads, 128))
+    vp, v_tok, v_head = _heads(v, dtype, device, "v", (num_kv, heads, 128))
+    rp = _strided(k_rope, dtype, device, "k_rope", (num_kv, 64))
+    kr_tok, kr_dim = k_rope.stride()
+    if kr_dim != 1:
+        raise ValueError("k_rope must be dense in its last dimension")
+    op, o_tok, o_head = _heads(out, dtype, device, "out", (num_q, heads, 128))
+    return _call(load().mla_prefill_run, device, stream, check, qp, q_tok, q_head, kp, k_tok, k_head, rp, kr_tok, vp, v_tok,
+                 v_head, _dense(qo_indptr, _I64, device, "qo_indptr"), _dense(kv_indptr, _I32, device, "kv_indptr", bs + 1),
+                 bs, max_q, max_kv, num_q, num_kv, heads, code, scale, 1 if causal else 0, op, o_tok, o_head,
+                 _dense(lse, _F32, device, "lse", num_q * heads), nsplit, _dense(workspace, torch.uint8, device, "workspace"),
+                 workspace.numel() if workspace is not None else 0, _dense(err, _I32, device, "err"))
+
+
+class MlaPrefill:
+    """Owns the split count and the workspace of ``prefill_run`` for fixed upper
+    bounds: ``bs`` requests of at most ``max_q`` new tokens and ``max_kv`` keys
+    each, in buffers of ``num_q`` query rows.
+
+    ``__call__`` never synchronises, so it can be captured in a graph.  Calls of
+    one object share its workspace: order them, or use an object each."""
+
+    def __init__(self, bs, max_q, num_q, max_kv, num_heads, device=None):
+        self.device = torch.device("cuda", torch.cuda.current_device() if device is None else device)
+        sms = torch.cuda.get_device_properties(self.device).multi_processor_count
+        self.bs, self.max_q, self.max_kv, self.num_q, self.num_heads = bs, max_q, max_kv, num_q, num_heads
+        self.nsplit, size = prefill_workspace(sms, bs, max_q, max_kv, num_q, num_heads)
+        self.workspace = torch.empty(size, dtype=torch.uint8, device=self.device) if size else None
+        self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+
+    def __call__(self, q, k_nope, k_rope, v, qo_indptr, kv_indptr, scale, out=None, lse=None, causal=True, stream=None):
+        """Returns (out, lse), allocated where they are not given (zeroed then: rows of no request stay as they are)."""
+        if q.shape[0] > self.num_q or q.shape[1] != self.num_heads or qo_indptr.numel() > self.bs + 1:
+            raise ValueError("the batch exceeds the bounds of this object")
+        if out is None:
+            out = torch.zeros((q.shape[0], q.shape[1], 128), dtype=q.dtype, device=q.device)
+        if lse is None:
+            lse = torch.zeros(tuple(q.shape[:2]), dtype=torch.float32, device=q.device)
+        prefill_run(q, k_nope, k_rope, v, qo_indptr, kv_indptr, self.max_q, self.max_kv, scale, out, lse, causal,
+                    self.nsplit, self.workspace, self.err, stream)
+        return out, lse
+
+    def device_error(self) -> int:
+        """The sticky error word (synchronises)."""
+        return int(self.err.item())
+
+
+def norm_rope_write(turns, positions, eps: float, layout: int = ROPE_INTERLEAVED, amplitude: float = 1.0, q_in=None,
+                    q_weight=None, q_nope=None, q_rope=None, c_in=None, c_weight=None, k_in=None, out_cache_loc=None,
+                    kv_pool=None, num_valid=None, err=None, stream=None, check: bool = True) -> int:
+    """Enqueues ``rope_write`` with root-mean-square norms in the same pass: the
+    heads of ``q_in`` [tokens, heads, nope + rope_dim] normalised by
+    ``q_weight`` (if given) into ``q_nope`` [tokens, heads, nope] and, turned,
+    ``q_rope`` [tokens, heads, rope_dim]; the latent rows ``c_in`` [tokens, 512]
+    normalised by ``c_weight`` (if given) and the turned ``k_in`` [tokens, 64]
+    written into ``kv_pool`` at ``out_cache_loc``.  Either half may be left out
+    (see the header)."""
+    if (q_in is None) != (q_rope is None):
+        raise ValueError("q_in and q_rope go together")
+    some = q_in if q_in is not None else c_in
+    if some is None:
+        raise ValueError("neither q_in nor c_in is given")
+    dtype = some.dtype
+    code = _code_of(some, "q_in" if q_in is not None else "c_in", _DTYPES)
+    if num_valid is not None and num_valid.numel() != 1:
+        raise ValueError("num_valid must hold one element")
+    device = _device_of(some, "q_in" if q_in is not None else "c_in")
+    tokens, rope_dim = positions.numel(), 2 * turns.numel()
+    qi = qn = qr = kp = cp = lp = pool = None
+    q_tok = q_head = n_tok = n_head = r_tok = r_head = heads = nope = k_tok = c_tok = slots = 0
+    if q_in is not None:
+        if q_in.dim() != 3 or q_in.shape[2] < rope_dim:
+            raise ValueError("q_in must be [tokens, heads, nope + rope_dim]")
+        heads, nope = q_in.shape[1], q_in.shape[2] - rope_dim
+        qi, q_tok, q_head = _heads(q_in, dtype, device, "q_in", (tokens, heads, nope + rope_dim))
+        qr, r_tok, r_head = _heads(q_rope, dtype, device, "q_rope", (tokens, heads, rope_dim))
+        if (q_nope is not None) != (q_weight is not None and nope > 0):
+            raise ValueError("q_nope goes with q_weight")
+        if q_nope is not None:
+            qn, n_tok, n_head = _heads(q_nope, dtype, device, "q_nope", (tokens, heads, nope))
+    elif q_nope is not None or q_weight is not None:
+        raise ValueError("q_weight and q_nope need q_in")
+    if kv_pool is not None or c_in is not None or k_in is not None or out_cache_loc is not None or c_weight is not None:
+        if kv_pool is None or c_in is None or k_in is None or out_cache_loc is None:
+            raise ValueError("kv_pool, c_in, k_in and out_cache_loc go together")
+        slots = kv_pool.shape[0]
+        if slots == 0:
+            raise ValueError("kv_pool is empty")
+        kp, cp = _strided(k_in, dtype, device, "k_in", (tokens, 64)), _strided(c_in, dtype, device, "c_in", (tokens, 512))
+        (k_tok, k_dim), (c_tok, c_dim) = k_in.stride(), c_in.stride()
+        if k_dim != 1 or c_dim != 1:
+            raise ValueError("k_in and c_in must be dense in their last dimension")
+        lp = _dense(out_cache_loc, _I64, device, "out_cache_loc", tokens)
+        pool = _dense(kv_pool, _BF16, device, "kv_pool", 576 * slots)
+    return _call(load().mla_norm_rope_write, device, stream, check, _dense(turns, _I64, device, "turns"), rope_dim, amplitude,
+                 layout, _dense(positions, _I64, device, "positions"), tokens, _dense(num_valid, _I64, device, "num_valid"),
+                 code, eps, qi, q_tok, q_head, heads, nope, _dense(q_weight, dtype, device, "q_weight", nope + rope_dim), qn,
+                 n_tok, n_head, qr, r_tok, r_head, cp, c_tok, _dense(c_weight, dtype, device, "c_weight", 512), kp, k_tok,
+                 lp, pool, slots, _dense(err, _I32, device, "err"))
+
 
 
 class MlaTreeVerify:
