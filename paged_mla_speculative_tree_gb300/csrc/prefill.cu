@@ -1,31 +1,87 @@
 // Causal attention of new tokens over keys and values expanded from latents
 // (head parts of 128 + 64 and 128): the form for prompts, where every query
 // row has many neighbours.
+//
+// prefill_kernel.  A block owns 256 query rows of one head (two stages of 128)
+// and walks the request's keys in tiles of 128, one pass with the running
+// maximum and sum of a softmax:
+//   S = Q K^T      12 k-steps of 16, both operands in shared memory, S in TMEM
+//   P = 2^(S c - m c) in the input type, over S's columns in TMEM
+//   O += P V       8 k-steps, P from TMEM, V as an MN-major operand
+// Roles: one warp issues the MMAs, one the TMA copies, and four warps a stage
+// the softmax, a thread a row.  While one stage's softmax works, the tensor
+// core computes the other's O += P V and next S, so that the order of issue is
+// PV0(j) QK0(j+1) PV1(j) QK1(j+1) PV0(j+1) ...  MMAs of one thread run in
+// order: S(j+1) may overwrite P(j) without a wait, and S(j+1) being there says
+// that O holds everything up to j.
+//
+// Shared memory: Q 96 KB and a ring of eight 16 KB slots that K (three slots of
+// 64 dims a tile) and V (two of 64 keys) pass through in the order of their
+// use.  Every slot is freed by its own commit, so a copy has two thirds of a
+// tile's time (about 1,800 of 2,600 cycles at full rate) from its slot's
+// release to its use; whole tiles of K and V do not fit twice beside Q.
+// TMEM: S0, S1, O0, O1 of 128 columns each.
+//
+// The maximum that scores refer to moves only when a row's scores grow by more
+// than 2^8 past it (weights stay below 2^8), so O is rarely rescaled.  P is
+// rounded to the input type, sums of weights stay in fp32.
+//
+// Every wait is bounded: one that gives up sets MTV_DEVERR_TIMEOUT and a flag
+// that ends the block's other waits; copies and MMAs in flight are waited for
+// (bounded too) before TMEM is freed.
+//
+// With few query rows the keys are split over blocks: each writes its
+// normalised part and its lse, and combine_kernel joins them.
 #include <math.h>
 #include <stdint.h>
 
+#include <type_traits>
+
 #include "mla_layer_ops.h"
 #include "mtv_internal.cuh"
+#include "tc_ptx.cuh"
+#include "tma.cuh"
 #include "vec_io.cuh"
 
 namespace mtv {
 namespace {
 
+using namespace ptx;
+
 constexpr int kNope = 128, kRope = 64, kQK = kNope + kRope, kV = 128;
+constexpr int kStageRows = 128, kBlockRows = 2 * kStageRows, kKeys = 128;
+constexpr int kThreads = 320;  // 4 + 4 softmax warps, MMA, TMA
+constexpr uint32_t kSlot = 16384;
+constexpr int kSlots = 8;
+constexpr uint32_t kQStage = 3 * kSlot, kOffRing = 2 * kQStage, kOffBars = kOffRing + kSlots * kSlot;
+enum : int {
+  B_Q = 0, B_FULL = 2, B_EMPTY = B_FULL + kSlots, B_S = B_EMPTY + kSlots, B_P = B_S + 2, B_O = B_P + 2, B_FIN = B_O + 2,
+  B_COUNT
+};
+constexpr uint32_t kOffCtl = kOffBars + 8 * B_COUNT;
+constexpr uint32_t kSmem = kOffCtl + 16 + 1024;  // + slack for 1 KB alignment
+static_assert(kSmem <= 227 * 1024, "shared memory");
+constexpr uint32_t kTmemS = 0, kTmemO = 256;
+constexpr float kRescaleLog2 = 8.f;
+constexpr long long kWaitCycles = 1ll << 31;
 
 struct PrefillArgs {
-  const void* q;
-  const void* k_nope;
-  const void* k_rope;
-  const void* v;
+  CUtensorMap q, k_nope, k_rope, v;
   void* out;
   float* lse;
+  float* part;      // [nsplit, num_q * heads, 128], then the lse [nsplit, num_q * heads]
   const int64_t* qo_indptr;
   const int32_t* kv_indptr;
   uint32_t* err;
-  int64_t q_tok, q_head, k_tok, k_head, kr_tok, v_tok, v_head, o_tok, o_head, num_q, num_kv, max_q, max_kv;
+  int64_t o_tok, o_head, num_q, num_kv, max_q, max_kv;
   float scale;
-  int bs, heads, causal;
+  int bs, heads, causal, nsplit, q_blocks;
+  int q_by_head, k_by_head, v_by_head;  // 0: one map for all heads
+};
+
+struct Ctl {
+  uint32_t tmem;
+  volatile int abort;
 };
 
 struct PrefillReq {
@@ -44,44 +100,378 @@ __device__ __forceinline__ PrefillReq load_prefill_req(const PrefillArgs& A, int
   return R;
 }
 
-// A warp a query row of one head, a key at a time.
-template <typename T>
-__global__ void __launch_bounds__(128) prefill_plain_kernel(const PrefillArgs A) {
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, r = blockIdx.z;
-  const PrefillReq R = load_prefill_req(A, r, threadIdx.x == 0);
-  const int64_t i = int64_t(blockIdx.x) * 4 + warp;
-  if (i >= R.n) return;
-  const T* q = static_cast<const T*>(A.q) + (R.q0 + i) * A.q_tok + h * A.q_head;
-  float x[6], acc[4] = {}, m = -INFINITY, l = 0.f;
-#pragma unroll
-  for (int u = 0; u < 6; ++u) x[u] = to_float(q[lane + 32 * u]) * A.scale;
-  const int64_t end = A.causal ? min(R.len, R.len - R.n + i + 1) : R.len;
-  for (int64_t j = 0; j < end; ++j) {
-    const T* kn = static_cast<const T*>(A.k_nope) + (R.k0 + j) * A.k_tok + h * A.k_head;
-    const T* kr = static_cast<const T*>(A.k_rope) + (R.k0 + j) * A.kr_tok;
-    const T* v = static_cast<const T*>(A.v) + (R.k0 + j) * A.v_tok + h * A.v_head;
-    float s = 0.f;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) s = fmaf(x[u], to_float(kn[lane + 32 * u]), s);
-#pragma unroll
-    for (int u = 0; u < 2; ++u) s = fmaf(x[4 + u], to_float(kr[lane + 32 * u]), s);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-    const float top = fmaxf(m, s), keep = expf(m - top), p = expf(s - top);
-    l = l * keep + p;
-#pragma unroll
-    for (int u = 0; u < 4; ++u) acc[u] = acc[u] * keep + p * to_float(v[lane + 32 * u]);
-    m = top;
+__device__ __forceinline__ float ex2(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
+// False when the wait gave up or another one has.
+__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (ctl->abort) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      ctl->abort = 1;
+      if (err) atomicOr(err, MTV_DEVERR_TIMEOUT);
+      return false;
+    }
   }
-  T* out = static_cast<T*>(A.out) + (R.q0 + i) * A.o_tok + h * A.o_head;
+  return true;
+}
+__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err) {
+  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, ctl, err);
+}
+// The same for what has to land before the block may end: ignores the flag.
+__device__ __noinline__ void drain(uint32_t bar, uint32_t parity, uint32_t* err) {
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity))
+    if (clock64() - t0 > kWaitCycles) {
+      if (err) atomicOr(err, MTV_DEVERR_TIMEOUT);
+      return;
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs A) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (base - raw) + kOffCtl);
+  auto bar = [&](int i) { return base + kOffBars + 8u * uint32_t(i); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  // blocks of a head side by side, the longest first; then splits, heads, requests
+  unsigned id = blockIdx.x;
+  const int qb = A.q_blocks - 1 - int(id % unsigned(A.q_blocks));
+  id /= unsigned(A.q_blocks);
+  const int split = int(id % unsigned(A.nsplit));
+  id /= unsigned(A.nsplit);
+  const int h = int(id % unsigned(A.heads)), r = int(id / unsigned(A.heads));
+  const PrefillReq R = load_prefill_req(A, r, tid == 0);
+  const int64_t row0 = int64_t(qb) * kBlockRows;
+  if (row0 >= R.n) return;
+
+  // key tiles of both stages: up to the last key that a stage's last row sees
+  const int64_t shift = R.len - R.n;  // query i sees keys up to shift + i
+  auto key_end = [&](int s) -> int64_t {
+    const int64_t first = row0 + s * kStageRows;
+    if (first >= R.n) return 0;
+    const int64_t last = min(R.n, first + kStageRows) - 1;
+    return A.causal ? max(int64_t(0), min(R.len, shift + last + 1)) : R.len;
+  };
+  auto tiles_of = [](int64_t keys) { return int((keys + kKeys - 1) / kKeys); };
+  const int tiles0 = tiles_of(key_end(0)), tiles1 = tiles_of(key_end(1));
+  const int each = (max(tiles0, tiles1) + A.nsplit - 1) / A.nsplit, begin = split * each;
+  auto mine = [&](int tiles) { return max(0, min(tiles - begin, each)); };
+  const int T0 = mine(tiles0), T1 = mine(tiles1), TN = max(T0, T1);
+
+  if (tid == 0) {
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i == B_P || i == B_P + 1 ? 4 : 1);
+    ctl->abort = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == 8) {
+    tmem_alloc(smem_u32(&ctl->tmem), 512);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+
+  if (warp == 9) {
+    // ------------------------------------------------------------- copies
+    if (lane == 0 && TN > 0) {
+      const int qh = A.q_by_head ? h : 0, kh = A.k_by_head ? h : 0, vh = A.v_by_head ? h : 0;
+      auto load_q = [&](int s) {
+        mbar_arrive_expect_tx(bar(B_Q + s), kQStage);
+        for (int c = 0; c < 3; ++c)
+          tma_load_3d(base + s * kQStage + c * kSlot, &A.q, 64 * c, qh, int(R.q0 + row0 + s * kStageRows), bar(B_Q + s));
+      };
+      int item = 0;
+      bool ok = true;
+      auto slot_for = [&]() -> bool {  // the next item's slot is free; its barrier expects the bytes
+        const int slot = item % kSlots;
+        if (item >= kSlots) ok = wait_for(bar(B_EMPTY + slot), ((item / kSlots) - 1) & 1, ctl, A.err);
+        if (ok) mbar_arrive_expect_tx(bar(B_FULL + slot), kSlot);
+        return ok;
+      };
+      if (T0 > 0) load_q(0);
+      for (int j = 0; j < TN && ok; ++j) {
+        const int row = int(R.k0) + (begin + j) * kKeys;
+        for (int c = 0; c < 3 && slot_for(); ++c, ++item) {
+          const uint32_t dst = base + kOffRing + (item % kSlots) * kSlot, full = bar(B_FULL + item % kSlots);
+          if (c < 2) tma_load_3d(dst, &A.k_nope, 64 * c, kh, row, full);
+          else tma_load_3d(dst, &A.k_rope, 0, 0, row, full);
+        }
+        if (j == 0 && T1 > 0) load_q(1);
+        for (int c = 0; c < 2 && ok && slot_for(); ++c, ++item) {
+          const uint32_t dst = base + kOffRing + (item % kSlots) * kSlot, full = bar(B_FULL + item % kSlots);
+          tma_load_3d(dst, &A.v, 0, vh, row + 64 * c, full);
+          tma_load_3d(dst + kSlot / 2, &A.v, 64, vh, row + 64 * c, full);
+        }
+      }
+      // what was asked for lands before the block ends, read or not (a second stage's Q is asked for with the first tile)
+      if (T0 > 0) drain(bar(B_Q), 0, A.err);
+      if (T1 > 0 && item >= 3) drain(bar(B_Q + 1), 0, A.err);
+      for (int i = max(0, item - kSlots); i < item; ++i) drain(bar(B_FULL + i % kSlots), (i / kSlots) & 1, A.err);
+    }
+    __syncwarp();
+  } else if (warp == 8) {
+    // ------------------------------------------------------------- products
+    constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
+    constexpr uint32_t id_qk = kBf16 ? idesc_bf16_f32(128, 128, 0, 0) : idesc_fp16_f32(128, 128, 0, 0);
+    constexpr uint32_t id_pv = kBf16 ? idesc_bf16_f32(128, 128, 0, 1) : idesc_fp16_f32(128, 128, 0, 1);
+    auto add = [](uint64_t d, uint32_t off) -> uint64_t {  // only the start address changes, without a carry
+      return (d & 0xFFFFFFFF00000000ull) | uint64_t(uint32_t(d) + (off >> 4));
+    };
+    auto slot_at = [&](int item) { return base + kOffRing + uint32_t(item % kSlots) * kSlot; };
+    auto arrived = [&](uint32_t b, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_for(b, parity, ctl, A.err)) != 0;
+    };
+    auto landed = [&](int item) { return arrived(bar(B_FULL + item % kSlots), (item / kSlots) & 1); };
+    auto qk = [&](int s, int j, bool last) -> bool {  // S_s = Q_s K(j)^T; `last` frees the tile's slots
+      for (int c = 0; c < 3; ++c) {
+        const int item = 5 * j + c;
+        if (!landed(item)) return false;
+        tc_fence_after();
+        if (lane == 0) {
+          const uint64_t a = smem_desc(base + s * kQStage + c * kSlot, 16, 1024, kSwizzle128B);
+          const uint64_t b = smem_desc(slot_at(item), 16, 1024, kSwizzle128B);
 #pragma unroll
-  for (int u = 0; u < 4; ++u) out[lane + 32 * u] = from_float<T>(end > 0 ? acc[u] / l : 0.f);
-  if (A.lse && lane == 0) A.lse[(R.q0 + i) * A.heads + h] = end > 0 ? m + logf(l) : -INFINITY;
+          for (int k = 0; k < 4; ++k) mma_ss(tmem + kTmemS + 128 * s, add(a, 32 * k), add(b, 32 * k), id_qk, c + k > 0);
+          if (last) mma_commit(bar(B_EMPTY + item % kSlots));
+        }
+      }
+      if (lane == 0) mma_commit(bar(B_S + s));
+      return true;
+    };
+    auto pv = [&](int s, int j, bool first, bool last, bool end) -> bool {  // O_s += P_s V(j)
+      // in the request's last tile, only k-steps that hold keys; the rows of V
+      // behind the last key may hold anything (another request's, or nobody's)
+      // and are zeroed, since a weight of 0 times NaN is NaN
+      const int keys = int(min(int64_t(kKeys), R.len - int64_t(begin + j) * kKeys)), steps = (keys + 15) / 16;
+      if (!landed(5 * j + 3) || !landed(5 * j + 4)) return false;
+      if (first && keys < 16 * steps) {
+        for (int u = 16 * keys + lane; u < 256 * steps; u += 32) {  // 16-byte units, 16 a row
+          const int key = u / 16, part = u % 16;
+          st_shared_v4(slot_at(5 * j + 3 + key / 64) + (part / 8) * (kSlot / 2) + (key % 64) * 128 + (part % 8) * 16, 0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+      }
+      if (!arrived(bar(B_P + s), j & 1)) return false;
+      tc_fence_after();
+      if (lane == 0) {
+#pragma unroll
+        for (int c = 0; c < 2; ++c) {
+          const uint64_t b = smem_desc(slot_at(5 * j + 3 + c), kSlot / 2, 1024, kSwizzle128B);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            if (4 * c + k < steps)
+              mma_ts(tmem + kTmemO + 128 * s, tmem + kTmemS + 128 * s + 8 * (4 * c + k), add(b, 2048 * k), id_pv,
+                     j > 0 || c + k > 0);
+          if (last) mma_commit(bar(B_EMPTY + (5 * j + 3 + c) % kSlots));
+        }
+        if (end) mma_commit(bar(B_O + s));
+      }
+      return true;
+    };
+    bool ok = true;
+    if (T0 > 0) ok = arrived(bar(B_Q), 0) && qk(0, 0, T1 == 0);
+    if (ok && T1 > 0) ok = arrived(bar(B_Q + 1), 0) && qk(1, 0, true);
+    for (int j = 0; j < TN && ok; ++j) {
+      // stage 1 uses a tile last where it uses it (T1 >= T0, or it is empty)
+      if (j < T0) ok = pv(0, j, true, j >= T1, j + 1 == T0) && (j + 1 >= T0 || qk(0, j + 1, j + 1 >= T1));
+      if (ok && j < T1) ok = pv(1, j, j >= T0, true, j + 1 == T1) && (j + 1 >= T1 || qk(1, j + 1, true));
+    }
+    if (lane == 0 && TN > 0) {  // every MMA issued has run once this arrives
+      mma_commit(bar(B_FIN));
+      drain(bar(B_FIN), 0, A.err);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- softmax
+    const int s = warp >> 2;
+    const int64_t i0 = row0 + s * kStageRows + (warp & 3) * 32, i = i0 + lane;  // rows of the request
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const int Ts = s ? T1 : T0;
+    const float c = A.scale * kLog2e, grow = kRescaleLog2 / c;
+    // keys before `end` are this row's; tiles that end before `clear` need no mask in this warp
+    const int end = int(A.causal ? max(int64_t(0), min(R.len, shift + i + 1)) : R.len);
+    const int clear = int(A.causal ? max(int64_t(0), min(R.len, shift + i0 + 1)) : R.len);
+    float m = -INFINITY, l = 0.f;
+    bool ok = true;
+    uint32_t x[128];
+    for (int j = 0; j < Ts; ++j) {
+      ok = wait_for(bar(B_S + s), j & 1, ctl, A.err);
+      ok = __all_sync(0xffffffffu, ok);
+      if (!ok) break;
+      tc_fence_after();
+      tmem_ld128_sync(tmem + lanes + kTmemS + 128 * s, x);
+      const int k0 = (begin + j) * kKeys;
+      if (k0 + kKeys > clear) {
+        const int live = end - k0;
+#pragma unroll
+        for (int u = 0; u < 128; ++u) x[u] = u < live ? x[u] : 0xff800000u;
+      }
+      float top0 = -INFINITY, top1 = -INFINITY, top2 = -INFINITY, top3 = -INFINITY;
+#pragma unroll
+      for (int u = 0; u < 128; u += 8) {
+        top0 = max3(top0, __uint_as_float(x[u]), __uint_as_float(x[u + 1]));
+        top1 = max3(top1, __uint_as_float(x[u + 2]), __uint_as_float(x[u + 3]));
+        top2 = max3(top2, __uint_as_float(x[u + 4]), __uint_as_float(x[u + 5]));
+        top3 = max3(top3, __uint_as_float(x[u + 6]), __uint_as_float(x[u + 7]));
+      }
+      const float top = fmaxf(max3(top0, top1, top2), top3);
+      const bool move = top > m + grow || m == -INFINITY;  // the first maximum is taken as it is
+      if (__any_sync(0xffffffffu, move && j > 0)) {
+        // O holds all tiles before this one (its scores come after them)
+        const float keep = move ? (m == -INFINITY ? 0.f : ex2((m - top) * c)) : 1.f;
+        l *= keep;
+        const uint32_t o = tmem + lanes + kTmemO + 128 * s;
+#pragma unroll 1
+        for (int u = 0; u < 128; u += 32) {
+          uint32_t y[32];
+          tmem_ld32_sync(o + u, y);
+#pragma unroll
+          for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * keep);
+          tmem_st32_sync(o + u, y);
+        }
+      }
+      if (move) m = top;
+      const float ref = m == -INFINITY ? 0.f : m * c;
+      const uint64_t c2 = f2_pack(c, c), ref2 = f2_pack(-ref, -ref);
+      uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
+#pragma unroll
+      for (int half = 0; half < 2; ++half) {
+        uint32_t p[32];
+#pragma unroll
+        for (int u = 0; u < 32; ++u) {
+          float a, b;
+          f2_unpack(f2_fma(f2_pack(__uint_as_float(x[64 * half + 2 * u]), __uint_as_float(x[64 * half + 2 * u + 1])), c2, ref2), a, b);
+          a = ex2(a), b = ex2(b);
+          if (u & 1) sum1 = f2_add(sum1, f2_pack(a, b));
+          else sum0 = f2_add(sum0, f2_pack(a, b));
+          p[u] = join(a, b, T());
+        }
+        tmem_st32_sync(tmem + lanes + kTmemS + 128 * s + 32 * half, p);
+      }
+      float a, b;
+      f2_unpack(f2_add(sum0, sum1), a, b);
+      l += a + b;
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_P + s));
+    }
+    if (ok && Ts > 0) ok = __all_sync(0xffffffffu, wait_for(bar(B_O + s), 0, ctl, A.err));
+    if (ok && i0 < R.n) {
+      const bool some = l != 0.f;  // true for a NaN too, which the row then shows
+      const float inv = some ? 1.f / l : 0.f;
+      const int64_t at = (R.q0 + i) * A.heads + h;
+      const float lse = some ? m * A.scale + logf(l) : -INFINITY;
+      const int live = int(min(int64_t(32), R.n - i0));
+      tc_fence_after();
+      // rows to memory through this stage's part of Q (every product that read it has run), so
+      // that a warp stores whole rows; 16-byte units are swizzled by the row
+      const uint32_t mine_s = base + s * kQStage + uint32_t((warp & 3) * 32) * 256u;
+      if (A.nsplit == 1) {
+        if (A.lse && i < R.n) A.lse[at] = lse;
+#pragma unroll
+        for (int u = 0; u < 128; u += 32) {
+          uint32_t y[32] = {};
+          if (Ts > 0) tmem_ld32_sync(tmem + lanes + kTmemO + 128 * s + u, y);
+#pragma unroll
+          for (int e = 0; e < 32; e += 8) {
+            float f[8];
+#pragma unroll
+            for (int g = 0; g < 8; ++g) f[g] = some ? __uint_as_float(y[e + g]) * inv : 0.f;
+            const uint4 w = pack<T>(f);
+            st_shared_v4(mine_s + lane * 256 + ((((u + e) / 8) ^ (lane & 15)) << 4), w.x, w.y, w.z, w.w);
+          }
+        }
+        __syncwarp();
+        T* out = static_cast<T*>(A.out) + (R.q0 + i0) * A.o_tok + int64_t(h) * A.o_head;
+#pragma unroll 4
+        for (int u = lane; u < live * 16; u += 32) {
+          const int rr = u >> 4, cc = u & 15;
+          const float4 w = ld_shared_f4(mine_s + rr * 256 + ((cc ^ (rr & 15)) << 4));
+          *reinterpret_cast<float4*>(out + int64_t(rr) * A.o_tok + cc * 8) = w;
+        }
+      } else {
+        const int64_t all = A.num_q * A.heads;
+        if (i < R.n) A.part[int64_t(A.nsplit) * all * kV + split * all + at] = lse;
+        // a part without weights is not read by the combine
+#pragma unroll 1
+        for (int u = 0; u < 128; u += 32) {
+          uint32_t y[32] = {};
+          if (Ts > 0) tmem_ld32_sync(tmem + lanes + kTmemO + 128 * s + u, y);
+#pragma unroll
+          for (int e = 0; e < 32; e += 4) {
+            const float f[4] = {__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv, __uint_as_float(y[e + 2]) * inv,
+                                __uint_as_float(y[e + 3]) * inv};
+            st_shared_v4(mine_s + lane * 128 + (((e / 4) ^ (lane & 7)) << 4), __float_as_uint(f[0]), __float_as_uint(f[1]),
+                         __float_as_uint(f[2]), __float_as_uint(f[3]));
+          }
+          __syncwarp();
+          float* part = A.part + (split * all + (R.q0 + i0) * A.heads + h) * kV + u;
+#pragma unroll 4
+          for (int w = lane; w < live * 8; w += 32) {
+            const int rr = w >> 3, cc = w & 7;
+            *reinterpret_cast<float4*>(part + int64_t(rr) * A.heads * kV + cc * 4) =
+                ld_shared_f4(mine_s + rr * 128 + ((cc ^ (rr & 7)) << 4));
+          }
+          __syncwarp();
+        }
+      }
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 8) tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of split keys by their lse: a warp a row of one head.
+template <typename T>
+__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ PrefillArgs A) {
+  const int lane = threadIdx.x & 31;
+  const int r = blockIdx.z, h = blockIdx.y;
+  const PrefillReq R = load_prefill_req(A, r, false);
+  const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+  if (i >= R.n) return;
+  const int64_t all = A.num_q * A.heads, at = (R.q0 + i) * A.heads + h;
+  const float* lse = A.part + int64_t(A.nsplit) * all * kV + at;
+  const float a = lane < A.nsplit ? lse[lane * all] : -INFINITY, b = lane + 32 < A.nsplit ? lse[(lane + 32) * all] : -INFINITY;
+  float top = fmaxf(a, b);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+  const float ref = top == -INFINITY ? 0.f : top;
+  float wa = expf(a - ref), wb = expf(b - ref), sum = wa + wb;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  const float inv = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+  for (int k = 0; k < A.nsplit; ++k) {
+    const float w = __shfl_sync(0xffffffffu, k < 32 ? wa : wb, k & 31) * inv;
+    if (w == 0.f) continue;  // a part without weights was not written
+    const float4 v = *reinterpret_cast<const float4*>(A.part + (k * all + at) * kV + 4 * lane);
+    acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y), acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+  }
+  T* out = static_cast<T*>(A.out) + (R.q0 + i) * A.o_tok + int64_t(h) * A.o_head;
+  *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(join(acc.x, acc.y, T()), join(acc.z, acc.w, T()));
+  if (A.lse && lane == 0) A.lse[at] = sum != 0.f ? ref + logf(sum) : -INFINITY;
 }
 
 template <typename T> cudaError_t launch_prefill(const PrefillArgs& A, cudaStream_t st) {
-  const dim3 grid(unsigned((A.max_q + 3) / 4), unsigned(A.heads), unsigned(A.bs));
-  prefill_plain_kernel<T><<<grid, 128, 0, st>>>(A);
+  const int64_t blocks = int64_t(A.q_blocks) * A.nsplit * A.heads * A.bs;
+  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+  if (e != cudaSuccess) return e;
+  prefill_kernel<T><<<unsigned(blocks), kThreads, kSmem, st>>>(A);
+  e = cudaGetLastError();
+  if (e != cudaSuccess || A.nsplit == 1) return e;
+  combine_kernel<T><<<dim3(unsigned((A.max_q + 7) / 8), unsigned(A.heads), unsigned(A.bs)), 256, 0, st>>>(A);
   return cudaGetLastError();
 }
 
@@ -99,7 +489,13 @@ extern "C" int mla_prefill_workspace(int num_sms, int bs, int64_t max_q, int64_t
   if (num_sms < 1 || bs < 0 || bs > MTV_MAX_HEADS || max_q < 0 || max_kv < 0 || num_q < 0 || num_q > INT32_MAX ||
       max_q > INT32_MAX || max_kv > INT32_MAX || num_heads < 0 || num_heads > MTV_MAX_HEADS)
     return MTV_E_BAD_ARGUMENT;
-  *nsplit_out = 1;
+  // as many splits as leave every one an SM, of eight key tiles at least (about 6 us: a split costs a
+  // second launch and its parts' way through memory)
+  const int64_t blocks = int64_t(bs) * num_heads * ((max_q + kBlockRows - 1) / kBlockRows);
+  const int64_t most = blocks > 0 ? num_sms / blocks : 1, worth = (max_kv + kKeys - 1) / kKeys / 8;
+  int64_t n = most < worth ? most : worth;
+  if (n > MTV_MAX_PREFILL_SPLITS) n = MTV_MAX_PREFILL_SPLITS;
+  *nsplit_out = n < 2 ? 1 : int(n);
   *bytes_out = workspace_bytes_of(*nsplit_out, num_q, num_heads);
   return MTV_OK;
 }
@@ -130,10 +526,32 @@ extern "C" int mla_prefill_run(const void* q, int64_t q_tok_stride, int64_t q_he
                     v_head_stride, out_tok_stride, out_head_stride})
     bits |= uintptr_t(s) * 2;
   if (bits & 15) return MTV_E_BAD_ARGUMENT;
-  const PrefillArgs A{q, k_nope, k_rope, v, out, lse, qo_indptr, kv_indptr, err, q_tok_stride, q_head_stride,
-                      k_tok_stride, k_head_stride, k_rope_stride, v_tok_stride, v_head_stride, out_tok_stride,
-                      out_head_stride, num_q, num_kv, max_q, max_kv, scale, bs, num_heads, causal};
+  // strides that a tensor map takes: no negative ones, rows apart
+  for (int64_t s : {q_tok_stride, q_head_stride, k_tok_stride, k_head_stride, k_rope_stride, v_tok_stride, v_head_stride})
+    if (!mappable_stride(s)) return MTV_E_BAD_ARGUMENT;
+  if ((num_q > 1 && q_tok_stride == 0) || (num_kv > 1 && (k_tok_stride == 0 || k_rope_stride == 0 || v_tok_stride == 0)))
+    return MTV_E_BAD_ARGUMENT;
+  const int64_t q_blocks = (max_q + kBlockRows - 1) / kBlockRows;
+  if (q_blocks * nsplit > INT32_MAX || q_blocks * nsplit * num_heads > INT32_MAX ||
+      q_blocks * nsplit * num_heads * bs > INT32_MAX)
+    return MTV_E_UNSUPPORTED;
+  PrefillArgs A;
+  const bool bf16 = dtype == MTV_DTYPE_BF16;
+  const int64_t kv_rows = num_kv > 0 ? num_kv : 1;  // without keys nothing is copied: any valid map will do
+  const void* kn = num_kv > 0 ? k_nope : q;
+  const void* kr = num_kv > 0 ? k_rope : q;
+  const void* vv = num_kv > 0 ? v : q;
+  if (!encode_heads_map(&A.q, bf16, q, num_q, q_tok_stride, num_heads, q_head_stride, kQK, 64, kStageRows) ||
+      !encode_heads_map(&A.k_nope, bf16, kn, kv_rows, k_tok_stride, num_heads, k_head_stride, kNope, 64, kKeys) ||
+      !encode_heads_map(&A.k_rope, bf16, kr, kv_rows, k_rope_stride, 1, 0, kRope, 64, kKeys) ||
+      !encode_heads_map(&A.v, bf16, vv, kv_rows, v_tok_stride, num_heads, v_head_stride, kV, 64, 64))
+    return MTV_E_CUDA;
+  A.out = out, A.lse = lse, A.part = static_cast<float*>(workspace), A.qo_indptr = qo_indptr, A.kv_indptr = kv_indptr;
+  A.err = err, A.o_tok = out_tok_stride, A.o_head = out_head_stride, A.num_q = num_q, A.num_kv = num_kv;
+  A.max_q = max_q, A.max_kv = max_kv, A.scale = scale, A.bs = bs, A.heads = num_heads, A.causal = causal;
+  A.nsplit = nsplit, A.q_blocks = int(q_blocks);
+  A.q_by_head = q_head_stride != 0, A.k_by_head = k_head_stride != 0, A.v_by_head = v_head_stride != 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == MTV_DTYPE_BF16 ? launch_prefill<__nv_bfloat16>(A, st) : launch_prefill<__half>(A, st);
+  const cudaError_t e = bf16 ? launch_prefill<__nv_bfloat16>(A, st) : launch_prefill<__half>(A, st);
   return e == cudaSuccess ? MTV_OK : MTV_E_CUDA;
 }
