@@ -65,6 +65,8 @@ extern "C" {
  * num_heads      0 .. MTV_MAX_HEADS.
  * k_dim, n_dim   1 .. MTV_MAX_HEAD_DIM.
  * dtype          MTV_DTYPE_BF16 or MTV_DTYPE_FP16, of x, w and out.
+ * err            device uint32 or NULL: MTV_DEVERR_TIMEOUT when a bounded wait
+ *                gave up.
  *
  * Any strides are taken.  The tensor-core kernel runs where every address and
  * every stride but the innermost is a multiple of 16 bytes and w is dense in k
@@ -73,7 +75,7 @@ extern "C" {
 int mla_head_product(const void* x, int64_t x_tok_stride, int64_t x_head_stride, const void* w,
                      int64_t w_head_stride, int64_t w_k_stride, int64_t w_n_stride, void* out,
                      int64_t out_tok_stride, int64_t out_head_stride, int64_t num_tokens, int num_heads, int k_dim,
-                     int n_dim, int dtype, void* stream);
+                     int n_dim, int dtype, uint32_t* err, void* stream);
 
 /*
  * mla_prefill_workspace -- workspace of mla_prefill_run and its split count,

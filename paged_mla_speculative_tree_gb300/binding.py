@@ -138,7 +138,7 @@ def load(path: str | None = None):
     lib.mla_token_logprobs.argtypes = [P, I32, I64, I32, I64, P, P, P, I64, P, P, I32, P, P, P, P]
     lib.mla_token_logprobs.restype = I32
     F32 = ctypes.c_float
-    lib.mla_head_product.argtypes = [P, I64, I64, P, I64, I64, I64, P, I64, I64, I64, I32, I32, I32, I32, P]
+    lib.mla_head_product.argtypes = [P, I64, I64, P, I64, I64, I64, P, I64, I64, I64, I32, I32, I32, I32, P, P]
     lib.mla_head_product.restype = I32
     lib.mla_prefill_workspace.argtypes = [I32, I32, I64, I64, I64, I32, ctypes.POINTER(I32), ctypes.POINTER(U64)]
     lib.mla_prefill_workspace.restype = I32
@@ -582,7 +582,7 @@ def _code_of(t, name, types):
     return _DTYPES[t.dtype]
 
 
-def head_product(x, w, out, stream=None, check: bool = True) -> int:
+def head_product(x, w, out, err=None, stream=None, check: bool = True) -> int:
     """Enqueues ``out[t, h] = x[t, h] @ w[h]`` of ``x`` [tokens, heads, k], ``w``
     [heads, k, n] and ``out`` [tokens, heads, n], bf16 or fp16: the products of
     latent attention's absorbed and expanded forms (see the header).  ``x`` and
@@ -598,7 +598,7 @@ def head_product(x, w, out, stream=None, check: bool = True) -> int:
     wp = _strided(w, x.dtype, device, "w", (heads, k_dim, n_dim))
     op, out_tok, out_head = _heads(out, x.dtype, device, "out", (tokens, heads, n_dim))
     return _call(load().mla_head_product, device, stream, check, xp, x_tok, x_head, wp, *w.stride(), op, out_tok, out_head,
-                 tokens, heads, k_dim, n_dim, code)
+                 tokens, heads, k_dim, n_dim, code, _dense(err, _I32, device, "err"))
 
 
 def prefill_workspace(num_sms: int, bs: int, max_q: int, max_kv: int, num_q: int, num_heads: int):

@@ -2,22 +2,279 @@
 // the values of latent outputs and the expansion of latents to every head's
 // keys and values (the latent form: "The Glue That Binds" -- "The Broader
 // Engineering Effort").
+//
+// head_product_kernel.  A unit is 128 tokens x nt outputs of one head; a block
+// takes a run of units, of which those of one (head, nt outputs) follow each
+// other, so that their weights (all of k, at most 128 KB) are loaded once and
+// stay in shared memory while the tokens stream through a ring of slots of
+// 128 tokens x 64 k.  Roles: one warp issues the copies, one the MMAs, four
+// take the sums (two TMEM buffers) through shared memory to bulk stores.  What
+// lies outside a tensor reads as zero and is not stored, so odd sizes need no
+// code of their own.
+//
+// Weights dense in k are a K-major operand (chunks of 64 k x nt rows), weights
+// dense in n an MN-major one (blocks of 64 n x 64 k).
+//
+// Every wait is bounded: one that gives up sets MTV_DEVERR_TIMEOUT and a flag
+// that ends the block's other waits; copies and MMAs in flight are waited for
+// (bounded too) before TMEM is freed.
 #include <stdint.h>
+
+#include <type_traits>
 
 #include "mla_layer_ops.h"
 #include "mtv_internal.cuh"
+#include "pipeline.cuh"
+#include "tc_ptx.cuh"
+#include "tma.cuh"
 #include "vec_io.cuh"
 
 namespace mtv {
 namespace {
 
+using namespace ptx;
+
 struct ProductArgs {
   const void* x;
   const void* w;
   void* out;
+  uint32_t* err;
   int64_t x_tok, x_head, w_head, w_k, w_n, out_tok, out_head, tokens;
   int heads, k_dim, n_dim;
 };
+
+constexpr int kRows = 128, kChunk = 64;   // tokens a unit, k a chunk
+constexpr int kMaxChunks = MTV_MAX_HEAD_DIM / kChunk, kMaxSlots = 8;
+constexpr uint32_t kXSlot = kRows * kChunk * 2, kMaxWeights = 131072;
+constexpr uint32_t kBlockBytes = 32 * 128;  // staged output: 32 rows x 64 columns a warp, two of them
+constexpr int kThreads = 192;
+enum : int {
+  B_XFULL = 0, B_XEMPTY = B_XFULL + kMaxSlots, B_WFULL = B_XEMPTY + kMaxSlots, B_WFREE = B_WFULL + kMaxChunks,
+  B_ACC, B_ACCFREE = B_ACC + 2, B_FIN = B_ACCFREE + 2, B_COUNT
+};
+constexpr uint32_t kOffCtl = 8 * B_COUNT, kOffData = 1024;
+static_assert(kOffCtl + sizeof(Ctl) <= kOffData, "barriers");
+
+struct TensorArgs {
+  CUtensorMap x, w, out;
+  uint32_t* err;
+  int64_t units, m_tiles, tokens;   // units: heads * n_tiles * m_tiles
+  int n_tiles, nt, chunks, slots, w_k_major, x_by_head, w_by_head, out_by_head, n_dim;
+};
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_constant__ TensorArgs A) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (base - raw) + kOffCtl);
+  auto bar = [&](int i) { return base + 8u * uint32_t(i); };
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const uint32_t w_chunk = uint32_t(A.nt) * 128u;
+  const uint32_t off_x = kOffData + uint32_t(A.chunks) * w_chunk, off_out = off_x + uint32_t(A.slots) * kXSlot;
+  const int64_t first = A.units * blockIdx.x / gridDim.x, last = A.units * (blockIdx.x + 1) / gridDim.x;
+  const uint32_t cols = A.nt <= 64 ? 128u : 2u * uint32_t(A.nt);
+
+  if (tid == 0) {
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i == B_ACCFREE || i == B_ACCFREE + 1 ? 4 : 1);
+    ctl->abort = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == 1) {
+    tmem_alloc(smem_u32(&ctl->tmem), cols);
+    tmem_relinquish();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- copies
+    if (lane == 0) {
+      int64_t item = 0, group = -1;
+      int loads = 0, asked = 0;  // of weights, and chunks of the last one
+      bool ok = true;
+      for (int64_t u = first; u < last && ok; ++u) {
+        const int64_t g = u / A.m_tiles;
+        const int h = int(g / A.n_tiles), n0 = int(g % A.n_tiles) * A.nt, t0 = int(u % A.m_tiles) * kRows;
+        const int xh = A.x_by_head ? h : 0, wh = A.w_by_head ? h : 0;
+        const bool fresh = g != group;
+        for (int c = 0; c < A.chunks && ok; ++c, ++item) {
+          const int slot = int(item % A.slots);
+          if (item >= A.slots) ok = wait_for(bar(B_XEMPTY + slot), uint32_t(item / A.slots - 1) & 1, ctl, A.err);
+          if (!ok) break;
+          mbar_arrive_expect_tx(bar(B_XFULL + slot), kXSlot);
+          tma_load_3d(base + off_x + slot * kXSlot, &A.x, c * kChunk, xh, t0, bar(B_XFULL + slot));
+          if (!fresh) continue;
+          if (c == 0) {
+            if (loads > 0) ok = wait_for(bar(B_WFREE), uint32_t(loads - 1) & 1, ctl, A.err);
+            if (!ok) {
+              ++item;
+              break;
+            }
+            ++loads, asked = 0, group = g;
+          }
+          ++asked;
+          const uint32_t dst = base + kOffData + c * w_chunk;
+          mbar_arrive_expect_tx(bar(B_WFULL + c), w_chunk);
+          if (A.w_k_major) {
+            tma_load_3d(dst, &A.w, c * kChunk, wh, n0, bar(B_WFULL + c));
+          } else {
+            for (int b = 0; b < A.nt; b += 64) tma_load_3d(dst + b * 128, &A.w, n0 + b, wh, c * kChunk, bar(B_WFULL + c));
+          }
+        }
+      }
+      // what was asked for lands before the block ends, read or not
+      for (int64_t i = item > A.slots ? item - A.slots : 0; i < item; ++i)
+        drain(bar(B_XFULL + int(i % A.slots)), uint32_t(i / A.slots) & 1, A.err);
+      for (int c = 0; c < asked; ++c) drain(bar(B_WFULL + c), uint32_t(loads - 1) & 1, A.err);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- products
+    if (lane == 0) {
+      const uint32_t id = std::is_same<T, __nv_bfloat16>::value ? idesc_bf16_f32(kRows, A.nt, 0, A.w_k_major ? 0 : 1)
+                                                                : idesc_fp16_f32(kRows, A.nt, 0, A.w_k_major ? 0 : 1);
+      const uint32_t w_step = A.w_k_major ? 32u : 2048u;
+      int64_t item = 0, group = -1, n = 0;
+      int loads = 0;
+      bool ok = true;
+      for (int64_t u = first; u < last && ok; ++u, ++n) {
+        const int64_t g = u / A.m_tiles;
+        const bool fresh = g != group;
+        if (fresh) ++loads, group = g;
+        const int buf = int(n & 1);
+        if (n >= 2) ok = wait_for(bar(B_ACCFREE + buf), uint32_t(n / 2 - 1) & 1, ctl, A.err);
+        for (int c = 0; c < A.chunks && ok; ++c, ++item) {
+          const int slot = int(item % A.slots);
+          if (fresh) ok = wait_for(bar(B_WFULL + c), uint32_t(loads - 1) & 1, ctl, A.err);
+          ok = ok && wait_for(bar(B_XFULL + slot), uint32_t(item / A.slots) & 1, ctl, A.err);
+          if (!ok) break;
+          tc_fence_after();
+          const uint64_t a = smem_desc(base + off_x + slot * kXSlot, 16, 1024, kSwizzle128B);
+          const uint64_t b = smem_desc(base + kOffData + c * w_chunk, A.w_k_major ? 16 : 8192, 1024, kSwizzle128B);
+#pragma unroll
+          for (int k = 0; k < 4; ++k)
+            mma_ss(tmem + uint32_t(A.nt) * buf, desc_add(a, 32 * k), desc_add(b, w_step * k), id, c + k > 0);
+          mma_commit(bar(B_XEMPTY + slot));
+        }
+        if (!ok) break;
+        mma_commit(bar(B_ACC + buf));
+        if (u + 1 < last && (u + 1) / A.m_tiles != g) mma_commit(bar(B_WFREE));
+      }
+      mma_commit(bar(B_FIN));  // every MMA issued has run once this arrives
+      drain(bar(B_FIN), 0, A.err);
+    }
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- sums to memory
+    const int q = warp & 3;  // TMEM lane quarter
+    const uint32_t stage = base + off_out + uint32_t(q) * 2u * kBlockBytes;
+    int64_t n = 0;
+    int block = 0;
+    for (int64_t u = first; u < last; ++u, ++n) {
+      const int64_t g = u / A.m_tiles;
+      const int h = int(g / A.n_tiles), n0 = int(g % A.n_tiles) * A.nt;
+      const int64_t t0 = u % A.m_tiles * kRows + q * 32;
+      const int buf = int(n & 1);
+      const bool ok = wait_for(bar(B_ACC + buf), uint32_t(n / 2) & 1, ctl, A.err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const int width = t0 < A.tokens ? min(A.nt, A.n_dim - n0) : 0;  // a store starts inside the tensor, which clips it
+      for (int b = 0; b < width; b += 64, ++block) {
+        const uint32_t to = stage + uint32_t(block & 1) * kBlockBytes;
+        if (lane == 0) bulk_wait_group_read<1>();  // the store before last has read its block
+        __syncwarp();
+        uint32_t y[64];
+        tmem_ld64_sync(tmem + (uint32_t(q * 32) << 16) + uint32_t(A.nt) * buf + b, y);
+#pragma unroll
+        for (int e = 0; e < 64; e += 8) {
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(y[e + i]);
+          const uint4 v = pack<T>(f);
+          st_shared_v4(to + lane * 128 + (((e / 8) ^ (lane & 7)) << 4), v.x, v.y, v.z, v.w);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&A.out, n0 + b, A.out_by_head ? h : 0, int(t0), to);
+          bulk_commit_group();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(bar(B_ACCFREE + buf));
+    }
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc(tmem, cols);
+}
+
+int sm_count() {
+  int device = 0, sms = 0;
+  if (cudaGetDevice(&device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess || sms < 1)
+    sms = 1;
+  return sms;
+}
+
+// Whether tensor maps take the layout: 16-byte addresses and strides, w dense in k or n.
+bool tensor_form(const ProductArgs& A) {
+  const uintptr_t bits = reinterpret_cast<uintptr_t>(A.x) | reinterpret_cast<uintptr_t>(A.w) | reinterpret_cast<uintptr_t>(A.out);
+  if (bits & 15) return false;
+  const bool k_major = A.w_k == 1, n_major = A.w_n == 1;
+  if (!k_major && !n_major) return false;
+  const int64_t w_row = k_major ? A.w_n : A.w_k;
+  const int64_t rows[] = {A.tokens, A.tokens, k_major ? A.n_dim : A.k_dim}, row[] = {A.x_tok, A.out_tok, w_row};
+  for (int i = 0; i < 3; ++i)
+    if (rows[i] > 1 && (!mappable_stride(row[i]) || row[i] == 0)) return false;
+  if (A.heads > 1 && (!mappable_stride(A.x_head) || !mappable_stride(A.w_head) || !mappable_stride(A.out_head) || A.out_head == 0))
+    return false;
+  return tensor_map_encoder() != nullptr;
+}
+
+template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream_t st) {
+  TensorArgs P = {};
+  const int sms = sm_count();
+  P.chunks = (A.k_dim + kChunk - 1) / kChunk;
+  P.m_tiles = (A.tokens + kRows - 1) / kRows;
+  // the widest tile whose weights fit and that still gives four of five SMs a unit: wide tiles read x
+  // less often, narrow ones spread few tokens over the SMs
+  P.nt = 64;
+  for (int nt : {256, 128}) {
+    if (uint32_t(P.chunks) * nt * 128u > kMaxWeights || nt >= 2 * A.n_dim) continue;
+    if (int64_t(A.heads) * ((A.n_dim + nt - 1) / nt) * P.m_tiles * 5 >= int64_t(sms) * 4) {
+      P.nt = nt;
+      break;
+    }
+  }
+  P.n_tiles = (A.n_dim + P.nt - 1) / P.nt;
+  P.units = int64_t(A.heads) * P.n_tiles * P.m_tiles;
+  const uint32_t fixed = 1024 + kOffData + uint32_t(P.chunks) * P.nt * 128u + 8 * kBlockBytes;
+  P.slots = int((227u * 1024u - fixed) / kXSlot);
+  if (P.slots > kMaxSlots) P.slots = kMaxSlots;
+  const uint32_t smem = fixed + P.slots * kXSlot;
+  const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  P.w_k_major = A.w_k == 1;
+  P.x_by_head = A.x_head != 0, P.w_by_head = A.w_head != 0, P.out_by_head = 1;
+  if (A.heads == 1) P.x_by_head = P.w_by_head = P.out_by_head = 0;
+  P.err = A.err, P.tokens = A.tokens, P.n_dim = A.n_dim;
+  const bool maps = encode_heads_map(&P.x, bf16, A.x, A.tokens, A.x_tok, A.heads, A.x_head, A.k_dim, 64, kRows) &&
+                    (P.w_k_major ? encode_heads_map(&P.w, bf16, A.w, A.n_dim, A.w_n, A.heads, A.w_head, A.k_dim, 64, P.nt)
+                                 : encode_heads_map(&P.w, bf16, A.w, A.k_dim, A.w_k, A.heads, A.w_head, A.n_dim, 64, 64)) &&
+                    encode_heads_map(&P.out, bf16, A.out, A.tokens, A.out_tok, A.heads, A.out_head, A.n_dim, 64, 32);
+  if (!maps) return cudaErrorInvalidValue;
+  const cudaError_t e = cudaFuncSetAttribute(head_product_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  if (e != cudaSuccess) return e;
+  const unsigned grid = unsigned(P.units < sms ? P.units : sms);
+  head_product_kernel<T><<<grid, kThreads, smem, st>>>(P);
+  return cudaGetLastError();
+}
 
 // The plain form, for any strides: a block a tile of 64 tokens x 64 outputs of
 // one head, 16 k at a time through shared memory, 4 x 4 sums a thread.
@@ -74,7 +331,7 @@ template <typename T> cudaError_t launch_plain(const ProductArgs& A, cudaStream_
 extern "C" int mla_head_product(const void* x, int64_t x_tok_stride, int64_t x_head_stride, const void* w,
                                 int64_t w_head_stride, int64_t w_k_stride, int64_t w_n_stride, void* out,
                                 int64_t out_tok_stride, int64_t out_head_stride, int64_t num_tokens, int num_heads,
-                                int k_dim, int n_dim, int dtype, void* stream) {
+                                int k_dim, int n_dim, int dtype, uint32_t* err, void* stream) {
   using namespace mtv;
   if (num_tokens < 0 || num_tokens > INT32_MAX || num_heads < 0 || num_heads > MTV_MAX_HEADS || k_dim < 1 ||
       k_dim > MTV_MAX_HEAD_DIM || n_dim < 1 || n_dim > MTV_MAX_HEAD_DIM ||
@@ -84,9 +341,12 @@ extern "C" int mla_head_product(const void* x, int64_t x_tok_stride, int64_t x_h
   if (!x || !w || !out) return MTV_E_NULL_POINTER;
   if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(out)) & 1)
     return MTV_E_BAD_ARGUMENT;
-  const ProductArgs A{x,          w,          out,        x_tok_stride,   x_head_stride,   w_head_stride,
-                      w_k_stride, w_n_stride, out_tok_stride, out_head_stride, num_tokens, num_heads, k_dim, n_dim};
+  const ProductArgs A{x, w, out, err, x_tok_stride, x_head_stride, w_head_stride, w_k_stride, w_n_stride, out_tok_stride,
+                      out_head_stride, num_tokens, num_heads, k_dim, n_dim};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == MTV_DTYPE_BF16 ? launch_plain<__nv_bfloat16>(A, st) : launch_plain<__half>(A, st);
+  const bool bf16 = dtype == MTV_DTYPE_BF16;
+  cudaError_t e;
+  if (tensor_form(A)) e = bf16 ? launch_tensor<__nv_bfloat16>(A, st) : launch_tensor<__half>(A, st);
+  else e = bf16 ? launch_plain<__nv_bfloat16>(A, st) : launch_plain<__half>(A, st);
   return e == cudaSuccess ? MTV_OK : MTV_E_CUDA;
 }

@@ -39,6 +39,7 @@
 
 #include "mla_layer_ops.h"
 #include "mtv_internal.cuh"
+#include "pipeline.cuh"
 #include "tc_ptx.cuh"
 #include "tma.cuh"
 #include "vec_io.cuh"
@@ -63,7 +64,6 @@ constexpr uint32_t kSmem = kOffCtl + 16 + 1024;  // + slack for 1 KB alignment
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
 constexpr float kRescaleLog2 = 8.f;
-constexpr long long kWaitCycles = 1ll << 31;
 
 struct PrefillArgs {
   CUtensorMap q, k_nope, k_rope, v;
@@ -77,11 +77,6 @@ struct PrefillArgs {
   float scale;
   int bs, heads, causal, nsplit, q_blocks;
   int q_by_head, k_by_head, v_by_head;  // 0: one map for all heads
-};
-
-struct Ctl {
-  uint32_t tmem;
-  volatile int abort;
 };
 
 struct PrefillReq {
@@ -104,32 +99,6 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
-}
-
-// False when the wait gave up or another one has.
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
-    if (ctl->abort) return false;
-    if (clock64() - t0 > kWaitCycles) {
-      ctl->abort = 1;
-      if (err) atomicOr(err, MTV_DEVERR_TIMEOUT);
-      return false;
-    }
-  }
-  return true;
-}
-__device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err) {
-  return mbar_try_wait(bar, parity) || wait_slow(bar, parity, ctl, err);
-}
-// The same for what has to land before the block may end: ignores the flag.
-__device__ __noinline__ void drain(uint32_t bar, uint32_t parity, uint32_t* err) {
-  const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity))
-    if (clock64() - t0 > kWaitCycles) {
-      if (err) atomicOr(err, MTV_DEVERR_TIMEOUT);
-      return;
-    }
 }
 
 template <typename T>
@@ -222,9 +191,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t id_qk = kBf16 ? idesc_bf16_f32(128, 128, 0, 0) : idesc_fp16_f32(128, 128, 0, 0);
     constexpr uint32_t id_pv = kBf16 ? idesc_bf16_f32(128, 128, 0, 1) : idesc_fp16_f32(128, 128, 0, 1);
-    auto add = [](uint64_t d, uint32_t off) -> uint64_t {  // only the start address changes, without a carry
-      return (d & 0xFFFFFFFF00000000ull) | uint64_t(uint32_t(d) + (off >> 4));
-    };
     auto slot_at = [&](int item) { return base + kOffRing + uint32_t(item % kSlots) * kSlot; };
     auto arrived = [&](uint32_t b, uint32_t parity) {
       return __all_sync(0xffffffffu, wait_for(b, parity, ctl, A.err)) != 0;
@@ -239,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           const uint64_t a = smem_desc(base + s * kQStage + c * kSlot, 16, 1024, kSwizzle128B);
           const uint64_t b = smem_desc(slot_at(item), 16, 1024, kSwizzle128B);
 #pragma unroll
-          for (int k = 0; k < 4; ++k) mma_ss(tmem + kTmemS + 128 * s, add(a, 32 * k), add(b, 32 * k), id_qk, c + k > 0);
+          for (int k = 0; k < 4; ++k) mma_ss(tmem + kTmemS + 128 * s, desc_add(a, 32 * k), desc_add(b, 32 * k), id_qk, c + k > 0);
           if (last) mma_commit(bar(B_EMPTY + item % kSlots));
         }
       }
@@ -269,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             if (4 * c + k < steps)
-              mma_ts(tmem + kTmemO + 128 * s, tmem + kTmemS + 128 * s + 8 * (4 * c + k), add(b, 2048 * k), id_pv,
+              mma_ts(tmem + kTmemO + 128 * s, tmem + kTmemS + 128 * s + 8 * (4 * c + k), desc_add(b, 2048 * k), id_pv,
                      j > 0 || c + k > 0);
           if (last) mma_commit(bar(B_EMPTY + (5 * j + 3 + c) % kSlots));
         }

@@ -95,7 +95,7 @@ def test_prefill_workspace_refusals(lib):
 # ------------------------------------------------------- refusals of the ABI
 
 PRODUCT = dict(x=FAKE, x_tok=1024, x_head=128, w=FAKE, w_head=65536, w_k=512, w_n=1, out=FAKE, out_tok=36864, out_head=576,
-               tokens=4, heads=8, k=128, n=512, dtype=0)
+               tokens=4, heads=8, k=128, n=512, dtype=0, err=None)
 
 
 def product(lib, **kw):
