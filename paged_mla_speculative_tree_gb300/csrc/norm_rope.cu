@@ -114,13 +114,14 @@ __global__ void __launch_bounds__(kPlainThreads) norm_rope_plain_kernel(const No
   }
 }
 
-// The vector form: a block a token; eight lanes a head, each with every eighth
-// 16-byte unit of it, so that the sum of squares takes three shuffles and a head
-// is read once (with the half layout a rotated unit's partner once more, from the
-// same lines); one more warp has the latent row.  Every load of the token is
-// issued before the angles are computed and before it is known to be valid.
-// Its conditions (whole 16-byte units everywhere, at most 64 a head) are checked
-// by the launch; the plain form above takes what is left.
+// The vector form: a block a token, eight lanes a head, in 16-byte units: of the
+// plain part every eighth unit a lane, of the rotated part every eighth unit or,
+// in the half layout, every eighth pair of units half a part apart, so that a
+// head is read once, its sum of squares takes three shuffles, and a lane turns
+// what it holds.  One more warp has the latent row.  Every load of the first 32
+// heads is issued before the angles are computed and before the token is known
+// to be valid.  Its conditions (whole units everywhere, at most NN and NR units
+// a lane) are checked by the launch; the plain form above takes what is left.
 constexpr int kVecThreads = 288, kGroups = 32;
 
 template <int N> __device__ __forceinline__ void load_floats(const float* from, float* to) {
@@ -137,75 +138,55 @@ template <int N> __device__ __forceinline__ void load_floats(const float* from, 
   }
 }
 
-// One unit of a rotated part, turned: x its values, p those of its partner half a
-// part away (half layout).
+// 2 V values of a rotated part, turned: two units half a part apart (half
+// layout), or one and nothing.
 template <int V, bool kHalf>
-__device__ __forceinline__ void turn_unit(const float* x, const float* p, int unit, int units, const float* cos_s,
-                                          const float* sin_s, float* y) {
-  if constexpr (kHalf) {
-    const bool second = unit >= units / 2;
-    const int pair = (second ? unit - units / 2 : unit) * V;
-    float c[V], s[V];
-    load_floats<V>(cos_s + pair, c);
-    load_floats<V>(sin_s + pair, s);
+__device__ __forceinline__ void turn_unit(float* x, int unit, const float* cos_s, const float* sin_s) {
+  constexpr int P = kHalf ? V : V / 2;
+  float c[P], s[P];
+  load_floats<P>(cos_s + unit * P, c);
+  load_floats<P>(sin_s + unit * P, s);
 #pragma unroll
-    for (int i = 0; i < V; ++i) y[i] = second ? p[i] * s[i] + x[i] * c[i] : x[i] * c[i] - p[i] * s[i];
-  } else {
-    float c[V / 2], s[V / 2];
-    load_floats<V / 2>(cos_s + unit * (V / 2), c);
-    load_floats<V / 2>(sin_s + unit * (V / 2), s);
-#pragma unroll
-    for (int i = 0; i < V / 2; ++i) {
-      y[2 * i] = x[2 * i] * c[i] - x[2 * i + 1] * s[i];
-      y[2 * i + 1] = x[2 * i] * s[i] + x[2 * i + 1] * c[i];
-    }
+  for (int i = 0; i < P; ++i) {
+    const int j = kHalf ? i : 2 * i, k = kHalf ? i + V : 2 * i + 1;
+    const float x1 = x[j], x2 = x[k];
+    x[j] = x1 * c[i] - x2 * s[i];
+    x[k] = x1 * s[i] + x2 * c[i];
   }
 }
 
 __device__ __forceinline__ uint4 load16(const void* p) { return *static_cast<const uint4*>(p); }
 
-// NI: units a lane holds of a head.
-template <typename T, bool kHalf, int NI>
-__global__ void __launch_bounds__(kVecThreads) norm_rope_vec_kernel(const NormArgs A) {
-  constexpr int V = 16 / int(sizeof(T));
-  constexpr int kHeadsAtOnce = NI <= 3 ? 2 : 1;
+// NN, NR: units of the plain part and units (half layout: pairs of them) of the
+// rotated part that a lane may hold.
+template <typename T, bool kHalf, int NN, int NR>
+__global__ void __launch_bounds__(kVecThreads, NN <= 2 ? 3 : 1) norm_rope_vec_kernel(const NormArgs A) {
+  constexpr int V = 16 / int(sizeof(T)), M = kHalf ? 2 : 1;
   constexpr int kLatentUnits = kDLat / V / 32;
   __shared__ __align__(16) float cos_s[MTV_MAX_ROPE_DIM / 2], sin_s[MTV_MAX_ROPE_DIM / 2];
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, l = tid & 7, group = tid >> 3;
   const bool queries = A.q_in && tid < kGroups * 8, latents = A.pool && tid >= kGroups * 8;
-  const int rope_units = A.rope_dim / V, nope_units = A.nope_dim / V;
-  const int skip = A.q_weight ? 0 : nope_units, count = nope_units + rope_units - skip;  // units read
-  auto partner = [&](int unit) {  // of a unit of the rotated part
-    return unit >= rope_units / 2 ? unit - rope_units / 2 : unit + rope_units / 2;
-  };
+  const int turned = A.rope_dim / V / M, apart = A.rope_dim / 2;  // units or pairs of a rotated part
+  const int plain = A.q_weight ? A.nope_dim / V : 0;              // units of the plain part, where it is read
 
   const T* q = static_cast<const T*>(A.q_in) + t * A.q_tok;
-  uint4 x[kHeadsAtOnce][NI], px[kHeadsAtOnce][NI], w[NI], pw[NI];
-  auto load_heads = [&](int h0) {
+  const T* weight = static_cast<const T*>(A.q_weight);
+  uint4 xn[NN > 0 ? NN : 1], xr[NR][M];
+  auto load_head = [&](const T* head) {
 #pragma unroll
-    for (int e = 0; e < kHeadsAtOnce; ++e)
+    for (int i = 0; i < NN; ++i)
+      if (l + 8 * i < plain) xn[i] = load16(head + (l + 8 * i) * V);
 #pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int h = h0 + e * kGroups, u = l + 8 * i;
-        if (h >= A.num_heads || u >= count) continue;
-        const T* head = q + h * A.q_head;
-        x[e][i] = load16(head + (skip + u) * V);
-        if (kHalf && skip + u >= nope_units) px[e][i] = load16(head + (nope_units + partner(skip + u - nope_units)) * V);
-      }
+    for (int i = 0; i < NR; ++i)
+#pragma unroll
+      for (int m = 0; m < M; ++m)
+        if (l + 8 * i < turned) xr[i][m] = load16(head + A.nope_dim + (l + 8 * i) * V + m * apart);
   };
-  uint4 c[kLatentUnits], cw[kLatentUnits], k = make_uint4(0, 0, 0, 0), pk = k;
+  uint4 c[kLatentUnits], cw[kLatentUnits], k[M];
   int64_t slot = -1;
   if (queries) {
-    load_heads(group);
-    if (A.q_weight)
-#pragma unroll
-      for (int i = 0; i < NI; ++i) {
-        const int u = l + 8 * i;
-        if (u >= count) continue;
-        w[i] = load16(static_cast<const T*>(A.q_weight) + u * V);
-        if (kHalf && u >= nope_units) pw[i] = load16(static_cast<const T*>(A.q_weight) + (nope_units + partner(u - nope_units)) * V);
-      }
+    if (group < A.num_heads) load_head(q + group * A.q_head);
   } else if (latents) {
     slot = A.out_cache_loc[t];
 #pragma unroll
@@ -213,10 +194,9 @@ __global__ void __launch_bounds__(kVecThreads) norm_rope_vec_kernel(const NormAr
       c[i] = load16(static_cast<const T*>(A.c_in) + t * A.c_tok + (lane + 32 * i) * V);
       if (A.c_weight) cw[i] = load16(static_cast<const T*>(A.c_weight) + (lane + 32 * i) * V);
     }
-    if (lane < rope_units) {
-      k = load16(static_cast<const T*>(A.k_in) + t * A.k_tok + lane * V);
-      if (kHalf) pk = load16(static_cast<const T*>(A.k_in) + t * A.k_tok + partner(lane) * V);
-    }
+#pragma unroll
+    for (int m = 0; m < M; ++m)
+      if (lane < turned) k[m] = load16(static_cast<const T*>(A.k_in) + t * A.k_tok + lane * V + m * apart);
   }
   const int64_t valid = A.num_valid ? *A.num_valid : INT64_MAX;
   angles(A, t, tid, kVecThreads, cos_s, sin_s);
@@ -224,54 +204,60 @@ __global__ void __launch_bounds__(kVecThreads) norm_rope_vec_kernel(const NormAr
   if (t >= valid) return;
 
   if (queries) {
-    for (int h0 = group; h0 - group < A.num_heads; h0 += kHeadsAtOnce * kGroups) {  // whole warps stay together
-      if (h0 != group) load_heads(h0);
-      __syncwarp();  // outputs may be the inputs: all of a head is read before any of it is written
+    for (int h = group; h - group < A.num_heads; h += kGroups) {  // whole warps stay together
+      const bool mine = h < A.num_heads;
+      if (h != group && mine) load_head(q + h * A.q_head);
+      float r = 1.f;
+      if (weight) {
+        float sum = 0.f;
+        auto add = [&](const uint4& u) {
+          float f[V];
+          expand<T>(u, f);
 #pragma unroll
-      for (int e = 0; e < kHeadsAtOnce; ++e) {
-        const int h = h0 + e * kGroups;
-        float r = 1.f;
-        if (A.q_weight) {
-          float sum = 0.f;
+          for (int d = 0; d < V; ++d) sum = fmaf(f[d], f[d], sum);
+        };
 #pragma unroll
-          for (int i = 0; i < NI; ++i) {
-            if (l + 8 * i >= count || h >= A.num_heads) continue;
-            float f[V];
-            expand<T>(x[e][i], f);
+        for (int i = 0; i < NN; ++i)
+          if (mine && l + 8 * i < plain) add(xn[i]);
 #pragma unroll
-            for (int d = 0; d < V; ++d) sum = fmaf(f[d], f[d], sum);
-          }
+        for (int i = 0; i < NR; ++i)
 #pragma unroll
-          for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-          r = rsqrtf(sum / float(count * V) + A.eps);
+          for (int m = 0; m < M; ++m)
+            if (mine && l + 8 * i < turned) add(xr[i][m]);
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        r = rsqrtf(sum / float(A.nope_dim + A.rope_dim) + A.eps);
+      }
+      if (!mine) continue;
+      // a lane writes what it has read, so outputs may be the inputs
+      auto scale = [&](float* f, int at) {  // the weights are in L1 from the blocks before
+        float g[V];
+        expand<T>(load16(weight + at), g);
+#pragma unroll
+        for (int d = 0; d < V; ++d) f[d] = f[d] * r * g[d];
+      };
+      T* nope = static_cast<T*>(A.q_nope) + t * A.nope_tok + h * A.nope_head;
+      T* rope = static_cast<T*>(A.q_rope) + t * A.rope_tok + h * A.rope_head;
+#pragma unroll
+      for (int i = 0; i < NN; ++i) {
+        if (l + 8 * i >= plain) continue;
+        float f[V];
+        expand<T>(xn[i], f);
+        scale(f, (l + 8 * i) * V);
+        *reinterpret_cast<uint4*>(nope + (l + 8 * i) * V) = pack<T>(f);
+      }
+#pragma unroll
+      for (int i = 0; i < NR; ++i) {
+        if (l + 8 * i >= turned) continue;
+        float f[2 * V];
+#pragma unroll
+        for (int m = 0; m < M; ++m) {
+          expand<T>(xr[i][m], f + m * V);
+          if (weight) scale(f + m * V, A.nope_dim + (l + 8 * i) * V + m * apart);
         }
-        if (h >= A.num_heads) continue;
+        turn_unit<V, kHalf>(f, l + 8 * i, cos_s, sin_s);
 #pragma unroll
-        for (int i = 0; i < NI; ++i) {
-          const int u = skip + l + 8 * i;
-          if (u >= skip + count) continue;
-          float f[V], p[V], y[V], g[V];
-          expand<T>(x[e][i], f);
-          if (A.q_weight) {
-            expand<T>(w[i], g);
-#pragma unroll
-            for (int d = 0; d < V; ++d) f[d] = f[d] * r * g[d];
-          }
-          if (u < nope_units) {
-            *reinterpret_cast<uint4*>(static_cast<T*>(A.q_nope) + t * A.nope_tok + h * A.nope_head + u * V) = pack<T>(f);
-            continue;
-          }
-          if constexpr (kHalf) {
-            expand<T>(px[e][i], p);
-            if (A.q_weight) {
-              expand<T>(pw[i], g);
-#pragma unroll
-              for (int d = 0; d < V; ++d) p[d] = p[d] * r * g[d];
-            }
-          }
-          turn_unit<V, kHalf>(f, p, u - nope_units, rope_units, cos_s, sin_s, y);
-          *reinterpret_cast<uint4*>(static_cast<T*>(A.q_rope) + t * A.rope_tok + h * A.rope_head + (u - nope_units) * V) = pack<T>(y);
-        }
+        for (int m = 0; m < M; ++m) *reinterpret_cast<uint4*>(rope + (l + 8 * i) * V + m * apart) = pack<T>(f + m * V);
       }
     }
     return;
@@ -305,17 +291,18 @@ __global__ void __launch_bounds__(kVecThreads) norm_rope_vec_kernel(const NormAr
     }
     store_bf16<V>(row + (lane + 32 * i) * V, f);
   }
-  if (lane < rope_units) {
-    float f[V], p[V], y[V];
-    expand<T>(k, f);
-    if constexpr (kHalf) expand<T>(pk, p);
-    turn_unit<V, kHalf>(f, p, lane, rope_units, cos_s, sin_s, y);
-    store_bf16<V>(row + kDLat + lane * V, y);
+  if (lane < turned) {
+    float f[2 * V];
+#pragma unroll
+    for (int m = 0; m < M; ++m) expand<T>(k[m], f + m * V);
+    turn_unit<V, kHalf>(f, lane, cos_s, sin_s);
+#pragma unroll
+    for (int m = 0; m < M; ++m) store_bf16<V>(row + kDLat + lane * V + m * apart, f + m * V);
   }
 }
 
-// Units a lane of the vector form holds, or 0 where it does not take the layout.
-template <typename T> int vector_units(const NormArgs& A) {
+// Whether every address that the vector form touches is 16-byte aligned.
+template <typename T> bool vector_form(const NormArgs& A) {
   constexpr int64_t v = 16 / int64_t(sizeof(T));
   uint64_t bits = 0;
   auto at = [&](const void* p) { bits |= reinterpret_cast<uintptr_t>(p); };
@@ -327,18 +314,18 @@ template <typename T> int vector_units(const NormArgs& A) {
     stride(A.nope_dim);
   }
   if (A.pool) at(A.c_in), at(A.c_weight), at(A.k_in), stride(A.c_tok), stride(A.k_tok);
-  if ((bits & 15) || A.rope_dim % (2 * v) || A.num_heads > INT32_MAX / 2) return 0;
-  const int64_t units = A.q_in ? (A.rope_dim + (A.q_weight ? A.nope_dim : 0)) / v : 1;
-  return units <= 64 ? int((units + 7) / 8) : 0;
+  return (bits & 15) == 0 && A.rope_dim % (2 * v) == 0 && A.num_heads <= INT32_MAX / 2;
 }
 
 template <typename T, bool kHalf> cudaError_t launch_norm_layout(const NormArgs& A, int64_t tokens, cudaStream_t st) {
-  const int units = vector_units<T>(A);
+  constexpr int v = 16 / int(sizeof(T));
   const unsigned grid = unsigned(tokens);
-  if (units == 0) norm_rope_plain_kernel<T, kHalf><<<grid, kPlainThreads, 0, st>>>(A);
-  else if (units == 1) norm_rope_vec_kernel<T, kHalf, 1><<<grid, kVecThreads, 0, st>>>(A);
-  else if (units <= 3) norm_rope_vec_kernel<T, kHalf, 3><<<grid, kVecThreads, 0, st>>>(A);
-  else norm_rope_vec_kernel<T, kHalf, 8><<<grid, kVecThreads, 0, st>>>(A);
+  const int plain = A.q_weight ? (A.nope_dim / v + 7) / 8 : 0, turned = (A.rope_dim / v / (kHalf ? 2 : 1) + 7) / 8;
+  if (!vector_form<T>(A) || plain > 8 || turned > 2) norm_rope_plain_kernel<T, kHalf><<<grid, kPlainThreads, 0, st>>>(A);
+  else if (plain == 0) norm_rope_vec_kernel<T, kHalf, 0, 2><<<grid, kVecThreads, 0, st>>>(A);
+  else if (plain <= 2 && turned == 1) norm_rope_vec_kernel<T, kHalf, 2, 1><<<grid, kVecThreads, 0, st>>>(A);
+  else if (plain <= 4) norm_rope_vec_kernel<T, kHalf, 4, 2><<<grid, kVecThreads, 0, st>>>(A);
+  else norm_rope_vec_kernel<T, kHalf, 8, 2><<<grid, kVecThreads, 0, st>>>(A);
   return cudaGetLastError();
 }
 
