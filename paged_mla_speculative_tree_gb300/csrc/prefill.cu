@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (base - raw) + kOffCtl);
   auto bar = [&](int i) { return base + kOffBars + 8u * uint32_t(i); };
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
 
   // blocks of a head side by side, the longest first; then splits, heads, requests
   unsigned id = blockIdx.x;
@@ -201,7 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         const int item = 5 * j + c;
         if (!landed(item)) return false;
         tc_fence_after();
-        if (lane == 0) {
+        if (elect_one()) {
           const uint64_t a = smem_desc(base + s * kQStage + c * kSlot, 16, 1024, kSwizzle128B);
           const uint64_t b = smem_desc(slot_at(item), 16, 1024, kSwizzle128B);
 #pragma unroll
@@ -209,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           if (last) mma_commit(bar(B_EMPTY + item % kSlots));
         }
       }
-      if (lane == 0) mma_commit(bar(B_S + s));
+      if (elect_one()) mma_commit(bar(B_S + s));
       return true;
     };
     auto pv = [&](int s, int j, bool first, bool last, bool end) -> bool {  // O_s += P_s V(j)
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       if (!arrived(bar(B_P + s), j & 1)) return false;
       tc_fence_after();
-      if (lane == 0) {
+      if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < 2; ++c) {
           const uint64_t b = smem_desc(slot_at(5 * j + 3 + c), kSlot / 2, 1024, kSwizzle128B);
@@ -251,7 +251,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (j < T0) ok = pv(0, j, true, j >= T1, j + 1 == T0) && (j + 1 >= T0 || qk(0, j + 1, j + 1 >= T1));
       if (ok && j < T1) ok = pv(1, j, j >= T0, true, j + 1 == T1) && (j + 1 >= T1 || qk(1, j + 1, true));
     }
-    if (lane == 0 && TN > 0) {  // every MMA issued has run once this arrives
+    if (TN > 0 && elect_one()) {  // every MMA issued has run once this arrives
       mma_commit(bar(B_FIN));
       drain(bar(B_FIN), 0, A.err);
     }
