@@ -8,18 +8,19 @@
 //   S = Q K^T      12 k-steps of 16, both operands in shared memory, S in TMEM
 //   P = 2^(S c - m c) in the input type, over S's columns in TMEM
 //   O += P V       8 k-steps, P from TMEM, V as an MN-major operand
-// Roles: one warp issues the MMAs, one the TMA copies, and four warps a stage
-// the softmax, a thread a row.  While one stage's softmax works, the tensor
-// core computes the other's O += P V and next S, so that the order of issue is
-// PV0(j) QK0(j+1) PV1(j) QK1(j+1) PV0(j+1) ...  MMAs of one thread run in
+// Roles: a warp a stage issues the MMAs, one the TMA copies, and four warps a
+// stage the softmax, a thread a row.  While one stage's softmax works, the tensor
+// core computes the other's O += P V and next S.  MMAs of one thread run in
 // order: S(j+1) may overwrite P(j) without a wait, and S(j+1) being there says
-// that O holds everything up to j.
+// that O holds everything up to j.  (One warp issuing for both stages was the
+// bottleneck: with its waits and commits it needed 930 cycles a stage and tile
+// beside about 50 an MMA, of which there are 20.)
 //
 // Shared memory: Q 96 KB and a ring of eight 16 KB slots that K (three slots of
 // 64 dims a tile) and V (two of 64 keys) pass through in the order of their
-// use.  Every slot is freed by its own commit, so a copy has two thirds of a
-// tile's time (about 1,800 of 2,600 cycles at full rate) from its slot's
-// release to its use; whole tiles of K and V do not fit twice beside Q.
+// use: K(0) V(0) K(1) V(1) ...  A copy has half of a tile's time (about 1,300 of
+// 2,600 cycles at full rate) from its slot's release to its use; whole tiles of
+// K and V do not fit twice beside Q.
 // TMEM: S0, S1, O0, O1 of 128 columns each.
 //
 // The maximum that scores refer to moves only when a row's scores grow by more
@@ -51,13 +52,13 @@ using namespace ptx;
 
 constexpr int kNope = 128, kRope = 64, kQK = kNope + kRope, kV = 128;
 constexpr int kStageRows = 128, kBlockRows = 2 * kStageRows, kKeys = 128;
-constexpr int kThreads = 320;  // 4 + 4 softmax warps, MMA, TMA
+constexpr int kThreads = 352;  // 4 + 4 softmax warps, 2 for the MMAs, 1 for the copies
 constexpr uint32_t kSlot = 16384;
 constexpr int kSlots = 8;
 constexpr uint32_t kQStage = 3 * kSlot, kOffRing = 2 * kQStage, kOffBars = kOffRing + kSlots * kSlot;
+// K and V tile j use the barriers j & 1; both stages release every tile
 enum : int {
-  B_Q = 0, B_FULL = 2, B_EMPTY = B_FULL + kSlots, B_S = B_EMPTY + kSlots, B_P = B_S + 2, B_O = B_P + 2, B_FIN = B_O + 2,
-  B_COUNT
+  B_Q = 0, B_KFULL = 2, B_VFULL = 4, B_KFREE = 6, B_VFREE = 8, B_S = 10, B_P = 12, B_O = 14, B_FIN = 16, B_COUNT = 18
 };
 constexpr uint32_t kOffCtl = kOffBars + 8 * B_COUNT;
 constexpr uint32_t kSmem = kOffCtl + 16 + 1024;  // + slack for 1 KB alignment
@@ -135,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const int T0 = mine(tiles0), T1 = mine(tiles1), TN = max(T0, T1);
 
   if (tid == 0) {
-    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i == B_P || i == B_P + 1 ? 4 : 1);
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_KFREE && i < B_S ? 2 : i == B_P || i == B_P + 1 ? 4 : 1);
     ctl->abort = 0;
     fence_mbar_init_cluster();
   }
@@ -148,7 +149,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
 
-  if (warp == 9) {
+  auto slot_at = [&](int item) { return base + kOffRing + uint32_t(item % kSlots) * kSlot; };
+  if (warp == 10) {
     // ------------------------------------------------------------- copies
     if (lane == 0 && TN > 0) {
       const int qh = A.q_by_head ? h : 0, kh = A.k_by_head ? h : 0, vh = A.v_by_head ? h : 0;
@@ -157,103 +159,116 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         for (int c = 0; c < 3; ++c)
           tma_load_3d(base + s * kQStage + c * kSlot, &A.q, 64 * c, qh, int(R.q0 + row0 + s * kStageRows), bar(B_Q + s));
       };
-      int item = 0;
       bool ok = true;
-      auto slot_for = [&]() -> bool {  // the next item's slot is free; its barrier expects the bytes
-        const int slot = item % kSlots;
-        if (item >= kSlots) ok = wait_for(bar(B_EMPTY + slot), ((item / kSlots) - 1) & 1, ctl, A.err);
-        if (ok) mbar_arrive_expect_tx(bar(B_FULL + slot), kSlot);
-        return ok;
-      };
+      int k_asked = 0, v_asked = 0;
       if (T0 > 0) load_q(0);
-      for (int j = 0; j < TN && ok; ++j) {
+      for (int j = 0; j < TN; ++j) {
+        // slots in the order of their use: K(j)'s first was K(j - 2)'s last, its others V(j - 2)'s, V(j)'s K(j - 1)'s first
         const int row = int(R.k0) + (begin + j) * kKeys;
-        for (int c = 0; c < 3 && slot_for(); ++c, ++item) {
-          const uint32_t dst = base + kOffRing + (item % kSlots) * kSlot, full = bar(B_FULL + item % kSlots);
-          if (c < 2) tma_load_3d(dst, &A.k_nope, 64 * c, kh, row, full);
-          else tma_load_3d(dst, &A.k_rope, 0, 0, row, full);
-        }
+        if (j >= 2) ok = wait_for(bar(B_KFREE + (j & 1)), uint32_t(j / 2 - 1) & 1, ctl, A.err) &&
+                         wait_for(bar(B_VFREE + (j & 1)), uint32_t(j / 2 - 1) & 1, ctl, A.err);
+        if (!ok) break;
+        const uint32_t kf = bar(B_KFULL + (j & 1)), vf = bar(B_VFULL + (j & 1));
+        mbar_arrive_expect_tx(kf, 3 * kSlot);
+        tma_load_3d(slot_at(5 * j), &A.k_nope, 0, kh, row, kf);
+        tma_load_3d(slot_at(5 * j + 1), &A.k_nope, 64, kh, row, kf);
+        tma_load_3d(slot_at(5 * j + 2), &A.k_rope, 0, 0, row, kf);
+        ++k_asked;
         if (j == 0 && T1 > 0) load_q(1);
-        for (int c = 0; c < 2 && ok && slot_for(); ++c, ++item) {
-          const uint32_t dst = base + kOffRing + (item % kSlots) * kSlot, full = bar(B_FULL + item % kSlots);
-          tma_load_3d(dst, &A.v, 0, vh, row + 64 * c, full);
-          tma_load_3d(dst + kSlot / 2, &A.v, 64, vh, row + 64 * c, full);
+        if (j >= 1) ok = wait_for(bar(B_KFREE + ((j - 1) & 1)), uint32_t((j - 1) / 2) & 1, ctl, A.err);
+        if (!ok) break;
+        mbar_arrive_expect_tx(vf, 2 * kSlot);
+        for (int c = 0; c < 2; ++c) {
+          tma_load_3d(slot_at(5 * j + 3 + c), &A.v, 0, vh, row + 64 * c, vf);
+          tma_load_3d(slot_at(5 * j + 3 + c) + kSlot / 2, &A.v, 64, vh, row + 64 * c, vf);
         }
+        ++v_asked;
       }
       // what was asked for lands before the block ends, read or not (a second stage's Q is asked for with the first tile)
       if (T0 > 0) drain(bar(B_Q), 0, A.err);
-      if (T1 > 0 && item >= 3) drain(bar(B_Q + 1), 0, A.err);
-      for (int i = max(0, item - kSlots); i < item; ++i) drain(bar(B_FULL + i % kSlots), (i / kSlots) & 1, A.err);
+      if (T1 > 0) drain(bar(B_Q + 1), 0, A.err);
+      for (int j = max(0, k_asked - 2); j < k_asked; ++j) drain(bar(B_KFULL + (j & 1)), uint32_t(j / 2) & 1, A.err);
+      for (int j = max(0, v_asked - 2); j < v_asked; ++j) drain(bar(B_VFULL + (j & 1)), uint32_t(j / 2) & 1, A.err);
     }
     __syncwarp();
-  } else if (warp == 8) {
+  } else if (warp >= 8) {
     // ------------------------------------------------------------- products
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t id_qk = kBf16 ? idesc_bf16_f32(128, 128, 0, 0) : idesc_fp16_f32(128, 128, 0, 0);
     constexpr uint32_t id_pv = kBf16 ? idesc_bf16_f32(128, 128, 0, 1) : idesc_fp16_f32(128, 128, 0, 1);
-    auto slot_at = [&](int item) { return base + kOffRing + uint32_t(item % kSlots) * kSlot; };
-    auto arrived = [&](uint32_t b, uint32_t parity) {
-      return __all_sync(0xffffffffu, wait_for(b, parity, ctl, A.err)) != 0;
+    const int s = warp - 8, Ts = s ? T1 : T0;
+    const uint32_t tmem_s = tmem + kTmemS + 128 * s, tmem_o = tmem + kTmemO + 128 * s;
+    auto arrived = [&](int b, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, A.err)) != 0;
     };
-    auto landed = [&](int item) { return arrived(bar(B_FULL + item % kSlots), (item / kSlots) & 1); };
-    auto qk = [&](int s, int j, bool last) -> bool {  // S_s = Q_s K(j)^T; `last` frees the tile's slots
-      for (int c = 0; c < 3; ++c) {
-        const int item = 5 * j + c;
-        if (!landed(item)) return false;
-        tc_fence_after();
-        if (elect_one()) {
-          const uint64_t a = smem_desc(base + s * kQStage + c * kSlot, 16, 1024, kSwizzle128B);
-          const uint64_t b = smem_desc(slot_at(item), 16, 1024, kSwizzle128B);
-#pragma unroll
-          for (int k = 0; k < 4; ++k) mma_ss(tmem + kTmemS + 128 * s, desc_add(a, 32 * k), desc_add(b, 32 * k), id_qk, c + k > 0);
-          if (last) mma_commit(bar(B_EMPTY + item % kSlots));
-        }
-      }
-      if (elect_one()) mma_commit(bar(B_S + s));
-      return true;
-    };
-    auto pv = [&](int s, int j, bool first, bool last, bool end) -> bool {  // O_s += P_s V(j)
-      // in the request's last tile, only k-steps that hold keys; the rows of V
-      // behind the last key may hold anything (another request's, or nobody's)
-      // and are zeroed, since a weight of 0 times NaN is NaN
-      const int keys = int(min(int64_t(kKeys), R.len - int64_t(begin + j) * kKeys)), steps = (keys + 15) / 16;
-      if (!landed(5 * j + 3) || !landed(5 * j + 4)) return false;
-      if (first && keys < 16 * steps) {
-        for (int u = 16 * keys + lane; u < 256 * steps; u += 32) {  // 16-byte units, 16 a row
-          const int key = u / 16, part = u % 16;
-          st_shared_v4(slot_at(5 * j + 3 + key / 64) + (part / 8) * (kSlot / 2) + (key % 64) * 128 + (part % 8) * 16, 0, 0, 0, 0);
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-      }
-      if (!arrived(bar(B_P + s), j & 1)) return false;
+    auto qk = [&](int j) -> bool {  // S = Q K(j)^T
+      if (!arrived(B_KFULL + (j & 1), uint32_t(j / 2) & 1)) return false;
       tc_fence_after();
       if (elect_one()) {
 #pragma unroll
-        for (int c = 0; c < 2; ++c) {
-          const uint64_t b = smem_desc(slot_at(5 * j + 3 + c), kSlot / 2, 1024, kSwizzle128B);
+        for (int c = 0; c < 3; ++c) {
+          const uint64_t a = smem_desc(base + s * kQStage + c * kSlot, 16, 1024, kSwizzle128B);
+          const uint64_t b = smem_desc(slot_at(5 * j + c), 16, 1024, kSwizzle128B);
 #pragma unroll
-          for (int k = 0; k < 4; ++k)
-            if (4 * c + k < steps)
-              mma_ts(tmem + kTmemO + 128 * s, tmem + kTmemS + 128 * s + 8 * (4 * c + k), desc_add(b, 2048 * k), id_pv,
-                     j > 0 || c + k > 0);
-          if (last) mma_commit(bar(B_EMPTY + (5 * j + 3 + c) % kSlots));
+          for (int k = 0; k < 4; ++k) mma_ss(tmem_s, desc_add(a, 32 * k), desc_add(b, 32 * k), id_qk, c + k > 0);
         }
-        if (end) mma_commit(bar(B_O + s));
+        mma_commit(bar(B_S + s));
+        mma_commit(bar(B_KFREE + (j & 1)));
       }
       return true;
     };
-    bool ok = true;
-    if (T0 > 0) ok = arrived(bar(B_Q), 0) && qk(0, 0, T1 == 0);
-    if (ok && T1 > 0) ok = arrived(bar(B_Q + 1), 0) && qk(1, 0, true);
+    auto pv = [&](int j) -> bool {  // O += P V(j)
+      if (!arrived(B_VFULL + (j & 1), uint32_t(j / 2) & 1)) return false;
+      const int keys = int(min(int64_t(kKeys), R.len - int64_t(begin + j) * kKeys));
+      const uint64_t v0 = smem_desc(slot_at(5 * j + 3), kSlot / 2, 1024, kSwizzle128B);
+      const uint64_t v1 = smem_desc(slot_at(5 * j + 4), kSlot / 2, 1024, kSwizzle128B);
+      if (keys == kKeys) {
+        if (!arrived(B_P + s, j & 1)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            mma_ts(tmem_o, tmem_s + 8 * k, desc_add(k < 4 ? v0 : v1, 2048 * (k & 3)), id_pv, j > 0 || k > 0);
+          mma_commit(bar(B_VFREE + (j & 1)));
+          if (j + 1 == Ts) mma_commit(bar(B_O + s));
+        }
+        return true;
+      }
+      // the request's last tile: only k-steps that hold keys; the rows of V behind
+      // the last key may hold anything (another request's, or nobody's) and are
+      // zeroed, by both stages alike, since a weight of 0 times NaN is NaN
+      const int steps = (keys + 15) / 16;
+      for (int u = 16 * keys + lane; u < 256 * steps; u += 32) {  // 16-byte units, 16 a row
+        const int key = u / 16, part = u % 16;
+        st_shared_v4(slot_at(5 * j + 3 + key / 64) + (part / 8) * (kSlot / 2) + (key % 64) * 128 + (part % 8) * 16, 0, 0, 0, 0);
+      }
+      fence_proxy_async_smem();
+      __syncwarp();
+      if (!arrived(B_P + s, j & 1)) return false;
+      tc_fence_after();
+      if (elect_one()) {
+        for (int k = 0; k < steps; ++k)
+          mma_ts(tmem_o, tmem_s + 8 * k, desc_add(k < 4 ? v0 : v1, 2048 * (k & 3)), id_pv, j > 0 || k > 0);
+        mma_commit(bar(B_VFREE + (j & 1)));
+        if (j + 1 == Ts) mma_commit(bar(B_O + s));
+      }
+      return true;
+    };
+    // a tile that this stage has no use for is released as soon as it is there
+    auto pass = [&](int full, int free, int j) -> bool {
+      if (!arrived(full + (j & 1), uint32_t(j / 2) & 1)) return false;
+      if (elect_one()) mbar_arrive(bar(free + (j & 1)));
+      return true;
+    };
+    bool ok = Ts == 0 || arrived(B_Q + s, 0);
+    if (ok && TN > 0) ok = Ts > 0 ? qk(0) : pass(B_KFULL, B_KFREE, 0);
     for (int j = 0; j < TN && ok; ++j) {
-      // stage 1 uses a tile last where it uses it (T1 >= T0, or it is empty)
-      if (j < T0) ok = pv(0, j, true, j >= T1, j + 1 == T0) && (j + 1 >= T0 || qk(0, j + 1, j + 1 >= T1));
-      if (ok && j < T1) ok = pv(1, j, j >= T0, true, j + 1 == T1) && (j + 1 >= T1 || qk(1, j + 1, true));
+      ok = j < Ts ? pv(j) : pass(B_VFULL, B_VFREE, j);
+      if (ok && j + 1 < TN) ok = j + 1 < Ts ? qk(j + 1) : pass(B_KFULL, B_KFREE, j + 1);
     }
-    if (TN > 0 && elect_one()) {  // every MMA issued has run once this arrives
-      mma_commit(bar(B_FIN));
-      drain(bar(B_FIN), 0, A.err);
+    if (Ts > 0 && elect_one()) {  // every MMA issued has run once this arrives
+      mma_commit(bar(B_FIN + s));
+      drain(bar(B_FIN + s), 0, A.err);
     }
     __syncwarp();
   } else {
