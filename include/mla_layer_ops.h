@@ -39,6 +39,8 @@ extern "C" {
 #define MTV_MAX_HEADS 65535
 /* Longest head that mla_norm_rope_write normalises. */
 #define MTV_MAX_NORM_DIM 1024
+/* Most query or key rows of mla_prefill_run. */
+#define MTV_MAX_PREFILL_ROWS (1 << 30)
 /* Most splits of mla_prefill_run's keys. */
 #define MTV_MAX_PREFILL_SPLITS 64
 
@@ -109,7 +111,7 @@ int mla_prefill_workspace(int num_sms, int bs, int64_t max_q, int64_t max_kv, in
  * kv_indptr      device, int32 [bs + 1]: offsets of their keys.
  * bs             0 .. MTV_MAX_HEADS.
  * max_q, max_kv  host: bounds of n and L (they size the grid).
- * num_q, num_kv  host: rows of the buffers, < 2^31.
+ * num_q, num_kv  host: rows of the buffers, at most MTV_MAX_PREFILL_ROWS.
  * num_heads      0 .. MTV_MAX_HEADS.
  * dtype          MTV_DTYPE_BF16 or MTV_DTYPE_FP16: q, k_nope, k_rope, v, out.
  *                All their addresses and strides are multiples of 16 bytes.

@@ -32,7 +32,9 @@
 // (bounded too) before TMEM is freed.
 //
 // With few query rows the keys are split over blocks: each writes its
-// normalised part and its lse, and combine_kernel joins them.
+// normalised part and its lse, and combine_kernel joins them. 
+// (Letting both stages take a request's 128 rows or fewer and its tiles in turn was
+// no faster: such calls are bound by the keys' way from memory.)
 #include <math.h>
 #include <stdint.h>
 
@@ -81,17 +83,17 @@ struct PrefillArgs {
 };
 
 struct PrefillReq {
-  int64_t q0, k0, n, len;
+  int q0, k0, n, len;
 };
 
 // The request's rows, checked against the buffers and the bounds; n = 0 where
 // they do not hold.
 __device__ __forceinline__ PrefillReq load_prefill_req(const PrefillArgs& A, int r, bool report) {
   const int64_t q0 = A.qo_indptr[r], q1 = A.qo_indptr[r + 1], k0 = A.kv_indptr[r], k1 = A.kv_indptr[r + 1];
-  PrefillReq R{q0, k0, q1 - q0, k1 - k0};
-  if (q0 < 0 || q1 < q0 || q1 > A.num_q || k0 < 0 || k1 < k0 || k1 > A.num_kv || R.n > A.max_q || R.len > A.max_kv) {
+  PrefillReq R{int(q0), int(k0), int(q1 - q0), int(k1 - k0)};
+  if (q0 < 0 || q1 < q0 || q1 > A.num_q || k0 < 0 || k1 < k0 || k1 > A.num_kv || q1 - q0 > A.max_q || k1 - k0 > A.max_kv) {
     if (report && A.err) atomicOr(A.err, MTV_DEVERR_INDPTR);
-    R.n = 0;
+    R.n = R.len = 0;
   }
   return R;
 }
@@ -118,27 +120,34 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   id /= unsigned(A.nsplit);
   const int h = int(id % unsigned(A.heads)), r = int(id / unsigned(A.heads));
   const PrefillReq R = load_prefill_req(A, r, tid == 0);
-  const int64_t row0 = int64_t(qb) * kBlockRows;
+  const int row0 = qb * kBlockRows;
   if (row0 >= R.n) return;
 
   // key tiles of both stages: up to the last key that a stage's last row sees
-  const int64_t shift = R.len - R.n;  // query i sees keys up to shift + i
-  auto key_end = [&](int s) -> int64_t {
-    const int64_t first = row0 + s * kStageRows;
+  const int shift = R.len - R.n;  // query i sees keys up to shift + i
+  auto tiles_of = [&](int s) -> int {
+    const int first = row0 + s * kStageRows;
     if (first >= R.n) return 0;
-    const int64_t last = min(R.n, first + kStageRows) - 1;
-    return A.causal ? max(int64_t(0), min(R.len, shift + last + 1)) : R.len;
+    const int last = min(R.n, first + kStageRows) - 1;
+    const int keys = A.causal ? max(0, min(R.len, shift + last + 1)) : R.len;
+    return (keys + kKeys - 1) / kKeys;
   };
-  auto tiles_of = [](int64_t keys) { return int((keys + kKeys - 1) / kKeys); };
-  const int tiles0 = tiles_of(key_end(0)), tiles1 = tiles_of(key_end(1));
+  const int tiles0 = tiles_of(0), tiles1 = tiles_of(1);
   const int each = (max(tiles0, tiles1) + A.nsplit - 1) / A.nsplit, begin = split * each;
   auto mine = [&](int tiles) { return max(0, min(tiles - begin, each)); };
   const int T0 = mine(tiles0), T1 = mine(tiles1), TN = max(T0, T1);
+  auto stage_tiles = [&](int s) { return s ? T1 : T0; };
 
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_KFREE && i < B_S ? 2 : i == B_P || i == B_P + 1 ? 4 : 1);
     ctl->abort = 0;
     fence_mbar_init_cluster();
+  }
+  if (warp == 10 && lane == 0) {
+    prefetch_map(&A.q);
+    prefetch_map(&A.k_nope);
+    prefetch_map(&A.k_rope);
+    prefetch_map(&A.v);
   }
   if (warp == 8) {
     tmem_alloc(smem_u32(&ctl->tmem), 512);
@@ -157,14 +166,14 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       auto load_q = [&](int s) {
         mbar_arrive_expect_tx(bar(B_Q + s), kQStage);
         for (int c = 0; c < 3; ++c)
-          tma_load_3d(base + s * kQStage + c * kSlot, &A.q, 64 * c, qh, int(R.q0 + row0 + s * kStageRows), bar(B_Q + s));
+          tma_load_3d(base + s * kQStage + c * kSlot, &A.q, 64 * c, qh, R.q0 + row0 + s * kStageRows, bar(B_Q + s));
       };
       bool ok = true;
       int k_asked = 0, v_asked = 0;
-      if (T0 > 0) load_q(0);
+      if (stage_tiles(0) > 0) load_q(0);
       for (int j = 0; j < TN; ++j) {
         // slots in the order of their use: K(j)'s first was K(j - 2)'s last, its others V(j - 2)'s, V(j)'s K(j - 1)'s first
-        const int row = int(R.k0) + (begin + j) * kKeys;
+        const int row = R.k0 + (begin + j) * kKeys;
         if (j >= 2) ok = wait_for(bar(B_KFREE + (j & 1)), uint32_t(j / 2 - 1) & 1, ctl, A.err) &&
                          wait_for(bar(B_VFREE + (j & 1)), uint32_t(j / 2 - 1) & 1, ctl, A.err);
         if (!ok) break;
@@ -174,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         tma_load_3d(slot_at(5 * j + 1), &A.k_nope, 64, kh, row, kf);
         tma_load_3d(slot_at(5 * j + 2), &A.k_rope, 0, 0, row, kf);
         ++k_asked;
-        if (j == 0 && T1 > 0) load_q(1);
+        if (j == 0 && stage_tiles(1) > 0) load_q(1);
         if (j >= 1) ok = wait_for(bar(B_KFREE + ((j - 1) & 1)), uint32_t((j - 1) / 2) & 1, ctl, A.err);
         if (!ok) break;
         mbar_arrive_expect_tx(vf, 2 * kSlot);
@@ -185,8 +194,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         ++v_asked;
       }
       // what was asked for lands before the block ends, read or not (a second stage's Q is asked for with the first tile)
-      if (T0 > 0) drain(bar(B_Q), 0, A.err);
-      if (T1 > 0) drain(bar(B_Q + 1), 0, A.err);
+      for (int s = 0; s < 2; ++s)
+        if (stage_tiles(s) > 0) drain(bar(B_Q + s), 0, A.err);
       for (int j = max(0, k_asked - 2); j < k_asked; ++j) drain(bar(B_KFULL + (j & 1)), uint32_t(j / 2) & 1, A.err);
       for (int j = max(0, v_asked - 2); j < v_asked; ++j) drain(bar(B_VFULL + (j & 1)), uint32_t(j / 2) & 1, A.err);
     }
@@ -196,7 +205,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     constexpr bool kBf16 = std::is_same<T, __nv_bfloat16>::value;
     constexpr uint32_t id_qk = kBf16 ? idesc_bf16_f32(128, 128, 0, 0) : idesc_fp16_f32(128, 128, 0, 0);
     constexpr uint32_t id_pv = kBf16 ? idesc_bf16_f32(128, 128, 0, 1) : idesc_fp16_f32(128, 128, 0, 1);
-    const int s = warp - 8, Ts = s ? T1 : T0;
+    const int s = warp - 8, Ts = stage_tiles(s);
     const uint32_t tmem_s = tmem + kTmemS + 128 * s, tmem_o = tmem + kTmemO + 128 * s;
     auto arrived = [&](int b, uint32_t parity) {
       return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, A.err)) != 0;
@@ -219,7 +228,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
     auto pv = [&](int j) -> bool {  // O += P V(j)
       if (!arrived(B_VFULL + (j & 1), uint32_t(j / 2) & 1)) return false;
-      const int keys = int(min(int64_t(kKeys), R.len - int64_t(begin + j) * kKeys));
+      const int keys = min(kKeys, R.len - (begin + j) * kKeys);
       const uint64_t v0 = smem_desc(slot_at(5 * j + 3), kSlot / 2, 1024, kSwizzle128B);
       const uint64_t v1 = smem_desc(slot_at(5 * j + 4), kSlot / 2, 1024, kSwizzle128B);
       if (keys == kKeys) {
@@ -274,23 +283,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   } else {
     // ------------------------------------------------------------- softmax
     const int s = warp >> 2;
-    const int64_t i0 = row0 + s * kStageRows + (warp & 3) * 32, i = i0 + lane;  // rows of the request
+    const int i0 = row0 + s * kStageRows + (warp & 3) * 32, i = i0 + lane;  // rows of the request
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    const int Ts = s ? T1 : T0;
+    const int Ts = stage_tiles(s);
     const float c = A.scale * kLog2e, grow = kRescaleLog2 / c;
     // keys before `end` are this row's; tiles that end before `clear` need no mask in this warp
-    const int end = int(A.causal ? max(int64_t(0), min(R.len, shift + i + 1)) : R.len);
-    const int clear = int(A.causal ? max(int64_t(0), min(R.len, shift + i0 + 1)) : R.len);
+    int end = A.causal ? max(0, min(R.len, shift + i + 1)) : R.len;
+    int clear = A.causal ? max(0, min(R.len, shift + i0 + 1)) : R.len;
+    end -= begin * kKeys, clear -= begin * kKeys;  // from the block's first tile on
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    uint32_t x[128];
+    uint32_t x[128] = {};
     for (int j = 0; j < Ts; ++j) {
       ok = wait_for(bar(B_S + s), j & 1, ctl, A.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
       tmem_ld128_sync(tmem + lanes + kTmemS + 128 * s, x);
-      const int k0 = (begin + j) * kKeys;
+      const int k0 = j * kKeys;
       if (k0 + kKeys > clear) {
         const int live = end - k0;
 #pragma unroll
@@ -326,7 +336,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
-        uint32_t p[32];
 #pragma unroll
         for (int u = 0; u < 32; ++u) {
           float a, b;
@@ -334,76 +343,67 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           a = ex2(a), b = ex2(b);
           if (u & 1) sum1 = f2_add(sum1, f2_pack(a, b));
           else sum0 = f2_add(sum0, f2_pack(a, b));
-          p[u] = join(a, b, T());
+          x[64 * half + u] = join(a, b, T());  // in place: the register is read already
         }
-        tmem_st32_sync(tmem + lanes + kTmemS + 128 * s + 32 * half, p);
+        tmem_st32_sync(tmem + lanes + kTmemS + 128 * s + 32 * half, reinterpret_cast<const uint32_t(&)[32]>(x[64 * half]));
       }
-      float a, b;
-      f2_unpack(f2_add(sum0, sum1), a, b);
-      l += a + b;
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(bar(B_P + s));
+      float a, b;
+      f2_unpack(f2_add(sum0, sum1), a, b);
+      l += a + b;
     }
     if (ok && Ts > 0) ok = __all_sync(0xffffffffu, wait_for(bar(B_O + s), 0, ctl, A.err));
     if (ok && i0 < R.n) {
       const bool some = l != 0.f;  // true for a NaN too, which the row then shows
       const float inv = some ? 1.f / l : 0.f;
-      const int64_t at = (R.q0 + i) * A.heads + h;
-      const float lse = some ? m * A.scale + logf(l) : -INFINITY;
-      const int live = int(min(int64_t(32), R.n - i0));
+      const int live = min(32, R.n - i0);
       tc_fence_after();
+      if (Ts > 0) tmem_ld128_sync(tmem + lanes + kTmemO + 128 * s, x);
       // rows to memory through this stage's part of Q (every product that read it has run), so
       // that a warp stores whole rows; 16-byte units are swizzled by the row
       const uint32_t mine_s = base + s * kQStage + uint32_t((warp & 3) * 32) * 256u;
+#pragma unroll
+      for (int u = 0; u < 128; ++u) x[u] = some ? __float_as_uint(__uint_as_float(x[u]) * inv) : 0u;
+      const int64_t all = A.num_q * A.heads, at = int64_t(R.q0 + i0) * A.heads + h;
       if (A.nsplit == 1) {
-        if (A.lse && i < R.n) A.lse[at] = lse;
 #pragma unroll
-        for (int u = 0; u < 128; u += 32) {
-          uint32_t y[32] = {};
-          if (Ts > 0) tmem_ld32_sync(tmem + lanes + kTmemO + 128 * s + u, y);
-#pragma unroll
-          for (int e = 0; e < 32; e += 8) {
-            float f[8];
-#pragma unroll
-            for (int g = 0; g < 8; ++g) f[g] = some ? __uint_as_float(y[e + g]) * inv : 0.f;
-            const uint4 w = pack<T>(f);
-            st_shared_v4(mine_s + lane * 256 + ((((u + e) / 8) ^ (lane & 15)) << 4), w.x, w.y, w.z, w.w);
-          }
+        for (int u = 0; u < 128; u += 8) {
+          const uint4 w = pack<T>(reinterpret_cast<const float*>(x) + u);
+          st_shared_v4(mine_s + lane * 256 + (((u / 8) ^ (lane & 15)) << 4), w.x, w.y, w.z, w.w);
         }
         __syncwarp();
-        T* out = static_cast<T*>(A.out) + (R.q0 + i0) * A.o_tok + int64_t(h) * A.o_head;
-#pragma unroll 4
-        for (int u = lane; u < live * 16; u += 32) {
-          const int rr = u >> 4, cc = u & 15;
-          const float4 w = ld_shared_f4(mine_s + rr * 256 + ((cc ^ (rr & 15)) << 4));
-          *reinterpret_cast<float4*>(out + int64_t(rr) * A.o_tok + cc * 8) = w;
-        }
-      } else {
-        const int64_t all = A.num_q * A.heads;
-        if (i < R.n) A.part[int64_t(A.nsplit) * all * kV + split * all + at] = lse;
-        // a part without weights is not read by the combine
-#pragma unroll 1
-        for (int u = 0; u < 128; u += 32) {
-          uint32_t y[32] = {};
-          if (Ts > 0) tmem_ld32_sync(tmem + lanes + kTmemO + 128 * s + u, y);
+        T* out = static_cast<T*>(A.out) + int64_t(R.q0 + i0) * A.o_tok + int64_t(h) * A.o_head + (lane & 15) * 8;
 #pragma unroll
-          for (int e = 0; e < 32; e += 4) {
-            const float f[4] = {__uint_as_float(y[e]) * inv, __uint_as_float(y[e + 1]) * inv, __uint_as_float(y[e + 2]) * inv,
-                                __uint_as_float(y[e + 3]) * inv};
-            st_shared_v4(mine_s + lane * 128 + (((e / 4) ^ (lane & 7)) << 4), __float_as_uint(f[0]), __float_as_uint(f[1]),
-                         __float_as_uint(f[2]), __float_as_uint(f[3]));
-          }
+        for (int u = 0; u < 32; u += 2) {
+          const int rr = u + (lane >> 4);
+          const float4 w = ld_shared_f4(mine_s + rr * 256 + (((lane & 15) ^ (rr & 15)) << 4));
+          if (rr < live) *reinterpret_cast<float4*>(out + int64_t(rr) * A.o_tok) = w;
+        }
+      } else {  // a part without weights is not read by the combine
+        float* part = A.part + (split * all + at) * kV + (lane & 15) * 4;
+#pragma unroll
+        for (int half = 0; half < 128; half += 64) {
+#pragma unroll
+          for (int u = 0; u < 64; u += 4)
+            st_shared_v4(mine_s + lane * 256 + (((u / 4) ^ (lane & 15)) << 4), x[half + u], x[half + u + 1], x[half + u + 2],
+                         x[half + u + 3]);
           __syncwarp();
-          float* part = A.part + (split * all + (R.q0 + i0) * A.heads + h) * kV + u;
-#pragma unroll 4
-          for (int w = lane; w < live * 8; w += 32) {
-            const int rr = w >> 3, cc = w & 7;
-            *reinterpret_cast<float4*>(part + int64_t(rr) * A.heads * kV + cc * 4) =
-                ld_shared_f4(mine_s + rr * 128 + ((cc ^ (rr & 7)) << 4));
+#pragma unroll
+          for (int u = 0; u < 32; u += 2) {
+            const int rr = u + (lane >> 4);
+            const float4 w = ld_shared_f4(mine_s + rr * 256 + (((lane & 15) ^ (rr & 15)) << 4));
+            if (rr < live) *reinterpret_cast<float4*>(part + int64_t(rr) * A.heads * kV + half) = w;
           }
           __syncwarp();
         }
+      }
+      if (lane < live) {
+        const float lse = some ? m * A.scale + logf(l) : -INFINITY;
+        const int64_t to = at + int64_t(lane) * A.heads;
+        if (A.nsplit > 1) A.part[int64_t(A.nsplit) * all * kV + split * all + to] = lse;
+        else if (A.lse) A.lse[to] = lse;
       }
     }
   }
@@ -413,34 +413,56 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of split keys by their lse: a warp a row of one head.
+// Joins the parts of split keys by their lse: a block a row of one head, whose
+// four warps take every fourth part with eight loads in flight (one warp a row
+// with four took 6 us for 38 parts).
 template <typename T>
-__global__ void __launch_bounds__(256) combine_kernel(const __grid_constant__ PrefillArgs A) {
-  const int lane = threadIdx.x & 31;
-  const int r = blockIdx.z, h = blockIdx.y;
-  const PrefillReq R = load_prefill_req(A, r, false);
-  const int64_t i = int64_t(blockIdx.x) * 8 + (threadIdx.x >> 5);
+__global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ PrefillArgs A) {
+  __shared__ float4 sums[4][32];
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, i = blockIdx.x;
+  const PrefillReq R = load_prefill_req(A, blockIdx.z, false);
   if (i >= R.n) return;
-  const int64_t all = A.num_q * A.heads, at = (R.q0 + i) * A.heads + h;
+  const int64_t all = A.num_q * A.heads, at = int64_t(R.q0 + i) * A.heads + h;
   const float* lse = A.part + int64_t(A.nsplit) * all * kV + at;
+  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts are being written
   const float a = lane < A.nsplit ? lse[lane * all] : -INFINITY, b = lane + 32 < A.nsplit ? lse[(lane + 32) * all] : -INFINITY;
   float top = fmaxf(a, b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
   const float ref = top == -INFINITY ? 0.f : top;
-  float wa = expf(a - ref), wb = expf(b - ref), sum = wa + wb;
+  const float wa = expf(a - ref), wb = expf(b - ref);
+  float sum = wa + wb;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float inv = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
-  for (int k = 0; k < A.nsplit; ++k) {
-    const float w = __shfl_sync(0xffffffffu, k < 32 ? wa : wb, k & 31) * inv;
-    if (w == 0.f) continue;  // a part without weights was not written
-    const float4 v = *reinterpret_cast<const float4*>(A.part + (k * all + at) * kV + 4 * lane);
-    acc.x = fmaf(w, v.x, acc.x), acc.y = fmaf(w, v.y, acc.y), acc.z = fmaf(w, v.z, acc.z), acc.w = fmaf(w, v.w, acc.w);
+  for (int k0 = warp; k0 < A.nsplit; k0 += 32) {
+    float4 v[8];
+    float w[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int k = k0 + 4 * e;
+      w[e] = __shfl_sync(0xffffffffu, k < 32 ? wa : wb, k & 31) * inv;
+      if (k >= A.nsplit) w[e] = 0.f;
+      v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
+      // a part without weights was not written
+      if (w[e] != 0.f) v[e] = *reinterpret_cast<const float4*>(A.part + (k * all + at) * kV + 4 * lane);
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      acc.x = fmaf(w[e], v[e].x, acc.x), acc.y = fmaf(w[e], v[e].y, acc.y);
+      acc.z = fmaf(w[e], v[e].z, acc.z), acc.w = fmaf(w[e], v[e].w, acc.w);
+    }
   }
-  T* out = static_cast<T*>(A.out) + (R.q0 + i) * A.o_tok + int64_t(h) * A.o_head;
+  sums[warp][lane] = acc;
+  __syncthreads();
+  if (warp != 0) return;
+#pragma unroll
+  for (int e = 1; e < 4; ++e) {
+    const float4 v = sums[e][lane];
+    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+  }
+  T* out = static_cast<T*>(A.out) + int64_t(R.q0 + i) * A.o_tok + int64_t(h) * A.o_head;
   *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(join(acc.x, acc.y, T()), join(acc.z, acc.w, T()));
   if (A.lse && lane == 0) A.lse[at] = sum != 0.f ? ref + logf(sum) : -INFINITY;
 }
@@ -452,8 +474,16 @@ template <typename T> cudaError_t launch_prefill(const PrefillArgs& A, cudaStrea
   prefill_kernel<T><<<unsigned(blocks), kThreads, kSmem, st>>>(A);
   e = cudaGetLastError();
   if (e != cudaSuccess || A.nsplit == 1) return e;
-  combine_kernel<T><<<dim3(unsigned((A.max_q + 7) / 8), unsigned(A.heads), unsigned(A.bs)), 256, 0, st>>>(A);
-  return cudaGetLastError();
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = dim3(unsigned(A.max_q), unsigned(A.heads), unsigned(A.bs));
+  config.blockDim = dim3(128);
+  config.stream = st;
+  config.attrs = early;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, combine_kernel<T>, A);
 }
 
 uint64_t workspace_bytes_of(int nsplit, int64_t num_q, int heads) {
@@ -467,13 +497,13 @@ extern "C" int mla_prefill_workspace(int num_sms, int bs, int64_t max_q, int64_t
                                      int* nsplit_out, uint64_t* bytes_out) {
   using namespace mtv;
   if (!nsplit_out || !bytes_out) return MTV_E_NULL_POINTER;
-  if (num_sms < 1 || bs < 0 || bs > MTV_MAX_HEADS || max_q < 0 || max_kv < 0 || num_q < 0 || num_q > INT32_MAX ||
-      max_q > INT32_MAX || max_kv > INT32_MAX || num_heads < 0 || num_heads > MTV_MAX_HEADS)
+  if (num_sms < 1 || bs < 0 || bs > MTV_MAX_HEADS || max_q < 0 || max_kv < 0 || num_q < 0 ||
+      num_q > MTV_MAX_PREFILL_ROWS || max_q > MTV_MAX_PREFILL_ROWS || max_kv > MTV_MAX_PREFILL_ROWS || num_heads < 0 || num_heads > MTV_MAX_HEADS)
     return MTV_E_BAD_ARGUMENT;
-  // as many splits as leave every one an SM, of eight key tiles at least (about 6 us: a split costs a
-  // second launch and its parts' way through memory)
+  // as many splits as leave every block an SM, of four key tiles at least (a split costs a second launch
+  // and its parts' way through memory)
   const int64_t blocks = int64_t(bs) * num_heads * ((max_q + kBlockRows - 1) / kBlockRows);
-  const int64_t most = blocks > 0 ? num_sms / blocks : 1, worth = (max_kv + kKeys - 1) / kKeys / 8;
+  const int64_t most = blocks > 0 ? num_sms / blocks : 1, worth = (max_kv + kKeys - 1) / kKeys / 4;
   int64_t n = most < worth ? most : worth;
   if (n > MTV_MAX_PREFILL_SPLITS) n = MTV_MAX_PREFILL_SPLITS;
   *nsplit_out = n < 2 ? 1 : int(n);
@@ -489,8 +519,9 @@ extern "C" int mla_prefill_run(const void* q, int64_t q_tok_stride, int64_t q_he
                                int64_t out_tok_stride, int64_t out_head_stride, float* lse, int nsplit,
                                void* workspace, uint64_t workspace_bytes, uint32_t* err, void* stream) {
   using namespace mtv;
-  if (bs < 0 || bs > MTV_MAX_HEADS || max_q < 0 || max_kv < 0 || max_q > INT32_MAX || max_kv > INT32_MAX ||
-      num_q < 0 || num_kv < 0 || num_q > INT32_MAX || num_kv > INT32_MAX || num_heads < 0 ||
+  if (bs < 0 || bs > MTV_MAX_HEADS || max_q < 0 || max_kv < 0 || num_q < 0 || num_kv < 0 ||
+      max_q > MTV_MAX_PREFILL_ROWS || max_kv > MTV_MAX_PREFILL_ROWS || num_q > MTV_MAX_PREFILL_ROWS ||
+      num_kv > MTV_MAX_PREFILL_ROWS || num_heads < 0 ||
       num_heads > MTV_MAX_HEADS || (dtype != MTV_DTYPE_BF16 && dtype != MTV_DTYPE_FP16) || !isfinite(scale) ||
       !(scale > 0) || (causal != 0 && causal != 1) || nsplit < 1 || nsplit > MTV_MAX_PREFILL_SPLITS)
     return MTV_E_BAD_ARGUMENT;

@@ -18,6 +18,7 @@ __device__ __forceinline__ uint32_t smem_u32(const void* p) {
 // whole warp, and one thread of a converged warp: code under both keeps the
 // operands of tcgen05 instructions in uniform registers.
 __device__ __forceinline__ int uniform_warp() { return __shfl_sync(0xffffffffu, int(threadIdx.x) >> 5, 0); }
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n .reg .pred p;\n elect.sync _|p, 0xffffffff;\n selp.u32 %0, 1, 0, p;\n}" : "=r"(p));
@@ -70,6 +71,26 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
       " selp.u32 %0, 1, 0, p;\n}"
       : "=r"(ok) : "r"(bar), "r"(parity) : "memory");
   return ok != 0;
+}
+
+// ---------------------------------------------------------------- launch control
+// Asks for a block of this grid that has not been launched yet: the 16-byte
+// answer arrives at `dst`, completing its bytes on `bar`.
+__device__ __forceinline__ void try_cancel(uint32_t dst, uint32_t bar) {
+  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
+               "r"(bar)
+               : "memory");
+}
+// Whether the answer names a block (which this one now has to do), and its x.
+__device__ __forceinline__ bool read_cancelled(uint32_t at, unsigned& x) {
+  uint32_t some, bx;
+  asm volatile(
+      "{\n .reg .pred p;\n .reg .b128 r;\n .reg .b32 y, z;\n ld.shared.b128 r, [%2];\n"
+      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
+      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, _}, r;\n}"
+      : "=r"(some), "=r"(bx) : "r"(at) : "memory");
+  if (some) x = bx;
+  return some != 0;
 }
 
 // ---------------------------------------------------------------- cluster
