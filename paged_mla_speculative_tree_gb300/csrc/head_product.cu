@@ -68,7 +68,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
   Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (base - raw) + kOffCtl);
   auto bar = [&](int i) { return base + 8u * uint32_t(i); };
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
   const uint32_t w_chunk = uint32_t(A.nt) * 128u;
   const uint32_t off_x = kOffData + uint32_t(A.chunks) * w_chunk, off_out = off_x + uint32_t(A.slots) * kXSlot;
   const int64_t first = A.units * blockIdx.x / gridDim.x, last = A.units * (blockIdx.x + 1) / gridDim.x;
@@ -132,36 +132,44 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
     __syncwarp();
   } else if (warp == 1) {
     // ------------------------------------------------------------- products
-    if (lane == 0) {
-      const uint32_t id = std::is_same<T, __nv_bfloat16>::value ? idesc_bf16_f32(kRows, A.nt, 0, A.w_k_major ? 0 : 1)
-                                                                : idesc_fp16_f32(kRows, A.nt, 0, A.w_k_major ? 0 : 1);
-      const uint32_t w_step = A.w_k_major ? 32u : 2048u;
-      int64_t item = 0, group = -1, n = 0;
-      int loads = 0;
-      bool ok = true;
-      for (int64_t u = first; u < last && ok; ++u, ++n) {
-        const int64_t g = u / A.m_tiles;
-        const bool fresh = g != group;
-        if (fresh) ++loads, group = g;
-        const int buf = int(n & 1);
-        if (n >= 2) ok = wait_for(bar(B_ACCFREE + buf), uint32_t(n / 2 - 1) & 1, ctl, A.err);
-        for (int c = 0; c < A.chunks && ok; ++c, ++item) {
-          const int slot = int(item % A.slots);
-          if (fresh) ok = wait_for(bar(B_WFULL + c), uint32_t(loads - 1) & 1, ctl, A.err);
-          ok = ok && wait_for(bar(B_XFULL + slot), uint32_t(item / A.slots) & 1, ctl, A.err);
-          if (!ok) break;
-          tc_fence_after();
-          const uint64_t a = smem_desc(base + off_x + slot * kXSlot, 16, 1024, kSwizzle128B);
-          const uint64_t b = smem_desc(base + kOffData + c * w_chunk, A.w_k_major ? 16 : 8192, 1024, kSwizzle128B);
+    const uint32_t id = std::is_same<T, __nv_bfloat16>::value ? idesc_bf16_f32(kRows, A.nt, 0, A.w_k_major ? 0 : 1)
+                                                              : idesc_fp16_f32(kRows, A.nt, 0, A.w_k_major ? 0 : 1);
+    const uint32_t w_step = A.w_k_major ? 32u : 2048u, acc = uniform(tmem), data = uniform(base);
+    auto arrived = [&](int b, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, A.err)) != 0;
+    };
+    int64_t group = -1;
+    int slot = 0, loads = 0, n = 0;
+    uint32_t phase = 0;  // of the ring's slots
+    bool ok = true;
+    for (int64_t u = first; u < last && ok; ++u, ++n) {
+      const int64_t g = u / A.m_tiles;
+      const bool fresh = g != group, change = u + 1 < last && (u + 1) / A.m_tiles != g;
+      if (fresh) ++loads, group = g;
+      const int buf = n & 1;
+      if (n >= 2) ok = arrived(B_ACCFREE + buf, uint32_t(n / 2 - 1) & 1);
+      for (int c = 0; c < A.chunks && ok; ++c) {
+        if (fresh) ok = arrived(B_WFULL + c, uint32_t(loads - 1) & 1);
+        ok = ok && arrived(B_XFULL + slot, phase);
+        if (!ok) break;
+        tc_fence_after();
+        if (elect_one()) {
+          const uint64_t a = smem_desc(data + off_x + slot * kXSlot, 16, 1024, kSwizzle128B);
+          const uint64_t b = smem_desc(data + kOffData + c * w_chunk, A.w_k_major ? 16 : 8192, 1024, kSwizzle128B);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
-            mma_ss(tmem + uint32_t(A.nt) * buf, desc_add(a, 32 * k), desc_add(b, w_step * k), id, c + k > 0);
+            mma_ss(acc + uint32_t(A.nt) * buf, desc_add(a, 32 * k), desc_add(b, w_step * k), id, c + k > 0);
           mma_commit(bar(B_XEMPTY + slot));
         }
-        if (!ok) break;
-        mma_commit(bar(B_ACC + buf));
-        if (u + 1 < last && (u + 1) / A.m_tiles != g) mma_commit(bar(B_WFREE));
+        if (++slot == A.slots) slot = 0, phase ^= 1;
       }
+      if (!ok) break;
+      if (elect_one()) {
+        mma_commit(bar(B_ACC + buf));
+        if (change) mma_commit(bar(B_WFREE));
+      }
+    }
+    if (elect_one()) {
       mma_commit(bar(B_FIN));  // every MMA issued has run once this arrives
       drain(bar(B_FIN), 0, A.err);
     }
