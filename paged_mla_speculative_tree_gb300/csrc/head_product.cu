@@ -46,7 +46,7 @@ struct ProductArgs {
 constexpr int kRows = 128, kChunk = 64;   // tokens a unit, k a chunk
 constexpr int kMaxChunks = MTV_MAX_HEAD_DIM / kChunk, kMaxSlots = 8;
 constexpr uint32_t kXSlot = kRows * kChunk * 2, kMaxWeights = 131072;
-constexpr uint32_t kBlockBytes = 32 * 128;  // staged output: 32 rows x 64 columns a warp, two of them
+constexpr uint32_t kBlockBytes = 32 * 128;  // staged output: 32 rows x 64 columns
 constexpr int kThreads = 192;
 enum : int {
   B_XFULL = 0, B_XEMPTY = B_XFULL + kMaxSlots, B_WFULL = B_XEMPTY + kMaxSlots, B_WFREE = B_WFULL + kMaxChunks,
@@ -58,8 +58,31 @@ static_assert(kOffCtl + sizeof(Ctl) <= kOffData, "barriers");
 struct TensorArgs {
   CUtensorMap x, w, out;
   uint32_t* err;
-  int64_t units, m_tiles, tokens;   // units: heads * n_tiles * m_tiles
-  int n_tiles, nt, chunks, slots, w_k_major, x_by_head, w_by_head, out_by_head, n_dim;
+  int64_t units, tokens;   // units: heads * n_tiles * m_tiles
+  int m_tiles, n_tiles, nt, chunks, slots, w_k_major, x_by_head, w_by_head, out_by_head, n_dim;
+};
+
+// A block's units in order: 128 tokens after 128 tokens of one (head, nt outputs),
+// then the next such group.  Counted on, since 64-bit divisions by every role and
+// chunk took longer than the chunk's products (8,191 tokens expanded: 186 us).
+struct Units {
+  int64_t left;
+  int h, n, t;  // head, outputs' tile, tokens' tile
+  bool fresh;   // the first of its group in this block
+  __device__ __forceinline__ Units(int64_t first, int64_t last, const TensorArgs& A) : left(last - first) {
+    const int64_t g = first / A.m_tiles;
+    t = int(first % A.m_tiles), h = int(g / A.n_tiles), n = int(g % A.n_tiles);
+    fresh = true;
+  }
+  __device__ __forceinline__ bool more() const { return left > 0; }
+  __device__ __forceinline__ bool changes(const TensorArgs& A) const { return left > 1 && t + 1 == A.m_tiles; }
+  __device__ __forceinline__ void next(const TensorArgs& A) {
+    --left;
+    fresh = ++t == A.m_tiles;
+    if (!fresh) return;
+    t = 0;
+    if (++n == A.n_tiles) n = 0, ++h;
+  }
 };
 
 template <typename T>
@@ -91,28 +114,23 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
   if (warp == 0) {
     // ------------------------------------------------------------- copies
     if (lane == 0) {
-      int64_t item = 0, group = -1;
-      int loads = 0, asked = 0;  // of weights, and chunks of the last one
+      int slot = 0, items = 0, loads = 0, asked = 0;  // loads of weights, and chunks of the last one
+      uint32_t phase = 1;                             // of the slots' releases: the first round waits for none
       bool ok = true;
-      for (int64_t u = first; u < last && ok; ++u) {
-        const int64_t g = u / A.m_tiles;
-        const int h = int(g / A.n_tiles), n0 = int(g % A.n_tiles) * A.nt, t0 = int(u % A.m_tiles) * kRows;
-        const int xh = A.x_by_head ? h : 0, wh = A.w_by_head ? h : 0;
-        const bool fresh = g != group;
-        for (int c = 0; c < A.chunks && ok; ++c, ++item) {
-          const int slot = int(item % A.slots);
-          if (item >= A.slots) ok = wait_for(bar(B_XEMPTY + slot), uint32_t(item / A.slots - 1) & 1, ctl, A.err);
+      for (Units u(first, last, A); u.more() && ok; u.next(A)) {
+        const int xh = A.x_by_head ? u.h : 0, wh = A.w_by_head ? u.h : 0, n0 = u.n * A.nt, t0 = u.t * kRows;
+        for (int c = 0; c < A.chunks && ok; ++c) {
+          if (items >= A.slots) ok = wait_for(bar(B_XEMPTY + slot), phase, ctl, A.err);
           if (!ok) break;
           mbar_arrive_expect_tx(bar(B_XFULL + slot), kXSlot);
           tma_load_3d(base + off_x + slot * kXSlot, &A.x, c * kChunk, xh, t0, bar(B_XFULL + slot));
-          if (!fresh) continue;
+          items = items < A.slots ? items + 1 : items;
+          if (++slot == A.slots) slot = 0, phase ^= 1;
+          if (!u.fresh) continue;
           if (c == 0) {
             if (loads > 0) ok = wait_for(bar(B_WFREE), uint32_t(loads - 1) & 1, ctl, A.err);
-            if (!ok) {
-              ++item;
-              break;
-            }
-            ++loads, asked = 0, group = g;
+            if (!ok) break;
+            ++loads, asked = 0;
           }
           ++asked;
           const uint32_t dst = base + kOffData + c * w_chunk;
@@ -124,9 +142,11 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
           }
         }
       }
-      // what was asked for lands before the block ends, read or not
-      for (int64_t i = item > A.slots ? item - A.slots : 0; i < item; ++i)
-        drain(bar(B_XFULL + int(i % A.slots)), uint32_t(i / A.slots) & 1, A.err);
+      // what was asked for lands before the block ends, read or not: the last items, slot by slot backwards
+      for (int i = 0; i < items; ++i) {
+        if (--slot < 0) slot = A.slots - 1, phase ^= 1;
+        drain(bar(B_XFULL + slot), phase ^ 1, A.err);
+      }
       for (int c = 0; c < asked; ++c) drain(bar(B_WFULL + c), uint32_t(loads - 1) & 1, A.err);
     }
     __syncwarp();
@@ -138,18 +158,15 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
     auto arrived = [&](int b, uint32_t parity) {
       return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, A.err)) != 0;
     };
-    int64_t group = -1;
     int slot = 0, loads = 0, n = 0;
     uint32_t phase = 0;  // of the ring's slots
     bool ok = true;
-    for (int64_t u = first; u < last && ok; ++u, ++n) {
-      const int64_t g = u / A.m_tiles;
-      const bool fresh = g != group, change = u + 1 < last && (u + 1) / A.m_tiles != g;
-      if (fresh) ++loads, group = g;
+    for (Units u(first, last, A); u.more() && ok; u.next(A), ++n) {
+      if (u.fresh) ++loads;
       const int buf = n & 1;
       if (n >= 2) ok = arrived(B_ACCFREE + buf, uint32_t(n / 2 - 1) & 1);
       for (int c = 0; c < A.chunks && ok; ++c) {
-        if (fresh) ok = arrived(B_WFULL + c, uint32_t(loads - 1) & 1);
+        if (u.fresh) ok = arrived(B_WFULL + c, uint32_t(loads - 1) & 1);
         ok = ok && arrived(B_XFULL + slot, phase);
         if (!ok) break;
         tc_fence_after();
@@ -166,7 +183,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
       if (!ok) break;
       if (elect_one()) {
         mma_commit(bar(B_ACC + buf));
-        if (change) mma_commit(bar(B_WFREE));
+        if (u.changes(A)) mma_commit(bar(B_WFREE));
       }
     }
     if (elect_one()) {
@@ -177,24 +194,25 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
   } else {
     // ------------------------------------------------------------- sums to memory
     const int q = warp & 3;  // TMEM lane quarter
-    const uint32_t stage = base + off_out + uint32_t(q) * 2u * kBlockBytes;
-    int64_t n = 0;
-    int block = 0;
-    for (int64_t u = first; u < last; ++u, ++n) {
-      const int64_t g = u / A.m_tiles;
-      const int h = int(g / A.n_tiles), n0 = int(g % A.n_tiles) * A.nt;
-      const int64_t t0 = u % A.m_tiles * kRows + q * 32;
-      const int buf = int(n & 1);
+    const int blocks = A.nt > 128 ? 2 : 1;  // staged a warp
+    const uint32_t stage = base + off_out + uint32_t(q * blocks) * kBlockBytes;
+    int n = 0, block = 0;
+    for (Units u(first, last, A); u.more(); u.next(A), ++n) {
+      const int h = u.h, n0 = u.n * A.nt, buf = n & 1;
+      const int64_t t0 = int64_t(u.t) * kRows + q * 32;
       const bool ok = wait_for(bar(B_ACC + buf), uint32_t(n / 2) & 1, ctl, A.err);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const int width = t0 < A.tokens ? min(A.nt, A.n_dim - n0) : 0;  // a store starts inside the tensor, which clips it
-      for (int b = 0; b < width; b += 64, ++block) {
-        const uint32_t to = stage + uint32_t(block & 1) * kBlockBytes;
-        if (lane == 0) bulk_wait_group_read<1>();  // the store before last has read its block
-        __syncwarp();
+      for (int b = 0; b < width; b += 64, block ^= blocks - 1) {
+        const uint32_t to = stage + uint32_t(block) * kBlockBytes;
         uint32_t y[64];
         tmem_ld64_sync(tmem + (uint32_t(q * 32) << 16) + uint32_t(A.nt) * buf + b, y);
+        if (lane == 0) {  // the last store from this block has read it
+          if (blocks > 1) bulk_wait_group_read<1>();
+          else bulk_wait_group_read<0>();
+        }
+        __syncwarp();
 #pragma unroll
         for (int e = 0; e < 64; e += 8) {
           float f[8];
@@ -250,7 +268,7 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
   TensorArgs P = {};
   const int sms = sm_count();
   P.chunks = (A.k_dim + kChunk - 1) / kChunk;
-  P.m_tiles = (A.tokens + kRows - 1) / kRows;
+  P.m_tiles = int((A.tokens + kRows - 1) / kRows);
   // the widest tile whose weights fit and that still gives four of five SMs a unit: wide tiles read x
   // less often, narrow ones spread few tokens over the SMs
   P.nt = 64;
@@ -263,7 +281,7 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
   }
   P.n_tiles = (A.n_dim + P.nt - 1) / P.nt;
   P.units = int64_t(A.heads) * P.n_tiles * P.m_tiles;
-  const uint32_t fixed = 1024 + kOffData + uint32_t(P.chunks) * P.nt * 128u + 8 * kBlockBytes;
+  const uint32_t fixed = 1024 + kOffData + uint32_t(P.chunks) * P.nt * 128u + 4 * (P.nt > 128 ? 2 : 1) * kBlockBytes;
   P.slots = int((227u * 1024u - fixed) / kXSlot);
   if (P.slots > kMaxSlots) P.slots = kMaxSlots;
   const uint32_t smem = fixed + P.slots * kXSlot;
@@ -286,30 +304,30 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
 
 // The plain form, for any strides: a block a tile of 64 tokens x 64 outputs of
 // one head, 16 k at a time through shared memory, 4 x 4 sums a thread.
-constexpr int kTile = 64, kStep = 16;
+constexpr int kTile = 64, kSum = 16;
 
 template <typename T>
 __global__ void __launch_bounds__(256) head_product_plain_kernel(const ProductArgs A) {
-  __shared__ float xs[kStep][kTile + 1], ws[kStep][kTile + 1];
+  __shared__ float xs[kSum][kTile + 1], ws[kSum][kTile + 1];
   const int h = blockIdx.y, n0 = blockIdx.z * kTile, tid = threadIdx.x;
   const int64_t t0 = int64_t(blockIdx.x) * kTile;
   const T* x = static_cast<const T*>(A.x) + int64_t(h) * A.x_head;
   const T* w = static_cast<const T*>(A.w) + int64_t(h) * A.w_head;
   const int tx = tid % 16, ty = tid / 16;
   float sum[4][4] = {};
-  for (int k0 = 0; k0 < A.k_dim; k0 += kStep) {
-    for (int i = tid; i < kStep * kTile; i += 256) {
-      const int k = i % kStep, t = i / kStep;
+  for (int k0 = 0; k0 < A.k_dim; k0 += kSum) {
+    for (int i = tid; i < kSum * kTile; i += 256) {
+      const int k = i % kSum, t = i / kSum;
       xs[k][t] = (k0 + k < A.k_dim && t0 + t < A.tokens) ? to_float(x[(t0 + t) * A.x_tok + k0 + k]) : 0.f;
     }
-    for (int i = tid; i < kStep * kTile; i += 256) {
+    for (int i = tid; i < kSum * kTile; i += 256) {
       const int n = i % kTile, k = i / kTile;
       ws[k][n] = (k0 + k < A.k_dim && n0 + n < A.n_dim) ? to_float(w[(k0 + k) * A.w_k + (n0 + n) * A.w_n]) : 0.f;
     }
     __syncthreads();
     // values of k past the end are zero on both sides
 #pragma unroll
-    for (int k = 0; k < kStep; ++k)
+    for (int k = 0; k < kSum; ++k)
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll

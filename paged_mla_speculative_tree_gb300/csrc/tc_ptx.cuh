@@ -73,26 +73,6 @@ __device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t par
   return ok != 0;
 }
 
-// ---------------------------------------------------------------- launch control
-// Asks for a block of this grid that has not been launched yet: the 16-byte
-// answer arrives at `dst`, completing its bytes on `bar`.
-__device__ __forceinline__ void try_cancel(uint32_t dst, uint32_t bar) {
-  asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(dst),
-               "r"(bar)
-               : "memory");
-}
-// Whether the answer names a block (which this one now has to do), and its x.
-__device__ __forceinline__ bool read_cancelled(uint32_t at, unsigned& x) {
-  uint32_t some, bx;
-  asm volatile(
-      "{\n .reg .pred p;\n .reg .b128 r;\n .reg .b32 y, z;\n ld.shared.b128 r, [%2];\n"
-      " clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, r;\n selp.u32 %0, 1, 0, p;\n mov.u32 %1, 0;\n"
-      " @p clusterlaunchcontrol.query_cancel.get_first_ctaid.v4.b32.b128 {%1, y, z, _}, r;\n}"
-      : "=r"(some), "=r"(bx) : "r"(at) : "memory");
-  if (some) x = bx;
-  return some != 0;
-}
-
 // ---------------------------------------------------------------- cluster
 __device__ __forceinline__ uint32_t cluster_ctarank() {
   uint32_t r;
@@ -191,7 +171,6 @@ __device__ __forceinline__ void mma_commit(uint32_t bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
                : "memory");
 }
-
 // tcgen05.ld of 32 lanes x N consecutive 32-bit columns (thread t <- lane
 // taddr.lane + t), fused with tcgen05.wait::ld in the same asm statement so the
 // compiler cannot consume the destination registers before the load lands.
