@@ -113,36 +113,44 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
 
   if (warp == 0) {
     // ------------------------------------------------------------- copies
-    if (lane == 0) {
-      int slot = 0, items = 0, loads = 0, asked = 0;  // loads of weights, and chunks of the last one
-      uint32_t phase = 1;                             // of the slots' releases: the first round waits for none
-      bool ok = true;
-      for (Units u(first, last, A); u.more() && ok; u.next(A)) {
-        const int xh = A.x_by_head ? u.h : 0, wh = A.w_by_head ? u.h : 0, n0 = u.n * A.nt, t0 = u.t * kRows;
-        for (int c = 0; c < A.chunks && ok; ++c) {
-          if (items >= A.slots) ok = wait_for(bar(B_XEMPTY + slot), phase, ctl, A.err);
+    int slot = 0, items = 0, loads = 0, asked = 0;  // loads of weights, and chunks of the last one
+    uint32_t phase = 1;                             // of the slots' releases: the first round waits for none
+    const uint32_t data = uniform(base);
+    auto released = [&](int b, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, A.err)) != 0;
+    };
+    bool ok = true;
+    for (Units u(first, last, A); u.more() && ok; u.next(A)) {
+      const int xh = A.x_by_head ? u.h : 0, wh = A.w_by_head ? u.h : 0, n0 = u.n * A.nt, t0 = u.t * kRows;
+      for (int c = 0; c < A.chunks && ok; ++c) {
+        if (items >= A.slots) ok = released(B_XEMPTY + slot, phase);
+        if (!ok) break;
+        if (elect_one()) {
+          mbar_arrive_expect_tx(data + 8 * (B_XFULL + slot), kXSlot);
+          tma_load_3d(data + off_x + slot * kXSlot, &A.x, c * kChunk, xh, t0, data + 8 * (B_XFULL + slot));
+        }
+        items = items < A.slots ? items + 1 : items;
+        if (++slot == A.slots) slot = 0, phase ^= 1;
+        if (!u.fresh) continue;
+        if (c == 0) {
+          if (loads > 0) ok = released(B_WFREE, uint32_t(loads - 1) & 1);
           if (!ok) break;
-          mbar_arrive_expect_tx(bar(B_XFULL + slot), kXSlot);
-          tma_load_3d(base + off_x + slot * kXSlot, &A.x, c * kChunk, xh, t0, bar(B_XFULL + slot));
-          items = items < A.slots ? items + 1 : items;
-          if (++slot == A.slots) slot = 0, phase ^= 1;
-          if (!u.fresh) continue;
-          if (c == 0) {
-            if (loads > 0) ok = wait_for(bar(B_WFREE), uint32_t(loads - 1) & 1, ctl, A.err);
-            if (!ok) break;
-            ++loads, asked = 0;
-          }
-          ++asked;
-          const uint32_t dst = base + kOffData + c * w_chunk;
-          mbar_arrive_expect_tx(bar(B_WFULL + c), w_chunk);
+          ++loads, asked = 0;
+        }
+        ++asked;
+        if (elect_one()) {
+          const uint32_t dst = data + kOffData + c * w_chunk, full = data + 8 * (B_WFULL + c);
+          mbar_arrive_expect_tx(full, w_chunk);
           if (A.w_k_major) {
-            tma_load_3d(dst, &A.w, c * kChunk, wh, n0, bar(B_WFULL + c));
+            tma_load_3d(dst, &A.w, c * kChunk, wh, n0, full);
           } else {
-            for (int b = 0; b < A.nt; b += 64) tma_load_3d(dst + b * 128, &A.w, n0 + b, wh, c * kChunk, bar(B_WFULL + c));
+            for (int b = 0; b < A.nt; b += 64) tma_load_3d(dst + b * 128, &A.w, n0 + b, wh, c * kChunk, full);
           }
         }
       }
-      // what was asked for lands before the block ends, read or not: the last items, slot by slot backwards
+    }
+    // what was asked for lands before the block ends, read or not: the last items, slot by slot backwards
+    if (elect_one()) {
       for (int i = 0; i < items; ++i) {
         if (--slot < 0) slot = A.slots - 1, phase ^= 1;
         drain(bar(B_XFULL + slot), phase ^ 1, A.err);
