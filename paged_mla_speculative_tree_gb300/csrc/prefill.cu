@@ -60,7 +60,7 @@ constexpr int kSlots = 8;
 constexpr uint32_t kQStage = 3 * kSlot, kOffRing = 2 * kQStage, kOffBars = kOffRing + kSlots * kSlot;
 // K and V tile j use the barriers j & 1; both stages release every tile
 enum : int {
-  B_Q = 0, B_KFULL = 2, B_VFULL = 4, B_KFREE = 6, B_VFREE = 8, B_S = 10, B_P = 12, B_O = 14, B_FIN = 16, B_COUNT = 18
+  B_Q = 0, B_KFULL = 2, B_VFULL = 4, B_KFREE = 6, B_VFREE = 8, B_S = 10, B_P = 12, B_O = 16, B_FIN = 18, B_COUNT = 20
 };
 constexpr uint32_t kOffCtl = kOffBars + 8 * B_COUNT;
 constexpr uint32_t kSmem = kOffCtl + 16 + 1024;  // + slack for 1 KB alignment
@@ -139,7 +139,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   auto stage_tiles = [&](int s) { return s ? T1 : T0; };
 
   if (tid == 0) {
-    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_KFREE && i < B_S ? 2 : i == B_P || i == B_P + 1 ? 4 : 1);
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_KFREE && i < B_S ? 2 : i >= B_P && i < B_O ? 4 : 1);
     ctl->abort = 0;
     fence_mbar_init_cluster();
   }
@@ -161,43 +161,57 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   auto slot_at = [&](int item) { return base + kOffRing + uint32_t(item % kSlots) * kSlot; };
   if (warp == 10) {
     // ------------------------------------------------------------- copies
-    if (lane == 0 && TN > 0) {
+    if (TN > 0) {
       const int qh = A.q_by_head ? h : 0, kh = A.k_by_head ? h : 0, vh = A.v_by_head ? h : 0;
+      const uint32_t data = uniform(base), bars = uniform(bar(0));
+      auto released = [&](int b, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, A.err)) != 0;
+      };
       auto load_q = [&](int s) {
-        mbar_arrive_expect_tx(bar(B_Q + s), kQStage);
-        for (int c = 0; c < 3; ++c)
-          tma_load_3d(base + s * kQStage + c * kSlot, &A.q, 64 * c, qh, R.q0 + row0 + s * kStageRows, bar(B_Q + s));
+        if (stage_tiles(s) > 0 && elect_one()) {
+          mbar_arrive_expect_tx(bars + 8 * (B_Q + s), kQStage);
+          for (int c = 0; c < 3; ++c)
+            tma_load_3d(data + s * kQStage + c * kSlot, &A.q, 64 * c, qh, R.q0 + row0 + s * kStageRows, bars + 8 * (B_Q + s));
+        }
       };
       bool ok = true;
       int k_asked = 0, v_asked = 0;
-      if (stage_tiles(0) > 0) load_q(0);
+      load_q(0);
       for (int j = 0; j < TN; ++j) {
         // slots in the order of their use: K(j)'s first was K(j - 2)'s last, its others V(j - 2)'s, V(j)'s K(j - 1)'s first
         const int row = R.k0 + (begin + j) * kKeys;
-        if (j >= 2) ok = wait_for(bar(B_KFREE + (j & 1)), uint32_t(j / 2 - 1) & 1, ctl, A.err) &&
-                         wait_for(bar(B_VFREE + (j & 1)), uint32_t(j / 2 - 1) & 1, ctl, A.err);
+        if (j >= 2) ok = released(B_KFREE + (j & 1), uint32_t(j / 2 - 1) & 1) && released(B_VFREE + (j & 1), uint32_t(j / 2 - 1) & 1);
         if (!ok) break;
-        const uint32_t kf = bar(B_KFULL + (j & 1)), vf = bar(B_VFULL + (j & 1));
-        mbar_arrive_expect_tx(kf, 3 * kSlot);
-        tma_load_3d(slot_at(5 * j), &A.k_nope, 0, kh, row, kf);
-        tma_load_3d(slot_at(5 * j + 1), &A.k_nope, 64, kh, row, kf);
-        tma_load_3d(slot_at(5 * j + 2), &A.k_rope, 0, 0, row, kf);
+        if (elect_one()) {
+          const uint32_t kf = bars + 8 * (B_KFULL + (j & 1));
+          mbar_arrive_expect_tx(kf, 3 * kSlot);
+          tma_load_3d(data + kOffRing + (5 * j) % kSlots * kSlot, &A.k_nope, 0, kh, row, kf);
+          tma_load_3d(data + kOffRing + (5 * j + 1) % kSlots * kSlot, &A.k_nope, 64, kh, row, kf);
+          tma_load_3d(data + kOffRing + (5 * j + 2) % kSlots * kSlot, &A.k_rope, 0, 0, row, kf);
+        }
         ++k_asked;
-        if (j == 0 && stage_tiles(1) > 0) load_q(1);
-        if (j >= 1) ok = wait_for(bar(B_KFREE + ((j - 1) & 1)), uint32_t((j - 1) / 2) & 1, ctl, A.err);
+        if (j == 0) load_q(1);
+        if (j >= 1) ok = released(B_KFREE + ((j - 1) & 1), uint32_t((j - 1) / 2) & 1);
         if (!ok) break;
-        mbar_arrive_expect_tx(vf, 2 * kSlot);
-        for (int c = 0; c < 2; ++c) {
-          tma_load_3d(slot_at(5 * j + 3 + c), &A.v, 0, vh, row + 64 * c, vf);
-          tma_load_3d(slot_at(5 * j + 3 + c) + kSlot / 2, &A.v, 64, vh, row + 64 * c, vf);
+        if (elect_one()) {
+          const uint32_t vf = bars + 8 * (B_VFULL + (j & 1));
+          mbar_arrive_expect_tx(vf, 2 * kSlot);
+#pragma unroll
+          for (int c = 0; c < 2; ++c) {
+            const uint32_t dst = data + kOffRing + (5 * j + 3 + c) % kSlots * kSlot;
+            tma_load_3d(dst, &A.v, 0, vh, row + 64 * c, vf);
+            tma_load_3d(dst + kSlot / 2, &A.v, 64, vh, row + 64 * c, vf);
+          }
         }
         ++v_asked;
       }
       // what was asked for lands before the block ends, read or not (a second stage's Q is asked for with the first tile)
-      for (int s = 0; s < 2; ++s)
-        if (stage_tiles(s) > 0) drain(bar(B_Q + s), 0, A.err);
-      for (int j = max(0, k_asked - 2); j < k_asked; ++j) drain(bar(B_KFULL + (j & 1)), uint32_t(j / 2) & 1, A.err);
-      for (int j = max(0, v_asked - 2); j < v_asked; ++j) drain(bar(B_VFULL + (j & 1)), uint32_t(j / 2) & 1, A.err);
+      if (elect_one()) {
+        for (int s = 0; s < 2; ++s)
+          if (stage_tiles(s) > 0) drain(bar(B_Q + s), 0, A.err);
+        for (int j = max(0, k_asked - 2); j < k_asked; ++j) drain(bar(B_KFULL + (j & 1)), uint32_t(j / 2) & 1, A.err);
+        for (int j = max(0, v_asked - 2); j < v_asked; ++j) drain(bar(B_VFULL + (j & 1)), uint32_t(j / 2) & 1, A.err);
+      }
     }
     __syncwarp();
   } else if (warp >= 8) {
@@ -206,7 +220,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     constexpr uint32_t id_qk = kBf16 ? idesc_bf16_f32(128, 128, 0, 0) : idesc_fp16_f32(128, 128, 0, 0);
     constexpr uint32_t id_pv = kBf16 ? idesc_bf16_f32(128, 128, 0, 1) : idesc_fp16_f32(128, 128, 0, 1);
     const int s = warp - 8, Ts = stage_tiles(s);
-    const uint32_t tmem_s = tmem + kTmemS + 128 * s, tmem_o = tmem + kTmemO + 128 * s;
+    const uint32_t tmem_s = uniform(tmem) + kTmemS + 128 * s, tmem_o = uniform(tmem) + kTmemO + 128 * s, data = uniform(base);
+    auto slot_of = [&](int item) { return data + kOffRing + uint32_t(item % kSlots) * kSlot; };
     auto arrived = [&](int b, uint32_t parity) {
       return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, A.err)) != 0;
     };
@@ -216,8 +231,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (elect_one()) {
 #pragma unroll
         for (int c = 0; c < 3; ++c) {
-          const uint64_t a = smem_desc(base + s * kQStage + c * kSlot, 16, 1024, kSwizzle128B);
-          const uint64_t b = smem_desc(slot_at(5 * j + c), 16, 1024, kSwizzle128B);
+          const uint64_t a = smem_desc(data + s * kQStage + c * kSlot, 16, 1024, kSwizzle128B);
+          const uint64_t b = smem_desc(slot_of(5 * j + c), 16, 1024, kSwizzle128B);
 #pragma unroll
           for (int k = 0; k < 4; ++k) mma_ss(tmem_s, desc_add(a, 32 * k), desc_add(b, 32 * k), id_qk, c + k > 0);
         }
@@ -229,15 +244,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     auto pv = [&](int j) -> bool {  // O += P V(j)
       if (!arrived(B_VFULL + (j & 1), uint32_t(j / 2) & 1)) return false;
       const int keys = min(kKeys, R.len - (begin + j) * kKeys);
-      const uint64_t v0 = smem_desc(slot_at(5 * j + 3), kSlot / 2, 1024, kSwizzle128B);
-      const uint64_t v1 = smem_desc(slot_at(5 * j + 4), kSlot / 2, 1024, kSwizzle128B);
+      const uint64_t v0 = smem_desc(slot_of(5 * j + 3), kSlot / 2, 1024, kSwizzle128B);
+      const uint64_t v1 = smem_desc(slot_of(5 * j + 4), kSlot / 2, 1024, kSwizzle128B);
       if (keys == kKeys) {
-        if (!arrived(B_P + s, j & 1)) return false;
+        if (!arrived(B_P + 2 * s, j & 1)) return false;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
-          for (int k = 0; k < 8; ++k)
-            mma_ts(tmem_o, tmem_s + 8 * k, desc_add(k < 4 ? v0 : v1, 2048 * (k & 3)), id_pv, j > 0 || k > 0);
+          for (int k = 0; k < 4; ++k) mma_ts(tmem_o, tmem_s + 8 * k, desc_add(v0, 2048 * k), id_pv, j > 0 || k > 0);
+        }
+        if (!arrived(B_P + 2 * s + 1, j & 1)) return false;
+        tc_fence_after();
+        if (elect_one()) {
+#pragma unroll
+          for (int k = 4; k < 8; ++k) mma_ts(tmem_o, tmem_s + 8 * k, desc_add(v1, 2048 * (k & 3)), id_pv, 1);
           mma_commit(bar(B_VFREE + (j & 1)));
           if (j + 1 == Ts) mma_commit(bar(B_O + s));
         }
@@ -249,11 +269,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const int steps = (keys + 15) / 16;
       for (int u = 16 * keys + lane; u < 256 * steps; u += 32) {  // 16-byte units, 16 a row
         const int key = u / 16, part = u % 16;
-        st_shared_v4(slot_at(5 * j + 3 + key / 64) + (part / 8) * (kSlot / 2) + (key % 64) * 128 + (part % 8) * 16, 0, 0, 0, 0);
+        st_shared_v4(slot_of(5 * j + 3 + key / 64) + (part / 8) * (kSlot / 2) + (key % 64) * 128 + (part % 8) * 16, 0, 0, 0, 0);
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (!arrived(B_P + s, j & 1)) return false;
+      if (!arrived(B_P + 2 * s, j & 1) || !arrived(B_P + 2 * s + 1, j & 1)) return false;
       tc_fence_after();
       if (elect_one()) {
         for (int k = 0; k < steps; ++k)
@@ -293,8 +313,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     end -= begin * kKeys, clear -= begin * kKeys;  // from the block's first tile on
     float m = -INFINITY, l = 0.f;
     bool ok = true;
-    uint32_t x[128] = {};
     for (int j = 0; j < Ts; ++j) {
+      uint32_t x[128];
       ok = wait_for(bar(B_S + s), j & 1, ctl, A.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
@@ -322,12 +342,12 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         l *= keep;
         const uint32_t o = tmem + lanes + kTmemO + 128 * s;
 #pragma unroll 1
-        for (int u = 0; u < 128; u += 32) {
-          uint32_t y[32];
-          tmem_ld32_sync(o + u, y);
+        for (int u = 0; u < 128; u += 16) {
+          uint32_t y[16];
+          tmem_ld16_sync(o + u, y);
 #pragma unroll
-          for (int e = 0; e < 32; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * keep);
-          tmem_st32_sync(o + u, y);
+          for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * keep);
+          tmem_st16_sync(o + u, y);
         }
       }
       if (move) m = top;
@@ -346,10 +366,10 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           x[64 * half + u] = join(a, b, T());  // in place: the register is read already
         }
         tmem_st32_sync(tmem + lanes + kTmemS + 128 * s + 32 * half, reinterpret_cast<const uint32_t(&)[32]>(x[64 * half]));
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(bar(B_P + 2 * s + half));
       }
-      tc_fence_before();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(bar(B_P + s));
       float a, b;
       f2_unpack(f2_add(sum0, sum1), a, b);
       l += a + b;
@@ -360,7 +380,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const float inv = some ? 1.f / l : 0.f;
       const int live = min(32, R.n - i0);
       tc_fence_after();
-      if (Ts > 0) tmem_ld128_sync(tmem + lanes + kTmemO + 128 * s, x);
+      uint32_t x[128];
+      tmem_ld128_sync(tmem + lanes + kTmemO + 128 * s, x);  // anything, where the stage had no tile
       // rows to memory through this stage's part of Q (every product that read it has run), so
       // that a warp stores whole rows; 16-byte units are swizzled by the row
       const uint32_t mine_s = base + s * kQStage + uint32_t((warp & 3) * 32) * 256u;
