@@ -60,7 +60,7 @@ constexpr int kSlots = 8;
 constexpr uint32_t kQStage = 3 * kSlot, kOffRing = 2 * kQStage, kOffBars = kOffRing + kSlots * kSlot;
 // K and V tile j use the barriers j & 1; both stages release every tile
 enum : int {
-  B_Q = 0, B_KFULL = 2, B_VFULL = 4, B_KFREE = 6, B_VFREE = 8, B_S = 10, B_P = 12, B_O = 16, B_FIN = 18, B_COUNT = 20
+  B_Q = 0, B_KFULL = 2, B_VFULL = 4, B_KFREE = 6, B_VFREE = 8, B_S = 10, B_P = 12, B_O = 16, B_FIN = 18, B_TURN = 20, B_COUNT = 22
 };
 constexpr uint32_t kOffCtl = kOffBars + 8 * B_COUNT;
 constexpr uint32_t kSmem = kOffCtl + 16 + 1024;  // + slack for 1 KB alignment
@@ -180,16 +180,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       for (int j = 0; j < TN; ++j) {
         // slots in the order of their use: K(j)'s first was K(j - 2)'s last, its others V(j - 2)'s, V(j)'s K(j - 1)'s first
         const int row = R.k0 + (begin + j) * kKeys;
-        if (j >= 2) ok = released(B_KFREE + (j & 1), uint32_t(j / 2 - 1) & 1) && released(B_VFREE + (j & 1), uint32_t(j / 2 - 1) & 1);
+        if (j >= 2) ok = released(B_KFREE + (j & 1), uint32_t(j / 2 - 1) & 1);
         if (!ok) break;
+        const uint32_t kf = bars + 8 * (B_KFULL + (j & 1));
         if (elect_one()) {
-          const uint32_t kf = bars + 8 * (B_KFULL + (j & 1));
           mbar_arrive_expect_tx(kf, 3 * kSlot);
           tma_load_3d(data + kOffRing + (5 * j) % kSlots * kSlot, &A.k_nope, 0, kh, row, kf);
-          tma_load_3d(data + kOffRing + (5 * j + 1) % kSlots * kSlot, &A.k_nope, 64, kh, row, kf);
-          tma_load_3d(data + kOffRing + (5 * j + 2) % kSlots * kSlot, &A.k_rope, 0, 0, row, kf);
         }
         ++k_asked;
+        if (j >= 2) ok = released(B_VFREE + (j & 1), uint32_t(j / 2 - 1) & 1);
+        if (elect_one()) {
+          if (ok) {
+            tma_load_3d(data + kOffRing + (5 * j + 1) % kSlots * kSlot, &A.k_nope, 64, kh, row, kf);
+            tma_load_3d(data + kOffRing + (5 * j + 2) % kSlots * kSlot, &A.k_rope, 0, 0, row, kf);
+          } else {
+            mbar_complete_tx(kf, 2 * kSlot);  // the first is on its way: its barrier expects no more
+          }
+        }
+        if (!ok) break;
         if (j == 0) load_q(1);
         if (j >= 1) ok = released(B_KFREE + ((j - 1) & 1), uint32_t((j - 1) / 2) & 1);
         if (!ok) break;
@@ -225,6 +233,20 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     auto arrived = [&](int b, uint32_t parity) {
       return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, A.err)) != 0;
     };
+    // Where both stages have work they take turns, 0 1 0 1 ...: O += P V(j) and the next S are
+    // one turn.  Left to themselves they drift into step, share the tensor core while both have
+    // work for it and leave it idle while both compute weights (8,192 tokens: 914 us, not 836).
+    const bool turns = T0 > 0 && T1 > 0;
+    int step = 0;
+    auto my_turn = [&]() -> bool {
+      if (!turns) return true;
+      const bool go = s ? arrived(B_TURN + 1, step & 1) : step == 0 || arrived(B_TURN, (step - 1) & 1);
+      ++step;
+      return go;
+    };
+    auto turn_over = [&]() {
+      if (turns && elect_one()) mbar_arrive(bar(B_TURN + 1 - s));
+    };
     auto qk = [&](int j) -> bool {  // S = Q K(j)^T
       if (!arrived(B_KFULL + (j & 1), uint32_t(j / 2) & 1)) return false;
       tc_fence_after();
@@ -237,6 +259,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           for (int k = 0; k < 4; ++k) mma_ss(tmem_s, desc_add(a, 32 * k), desc_add(b, 32 * k), id_qk, c + k > 0);
         }
         mma_commit(bar(B_S + s));
+        if (turns) mbar_arrive(bar(B_TURN + 1 - s));
         mma_commit(bar(B_KFREE + (j & 1)));
       }
       return true;
@@ -247,7 +270,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const uint64_t v0 = smem_desc(slot_of(5 * j + 3), kSlot / 2, 1024, kSwizzle128B);
       const uint64_t v1 = smem_desc(slot_of(5 * j + 4), kSlot / 2, 1024, kSwizzle128B);
       if (keys == kKeys) {
-        if (!arrived(B_P + 2 * s, j & 1)) return false;
+        if (!arrived(B_P + 2 * s, j & 1) || !my_turn()) return false;
         tc_fence_after();
         if (elect_one()) {
 #pragma unroll
@@ -273,7 +296,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       fence_proxy_async_smem();
       __syncwarp();
-      if (!arrived(B_P + 2 * s, j & 1) || !arrived(B_P + 2 * s + 1, j & 1)) return false;
+      if (!arrived(B_P + 2 * s, j & 1) || !arrived(B_P + 2 * s + 1, j & 1) || !my_turn()) return false;
       tc_fence_after();
       if (elect_one()) {
         for (int k = 0; k < steps; ++k)
@@ -284,16 +307,24 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       return true;
     };
     // a tile that this stage has no use for is released as soon as it is there
-    auto pass = [&](int full, int free, int j) -> bool {
-      if (!arrived(full + (j & 1), uint32_t(j / 2) & 1)) return false;
-      if (elect_one()) mbar_arrive(bar(free + (j & 1)));
+    auto pass_k = [&](int j) -> bool {
+      if (!arrived(B_KFULL + (j & 1), uint32_t(j / 2) & 1)) return false;
+      if (elect_one()) mbar_arrive(bar(B_KFREE + (j & 1)));
+      turn_over();
+      return true;
+    };
+    auto pass_v = [&](int j) -> bool {
+      if (!arrived(B_VFULL + (j & 1), uint32_t(j / 2) & 1) || !my_turn()) return false;
+      if (elect_one()) mbar_arrive(bar(B_VFREE + (j & 1)));
       return true;
     };
     bool ok = Ts == 0 || arrived(B_Q + s, 0);
-    if (ok && TN > 0) ok = Ts > 0 ? qk(0) : pass(B_KFULL, B_KFREE, 0);
+    if (ok && TN > 0) ok = my_turn() && (Ts > 0 ? qk(0) : pass_k(0));
     for (int j = 0; j < TN && ok; ++j) {
-      ok = j < Ts ? pv(j) : pass(B_VFULL, B_VFREE, j);
-      if (ok && j + 1 < TN) ok = j + 1 < Ts ? qk(j + 1) : pass(B_KFULL, B_KFREE, j + 1);
+      ok = j < Ts ? pv(j) : pass_v(j);
+      if (!ok) break;
+      if (j + 1 >= TN) turn_over();
+      else ok = j + 1 < Ts ? qk(j + 1) : pass_k(j + 1);
     }
     if (Ts > 0 && elect_one()) {  // every MMA issued has run once this arrives
       mma_commit(bar(B_FIN + s));
