@@ -71,8 +71,8 @@ extern "C" {
  *                gave up.
  *
  * Any strides are taken.  The tensor-core kernel runs where every address and
- * every stride but the innermost is a multiple of 16 bytes and w is dense in k
- * or in n; other layouts take a plain kernel.
+ * every stride but the innermost is a multiple of 16 bytes, n_dim is a multiple
+ * of 8 and w is dense in k or in n; other layouts take a plain kernel.
  */
 int mla_head_product(const void* x, int64_t x_tok_stride, int64_t x_head_stride, const void* w,
                      int64_t w_head_stride, int64_t w_k_stride, int64_t w_n_stride, void* out,
@@ -115,7 +115,7 @@ int mla_prefill_workspace(int num_sms, int bs, int64_t max_q, int64_t max_kv, in
  * num_heads      0 .. MTV_MAX_HEADS.
  * dtype          MTV_DTYPE_BF16 or MTV_DTYPE_FP16: q, k_nope, k_rope, v, out.
  *                All their addresses and strides are multiples of 16 bytes.
- * scale          finite, > 0.
+ * scale          > 0, finite also as a multiple of log2(e).
  * causal         0 or 1.
  * out            device, [num_q, heads, 128] with strides as q.
  * lse            device, fp32 [num_q, heads], or NULL to leave it out.

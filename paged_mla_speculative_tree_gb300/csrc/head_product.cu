@@ -257,8 +257,10 @@ int sm_count() {
   return sms;
 }
 
-// Whether tensor maps take the layout: 16-byte addresses and strides, w dense in k or n.
+// Whether tensor maps take the layout: 16-byte addresses and strides, w dense in k or n, and
+// whole 16 bytes of outputs (a bulk store writes what is left of its last 16 bytes as zeros).
 bool tensor_form(const ProductArgs& A) {
+  if (A.n_dim % 8 != 0) return false;
   const uintptr_t bits = reinterpret_cast<uintptr_t>(A.x) | reinterpret_cast<uintptr_t>(A.w) | reinterpret_cast<uintptr_t>(A.out);
   if (bits & 15) return false;
   const bool k_major = A.w_k == 1, n_major = A.w_n == 1;

@@ -574,7 +574,7 @@ extern "C" int mla_prefill_run(const void* q, int64_t q_tok_stride, int64_t q_he
   if (bs < 0 || bs > MTV_MAX_HEADS || max_q < 0 || max_kv < 0 || num_q < 0 || num_kv < 0 ||
       max_q > MTV_MAX_PREFILL_ROWS || max_kv > MTV_MAX_PREFILL_ROWS || num_q > MTV_MAX_PREFILL_ROWS ||
       num_kv > MTV_MAX_PREFILL_ROWS || num_heads < 0 ||
-      num_heads > MTV_MAX_HEADS || (dtype != MTV_DTYPE_BF16 && dtype != MTV_DTYPE_FP16) || !isfinite(scale) ||
+      num_heads > MTV_MAX_HEADS || (dtype != MTV_DTYPE_BF16 && dtype != MTV_DTYPE_FP16) || !isfinite(scale * mtv::kLog2e) ||
       !(scale > 0) || (causal != 0 && causal != 1) || nsplit < 1 || nsplit > MTV_MAX_PREFILL_SPLITS)
     return MTV_E_BAD_ARGUMENT;
   if (nsplit > 1) {

@@ -108,6 +108,56 @@ def test_head_product_reads_nothing_beyond_its_operands(tokens, k, n):
     check_product(x[:tokens, 1:3, :k], v[1:3, :n, :k].transpose(1, 2), pad_dim=8)
 
 
+@pytest.mark.parametrize("tokens,heads,k,n", [(3, 2, 7, 5), (129, 1, 65, 129), (40, 3, 1, 70), (200, 2, 130, 1), (257, 5, 513, 63),
+                                              (3, 2, 7, 8), (129, 1, 65, 136), (40, 3, 1, 72), (257, 5, 513, 64)])
+@pytest.mark.parametrize("dense", ["n", "k"])
+def test_head_product_of_odd_sizes_in_aligned_rows(tokens, heads, k, n, dense):
+    """Rows of whole 16 bytes that the operands and outputs only partly fill; NaN behind the operands."""
+    up = lambda v: (v + 7) // 8 * 8 + 8  # noqa: E731
+    x = torch.full((tokens, heads, up(k)), math.nan, dtype=torch.float16, device=DEV)
+    x[:, :, :k] = rnd(k, (tokens, heads, k), torch.float16)
+    w = torch.full((heads, k + 1, up(n)) if dense == "n" else (heads, n + 1, up(k)), math.nan, dtype=torch.float16, device=DEV)
+    inner = rnd(n, (heads, k, n), torch.float16)
+    w[:, :(k if dense == "n" else n), :(n if dense == "n" else k)] = inner if dense == "n" else inner.transpose(1, 2)
+    view = w[:, :k, :n] if dense == "n" else w[:, :n, :k].transpose(1, 2)
+    check_product(x[:, :, :k], view, pad_dim=up(n) - n)
+
+
+def test_head_product_of_shared_weights_and_head_major_rows():
+    """One weight for every head by its stride; operands and outputs with heads outside tokens."""
+    x = rnd(1, (6, 150, 96), torch.bfloat16).transpose(0, 1)
+    w = rnd(2, (1, 96, 200), torch.bfloat16).expand(6, 96, 200)
+    out = torch.empty((6, 150, 200), dtype=torch.bfloat16, device=DEV).transpose(0, 1)
+    pkg.head_product(x, w, out)
+    ref, mag = L.head_product(x, w)
+    within(out, ref, product_bound(ref, mag, 96, torch.bfloat16))
+
+
+def test_calls_on_two_streams_at_once():
+    """Products and split attention on two streams with buffers of their own, again and again."""
+    jobs = []
+    for i in range(2):
+        b = prefill_batch(50 + i, [(40, 4000 + i)], 2, torch.bfloat16)
+        p = pkg.MlaPrefill(1, 40, 43, 4001, 2)
+        x, w = rnd(60 + i, (300, 8, 128), torch.bfloat16), rnd(70 + i, (8, 128, 512), torch.bfloat16)
+        args = (b["q"], b["k_nope"], b["k_rope"], b["v"], i64(b["qo"]), i32(b["kv"]), 0.07)
+        want = torch.empty((300, 8, 512), dtype=torch.bfloat16, device=DEV)
+        pkg.head_product(x, w, want)
+        jobs.append((p, args, [t.clone() for t in p(*args)], x, w, want, torch.cuda.Stream(), []))
+    torch.cuda.synchronize()
+    for _ in range(10):
+        for p, args, _, x, w, want, stream, got in jobs:
+            with torch.cuda.stream(stream):
+                out = torch.empty_like(want)
+                pkg.head_product(x, w, out)
+                got.append((p(*args), out))
+    torch.cuda.synchronize()
+    for p, _, attention, _, _, want, _, got in jobs:
+        assert p.nsplit > 1 and p.device_error() == 0
+        for (out, lse), product in got:
+            assert torch.equal(out, attention[0]) and torch.equal(lse, attention[1]) and torch.equal(product, want)
+
+
 def test_head_product_keeps_rows_apart():
     """A row of NaN or infinity spoils its own outputs only."""
     x, w = rnd(5, (200, 2, 128), torch.bfloat16), rnd(6, (2, 128, 512), torch.bfloat16)
@@ -198,6 +248,8 @@ CASES = {
     "ragged": [(3, 3), (0, 7), (129, 200), (1, 64), (64, 65), (0, 0), (5, 127)],
     "fewer keys": [(9, 4), (140, 130), (6, 0), (2, 2)],
     "short": [(2, 2)] * 9,
+    "first rows without keys": [(300, 150), (600, 100), (257, 1)],
+    "many blocks": [(700, 1000), (513, 513)],
 }
 
 
@@ -267,6 +319,14 @@ def test_prefill_keeps_requests_apart(nsplit):
                         nsplit=nsplit, workspace=ws)
         for rows in (slice(0, 50), slice(80, 140)):
             assert torch.equal(out[rows], want[rows]) and torch.equal(lse[rows], want_lse[rows])
+
+
+def test_prefill_of_keys_and_values_shared_by_the_heads():
+    """Head strides of zero: the heads' queries over the same keys and values."""
+    b = prefill_batch(27, [(50, 90), (130, 140)], 4, torch.bfloat16)
+    b["k_nope"] = b["k_nope"][:, :1].expand(-1, 4, -1)
+    b["v"] = b["v"][:, :1].expand(-1, 4, -1)
+    check_prefill(b, torch.bfloat16)
 
 
 def test_prefill_is_the_same_each_time_and_alone_or_in_a_batch():

@@ -124,7 +124,7 @@ def prefill(lib, **kw):
 def test_prefill_refusals(lib):
     for kw in (dict(bs=-1), dict(bs=65536), dict(max_q=-1), dict(max_kv=-1), dict(max_q=1 << 31), dict(max_kv=1 << 31),
                dict(num_q=-1), dict(num_kv=1 << 31), dict(heads=65536), dict(dtype=2), dict(scale=0.0), dict(scale=-1.0),
-               dict(scale=math.inf), dict(scale=math.nan), dict(causal=2), dict(nsplit=0), dict(nsplit=65)):
+               dict(scale=math.inf), dict(scale=math.nan), dict(scale=3e38), dict(causal=2), dict(nsplit=0), dict(nsplit=65)):
         assert prefill(lib, **kw) == -3, kw
     for name in ("q_tok", "q_head", "k_tok", "k_head", "kr_tok", "v_tok", "v_head", "o_tok", "o_head"):
         assert prefill(lib, **{name: PREFILL[name] + 4}) == -3, name
