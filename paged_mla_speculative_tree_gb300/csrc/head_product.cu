@@ -59,6 +59,7 @@ struct TensorArgs {
   CUtensorMap x, w, out;
   uint32_t* err;
   int64_t units, tokens;   // units: heads * n_tiles * m_tiles
+  uint32_t x_bytes;        // of a copy of x: 64 k of 128 tokens, or of as many as there are
   int m_tiles, n_tiles, nt, chunks, slots, w_k_major, x_by_head, w_by_head, out_by_head, n_dim;
 };
 
@@ -117,7 +118,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
     uint32_t phase = 1;                             // of the slots' releases: the first round waits for none
     const uint32_t data = uniform(base);
     auto released = [&](int b, uint32_t parity) {
-      return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, A.err)) != 0;
+      return __all_sync(0xffffffffu, wait_for_call(bar(b), parity, ctl, A.err)) != 0;
     };
     bool ok = true;
     for (Units u(first, last, A); u.more() && ok; u.next(A)) {
@@ -126,7 +127,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
         if (items >= A.slots) ok = released(B_XEMPTY + slot, phase);
         if (!ok) break;
         if (elect_one()) {
-          mbar_arrive_expect_tx(data + 8 * (B_XFULL + slot), kXSlot);
+          mbar_arrive_expect_tx(data + 8 * (B_XFULL + slot), A.x_bytes);
           tma_load_3d(data + off_x + slot * kXSlot, &A.x, c * kChunk, xh, t0, data + 8 * (B_XFULL + slot));
         }
         items = items < A.slots ? items + 1 : items;
@@ -164,7 +165,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
                                                               : idesc_fp16_f32(kRows, A.nt, 0, A.w_k_major ? 0 : 1);
     const uint32_t w_step = A.w_k_major ? 32u : 2048u, acc = uniform(tmem), data = uniform(base);
     auto arrived = [&](int b, uint32_t parity) {
-      return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, A.err)) != 0;
+      return __all_sync(0xffffffffu, wait_for_call(bar(b), parity, ctl, A.err)) != 0;
     };
     int slot = 0, loads = 0, n = 0;
     uint32_t phase = 0;  // of the ring's slots
@@ -208,7 +209,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
     for (Units u(first, last, A); u.more(); u.next(A), ++n) {
       const int h = u.h, n0 = u.n * A.nt, buf = n & 1;
       const int64_t t0 = int64_t(u.t) * kRows + q * 32;
-      const bool ok = wait_for(bar(B_ACC + buf), uint32_t(n / 2) & 1, ctl, A.err);
+      const bool ok = wait_for_call(bar(B_ACC + buf), uint32_t(n / 2) & 1, ctl, A.err);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const int width = t0 < A.tokens ? min(A.nt, A.n_dim - n0) : 0;  // a store starts inside the tensor, which clips it
@@ -296,11 +297,15 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
   if (P.slots > kMaxSlots) P.slots = kMaxSlots;
   const uint32_t smem = fixed + P.slots * kXSlot;
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  // a copy takes time by its box, inside the tensor or not, so few tokens get a lower one; what the
+  // slot holds below it makes sums that nobody stores
+  const int x_rows = A.tokens < kRows ? int(A.tokens + 7) / 8 * 8 : kRows;
+  P.x_bytes = uint32_t(x_rows) * kChunk * 2;
   P.w_k_major = A.w_k == 1;
   P.x_by_head = A.x_head != 0, P.w_by_head = A.w_head != 0, P.out_by_head = 1;
   if (A.heads == 1) P.x_by_head = P.w_by_head = P.out_by_head = 0;
   P.err = A.err, P.tokens = A.tokens, P.n_dim = A.n_dim;
-  const bool maps = encode_heads_map(&P.x, bf16, A.x, A.tokens, A.x_tok, A.heads, A.x_head, A.k_dim, 64, kRows) &&
+  const bool maps = encode_heads_map(&P.x, bf16, A.x, A.tokens, A.x_tok, A.heads, A.x_head, A.k_dim, 64, x_rows) &&
                     (P.w_k_major ? encode_heads_map(&P.w, bf16, A.w, A.n_dim, A.w_n, A.heads, A.w_head, A.k_dim, 64, P.nt)
                                  : encode_heads_map(&P.w, bf16, A.w, A.k_dim, A.w_k, A.heads, A.w_head, A.n_dim, 64, 64)) &&
                     encode_heads_map(&P.out, bf16, A.out, A.tokens, A.out_tok, A.heads, A.out_head, A.n_dim, 64, 32);

@@ -17,7 +17,7 @@ struct Ctl {
 };
 
 // False when the wait gave up or another one of the block has.
-static __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err) {
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err) {
   const long long t0 = clock64();
   while (!ptx::mbar_try_wait(bar, parity)) {
     if (ctl->abort) return false;
@@ -32,8 +32,16 @@ static __device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, 
 __device__ __forceinline__ bool wait_for(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err) {
   return ptx::mbar_try_wait(bar, parity) || wait_slow(bar, parity, ctl, err);
 }
-// The same for what has to land before the block may end: ignores the flag.
-static __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, uint32_t* err) {
+// The same with the slow way as a call: less code, but a call's convention costs a
+// kernel without registers to spare its spills (prefill.cu).
+static __device__ __noinline__ bool wait_slow_call(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err) {
+  return wait_slow(bar, parity, ctl, err);
+}
+__device__ __forceinline__ bool wait_for_call(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err) {
+  return ptx::mbar_try_wait(bar, parity) || wait_slow_call(bar, parity, ctl, err);
+}
+// For what has to land before the block may end: ignores the flag.
+__device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, uint32_t* err) {
   const long long t0 = clock64();
   while (!ptx::mbar_try_wait(bar, parity))
     if (clock64() - t0 > kWaitCycles) {
