@@ -160,7 +160,7 @@ __device__ __forceinline__ uint4 load16(const void* p) { return *static_cast<con
 // NN, NR: units of the plain part and units (half layout: pairs of them) of the
 // rotated part that a lane may hold.
 template <typename T, bool kHalf, int NN, int NR>
-__global__ void __launch_bounds__(kVecThreads, NN <= 2 ? 3 : 1) norm_rope_vec_kernel(const NormArgs A) {
+__global__ void __launch_bounds__(kVecThreads, NN <= 2 ? 4 : 1) norm_rope_vec_kernel(const NormArgs A) {
   constexpr int V = 16 / int(sizeof(T)), M = kHalf ? 2 : 1;
   constexpr int kLatentUnits = kDLat / V / 32;
   __shared__ __align__(16) float cos_s[MTV_MAX_ROPE_DIM / 2], sin_s[MTV_MAX_ROPE_DIM / 2];
