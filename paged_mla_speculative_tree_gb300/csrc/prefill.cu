@@ -408,53 +408,59 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     if (ok && Ts > 0) ok = __all_sync(0xffffffffu, wait_for(bar(B_O + s), 0, ctl, A.err));
     if (ok && i0 < R.n) {
       const bool some = l != 0.f;  // true for a NaN too, which the row then shows
-      const float inv = some ? 1.f / l : 0.f;
+      const float inv = some ? __frcp_rn(l) : 0.f;
       const int live = min(32, R.n - i0);
-      tc_fence_after();
-      uint32_t x[128];
-      tmem_ld128_sync(tmem + lanes + kTmemO + 128 * s, x);  // anything, where the stage had no tile
-      // rows to memory through this stage's part of Q (every product that read it has run), so
-      // that a warp stores whole rows; 16-byte units are swizzled by the row
-      const uint32_t mine_s = base + s * kQStage + uint32_t((warp & 3) * 32) * 256u;
-#pragma unroll
-      for (int u = 0; u < 128; ++u) x[u] = some ? __float_as_uint(__uint_as_float(x[u]) * inv) : 0u;
       const int64_t all = A.num_q * A.heads, at = int64_t(R.q0 + i0) * A.heads + h;
-      if (A.nsplit == 1) {
+      tc_fence_after();
+      // rows to memory through this stage's part of Q (every product that read it has run), so
+      // that a warp stores whole rows; 16-byte units are swizzled by the row.  In short loops: a
+      // block runs this once, and straight code waits for its instructions (4,000 cycles)
+      const uint32_t mine_s = base + s * kQStage + uint32_t((warp & 3) * 32) * 256u;
+      const bool split_keys = A.nsplit > 1;  // fp32 parts, 64 columns at a time
+#pragma unroll 1
+      for (int u0 = 0; u0 < 128; u0 += split_keys ? 64 : 128) {
+        const int u1 = u0 + (split_keys ? 64 : 128);
+#pragma unroll 1
+        for (int u = u0; u < u1; u += 32) {
+          uint32_t y[32];  // anything, where the stage had no tile
+          tmem_ld32_sync(tmem + lanes + kTmemO + 128 * s + u, y);
 #pragma unroll
-        for (int u = 0; u < 128; u += 8) {
-          const uint4 w = pack<T>(reinterpret_cast<const float*>(x) + u);
-          st_shared_v4(mine_s + lane * 256 + (((u / 8) ^ (lane & 15)) << 4), w.x, w.y, w.z, w.w);
+          for (int e = 0; e < 32; ++e) y[e] = some ? __float_as_uint(__uint_as_float(y[e]) * inv) : 0u;
+          if (split_keys) {  // a part without weights is not read by the combine
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              st_shared_v4(mine_s + lane * 256 + ((((u - u0 + e) / 4) ^ (lane & 15)) << 4), y[e], y[e + 1], y[e + 2], y[e + 3]);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              const uint4 w = pack<T>(reinterpret_cast<const float*>(y) + e);
+              st_shared_v4(mine_s + lane * 256 + ((((u + e) / 8) ^ (lane & 15)) << 4), w.x, w.y, w.z, w.w);
+            }
+          }
         }
         __syncwarp();
-        T* out = static_cast<T*>(A.out) + int64_t(R.q0 + i0) * A.o_tok + int64_t(h) * A.o_head + (lane & 15) * 8;
-#pragma unroll
-        for (int u = 0; u < 32; u += 2) {
-          const int rr = u + (lane >> 4);
+        // half a warp a row of 256 bytes
+        unsigned char* to;
+        int64_t pitch;
+        if (split_keys) {
+          to = reinterpret_cast<unsigned char*>(A.part + (split * all + at) * kV + u0);
+          pitch = int64_t(A.heads) * kV * 4;
+        } else {
+          to = reinterpret_cast<unsigned char*>(static_cast<T*>(A.out) + int64_t(R.q0 + i0) * A.o_tok + int64_t(h) * A.o_head);
+          pitch = A.o_tok * int64_t(sizeof(T));
+        }
+        to += (lane >> 4) * pitch + (lane & 15) * 16;
+#pragma unroll 4
+        for (int rr = lane >> 4; rr < 32; rr += 2, to += 2 * pitch) {
           const float4 w = ld_shared_f4(mine_s + rr * 256 + (((lane & 15) ^ (rr & 15)) << 4));
-          if (rr < live) *reinterpret_cast<float4*>(out + int64_t(rr) * A.o_tok) = w;
+          if (rr < live) *reinterpret_cast<float4*>(to) = w;
         }
-      } else {  // a part without weights is not read by the combine
-        float* part = A.part + (split * all + at) * kV + (lane & 15) * 4;
-#pragma unroll
-        for (int half = 0; half < 128; half += 64) {
-#pragma unroll
-          for (int u = 0; u < 64; u += 4)
-            st_shared_v4(mine_s + lane * 256 + (((u / 4) ^ (lane & 15)) << 4), x[half + u], x[half + u + 1], x[half + u + 2],
-                         x[half + u + 3]);
-          __syncwarp();
-#pragma unroll
-          for (int u = 0; u < 32; u += 2) {
-            const int rr = u + (lane >> 4);
-            const float4 w = ld_shared_f4(mine_s + rr * 256 + (((lane & 15) ^ (rr & 15)) << 4));
-            if (rr < live) *reinterpret_cast<float4*>(part + int64_t(rr) * A.heads * kV + half) = w;
-          }
-          __syncwarp();
-        }
+        __syncwarp();
       }
       if (lane < live) {
         const float lse = some ? m * A.scale + logf(l) : -INFINITY;
         const int64_t to = at + int64_t(lane) * A.heads;
-        if (A.nsplit > 1) A.part[int64_t(A.nsplit) * all * kV + split * all + to] = lse;
+        if (split_keys) A.part[int64_t(A.nsplit) * all * kV + split * all + to] = lse;
         else if (A.lse) A.lse[to] = lse;
       }
     }
