@@ -122,6 +122,12 @@ __global__ void __launch_bounds__(kPlainThreads) norm_rope_plain_kernel(const No
 // heads is issued before the angles are computed and before the token is known
 // to be valid.  Its conditions (whole units everywhere, at most NN and NR units
 // a lane) are checked by the launch; the plain form above takes what is left.
+//
+// What bounds it (one GB300, 64 heads of 128 + 64): for many tokens the bytes of the
+// heads, read and written once (8,191 tokens in fp16 77 us, 5.5 TB/s; the plain form
+// 257); for few the launch (8 tokens 2.1 us).  Four blocks an SM in 56 registers
+// (three in 72: 84 us; 16 heads a block, six an SM: 76, but 1,024 tokens 9.3 us in
+// place of 8.0); streaming loads and stores were slower.
 constexpr int kVecThreads = 288, kGroups = 32;
 
 template <int N> __device__ __forceinline__ void load_floats(const float* from, float* to) {
@@ -160,7 +166,7 @@ __device__ __forceinline__ uint4 load16(const void* p) { return *static_cast<con
 // NN, NR: units of the plain part and units (half layout: pairs of them) of the
 // rotated part that a lane may hold.
 template <typename T, bool kHalf, int NN, int NR>
-__global__ void __launch_bounds__(kVecThreads, NN <= 2 ? 4 : 1) norm_rope_vec_kernel(const NormArgs A) {
+__global__ void __launch_bounds__(kVecThreads, NN <= 2 ? (sizeof(T) == 4 ? 3 : 4) : 1) norm_rope_vec_kernel(const NormArgs A) {
   constexpr int V = 16 / int(sizeof(T)), M = kHalf ? 2 : 1;
   constexpr int kLatentUnits = kDLat / V / 32;
   __shared__ __align__(16) float cos_s[MTV_MAX_ROPE_DIM / 2], sin_s[MTV_MAX_ROPE_DIM / 2];

@@ -10,11 +10,9 @@
 //   O += P V       8 k-steps, P from TMEM, V as an MN-major operand
 // Roles: a warp a stage issues the MMAs, one the TMA copies, and four warps a
 // stage the softmax, a thread a row.  While one stage's softmax works, the tensor
-// core computes the other's O += P V and next S.  MMAs of one thread run in
-// order: S(j+1) may overwrite P(j) without a wait, and S(j+1) being there says
-// that O holds everything up to j.  (One warp issuing for both stages was the
-// bottleneck: with its waits and commits it needed 930 cycles a stage and tile
-// beside about 50 an MMA, of which there are 20.)
+// core computes the other's O += P V and next S; the stages take turns at it (see
+// there).  MMAs of one thread run in order: S(j+1) may overwrite P(j) without a
+// wait, and S(j+1) being there says that O holds everything up to j.
 //
 // Shared memory: Q 96 KB and a ring of eight 16 KB slots that K (three slots of
 // 64 dims a tile) and V (two of 64 keys) pass through in the order of their
@@ -25,16 +23,28 @@
 //
 // The maximum that scores refer to moves only when a row's scores grow by more
 // than 2^8 past it (weights stay below 2^8), so O is rarely rescaled.  P is
-// rounded to the input type, sums of weights stay in fp32.
+// rounded to the input type, which the tensor core takes; sums of weights stay in
+// fp32.
+//
+// What bounds it (one GB300, 64 heads): the tensor core, for long prompts.  8,192
+// tokens in one piece take 0.773 ms, 1,780 TFLOP/s of what the causal mask leaves
+// (92 % of the measured bf16 rate); a pair of tiles 2,800 cycles of 2,600, a block
+// 9,000 more for its first copies and its output.  What each step gave there:
+// MMAs and copies issued under warp-uniform branches by an elected thread (their
+// operands stay in uniform registers) 1.41 -> 1.04 ms; a warp a stage for the MMAs
+// -> 0.90; no spills in the softmax -> 0.87; turns -> 0.80; K's first slot filled
+// before V's release -> 0.77.  Dropped: blocks that take the next one's number and
+// start its copies early (more registers: 0.85 ms), 64 columns a softmax thread
+// (0.95), P of both stages' rows in step (0.91).
 //
 // Every wait is bounded: one that gives up sets MTV_DEVERR_TIMEOUT and a flag
 // that ends the block's other waits; copies and MMAs in flight are waited for
 // (bounded too) before TMEM is freed.
 //
 // With few query rows the keys are split over blocks: each writes its
-// normalised part and its lse, and combine_kernel joins them. 
-// (Letting both stages take a request's 128 rows or fewer and its tiles in turn was
-// no faster: such calls are bound by the keys' way from memory.)
+// normalised part and its lse, and combine_kernel joins them (60 rows over 32,768
+// keys of 8 heads: 31 us, 21 of them the keys' way from memory).  Letting both
+// stages take the rows of such a block and its tiles in turn was no faster.
 #include <math.h>
 #include <stdint.h>
 
@@ -235,7 +245,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     };
     // Where both stages have work they take turns, 0 1 0 1 ...: O += P V(j) and the next S are
     // one turn.  Left to themselves they drift into step, share the tensor core while both have
-    // work for it and leave it idle while both compute weights (8,192 tokens: 914 us, not 836).
+    // work for it and leave it idle while both compute weights (8,192 tokens: 914 us, not 805).
     const bool turns = T0 > 0 && T1 > 0;
     int step = 0;
     auto my_turn = [&]() -> bool {
