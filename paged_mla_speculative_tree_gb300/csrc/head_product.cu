@@ -15,6 +15,19 @@
 // Weights dense in k are a K-major operand (chunks of 64 k x nt rows), weights
 // dense in n an MN-major one (blocks of 64 n x 64 k).
 //
+// What bounds it (one GB300, 64 heads): the bytes where each head has rows of its
+// own (1,024 tokens: queries to the latent space 14.9 us, latent outputs to values
+// 13.9, floors 13.8; 4,000 tokens 70 and 57, floors 50); for few tokens the chain
+// launch -> copies -> sums -> stores (8 tokens to the latent space 4.5 us, 1.3 of
+// bytes; 64 to values 5.4, 2.0 of bytes); for one latent expanded to all heads the
+// copies of x under way beside 128 KB of weights: 36 bytes a cycle and SM, each of
+// which meets 128 outputs (8,191 tokens to 64 x 256: 104 us, 1,320 TFLOP/s; one
+// library product of that shape 85).  There, sharing x between two blocks by
+// multicast changed nothing (it is a block's own ring that binds, not L2); two
+// chunks a wait (+ 10 %) and eight warps for the sums (+ 5 %) were slower.  Copies
+// and MMAs are issued under warp-uniform branches by an elected thread: by lane 0
+// of a divergent one they took two to four times as long (186 us).
+//
 // Every wait is bounded: one that gives up sets MTV_DEVERR_TIMEOUT and a flag
 // that ends the block's other waits; copies and MMAs in flight are waited for
 // (bounded too) before TMEM is freed.
@@ -59,8 +72,11 @@ struct TensorArgs {
   CUtensorMap x, w, out;
   uint32_t* err;
   int64_t units, tokens;   // units: heads * n_tiles * m_tiles
-  uint32_t x_bytes;        // of a copy of x: 64 k of 128 tokens, or of as many as there are
-  int m_tiles, n_tiles, nt, chunks, slots, w_k_major, x_by_head, w_by_head, out_by_head, n_dim;
+  uint32_t x_bytes;        // of a chunk of x: 64 k of 128 tokens, or of as many as there are
+  int m_tiles, n_tiles, nt, chunks, slots;
+  int gx, gw, gw_log;      // chunks a copy of x (and a slot of the ring) and of w (dense in k) has: 1, 2 or 4
+  int x_whole, w_whole;    // the maps are cut into chunks of 64
+  int w_k_major, x_by_head, w_by_head, out_by_head, n_dim;
 };
 
 // A block's units in order: 128 tokens after 128 tokens of one (head, nt outputs),
@@ -86,7 +102,8 @@ struct Units {
   }
 };
 
-template <typename T>
+// kFew: at most one tile of tokens, whose copies bring several chunks each.
+template <typename T, bool kFew>
 __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_constant__ TensorArgs A) {
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -94,7 +111,10 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
   auto bar = [&](int i) { return base + 8u * uint32_t(i); };
   const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
   const uint32_t w_chunk = uint32_t(A.nt) * 128u;
-  const uint32_t off_x = kOffData + uint32_t(A.chunks) * w_chunk, off_out = off_x + uint32_t(A.slots) * kXSlot;
+  const int gx = kFew ? A.gx : 1, gw = kFew ? A.gw : 1;
+  const uint32_t x_chunk = kFew ? A.x_bytes : kXSlot, x_slot = uint32_t(gx) * x_chunk;
+  const uint32_t off_x = kOffData + uint32_t(A.chunks) * w_chunk;
+  const uint32_t off_out = off_x + uint32_t(A.slots) * x_slot + (kXSlot - x_chunk);  // the MMAs read 128 rows of the last chunk
   const int64_t first = A.units * blockIdx.x / gridDim.x, last = A.units * (blockIdx.x + 1) / gridDim.x;
   const uint32_t cols = A.nt <= 64 ? 128u : 2u * uint32_t(A.nt);
 
@@ -124,15 +144,20 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
     for (Units u(first, last, A); u.more() && ok; u.next(A)) {
       const int xh = A.x_by_head ? u.h : 0, wh = A.w_by_head ? u.h : 0, n0 = u.n * A.nt, t0 = u.t * kRows;
       for (int c = 0; c < A.chunks && ok; ++c) {
-        if (items >= A.slots) ok = released(B_XEMPTY + slot, phase);
-        if (!ok) break;
-        if (elect_one()) {
-          mbar_arrive_expect_tx(data + 8 * (B_XFULL + slot), A.x_bytes);
-          tma_load_3d(data + off_x + slot * kXSlot, &A.x, c * kChunk, xh, t0, data + 8 * (B_XFULL + slot));
+        if ((c & (gx - 1)) == 0) {
+          if (items >= A.slots) ok = released(B_XEMPTY + slot, phase);
+          if (!ok) break;
+          if (elect_one()) {
+            const uint32_t full = data + 8 * (B_XFULL + slot);
+            mbar_arrive_expect_tx(full, x_slot);
+            const uint32_t dst = data + off_x + slot * x_slot;
+            if constexpr (kFew) tma_load_4d(dst, &A.x, A.x_whole ? 0 : c * kChunk, xh, t0, A.x_whole ? c : 0, full);
+            else tma_load_3d(dst, &A.x, c * kChunk, xh, t0, full);
+          }
+          items = items < A.slots ? items + 1 : items;
+          if (++slot == A.slots) slot = 0, phase ^= 1;
         }
-        items = items < A.slots ? items + 1 : items;
-        if (++slot == A.slots) slot = 0, phase ^= 1;
-        if (!u.fresh) continue;
+        if (!u.fresh || (c & (gw - 1)) != 0) continue;
         if (c == 0) {
           if (loads > 0) ok = released(B_WFREE, uint32_t(loads - 1) & 1);
           if (!ok) break;
@@ -140,12 +165,15 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
         }
         ++asked;
         if (elect_one()) {
-          const uint32_t dst = data + kOffData + c * w_chunk, full = data + 8 * (B_WFULL + c);
-          mbar_arrive_expect_tx(full, w_chunk);
-          if (A.w_k_major) {
-            tma_load_3d(dst, &A.w, c * kChunk, wh, n0, full);
+          const uint32_t dst = data + kOffData + c * w_chunk, full = data + 8 * (B_WFULL + (kFew ? c >> A.gw_log : c));
+          mbar_arrive_expect_tx(full, uint32_t(gw) * w_chunk);
+          if constexpr (kFew) {
+            if (A.w_k_major) tma_load_4d(dst, &A.w, A.w_whole ? 0 : c * kChunk, wh, n0, A.w_whole ? c : 0, full);
+            else if (A.w_whole) tma_load_4d(dst, &A.w, 0, wh, c * kChunk, n0 / 64, full);
+            else for (int b = 0; b < A.nt; b += 64) tma_load_4d(dst + b * 128, &A.w, n0 + b, wh, c * kChunk, 0, full);
           } else {
-            for (int b = 0; b < A.nt; b += 64) tma_load_3d(dst + b * 128, &A.w, n0 + b, wh, c * kChunk, full);
+            if (A.w_k_major) tma_load_3d(dst, &A.w, c * kChunk, wh, n0, full);
+            else for (int b = 0; b < A.nt; b += 64) tma_load_3d(dst + b * 128, &A.w, n0 + b, wh, c * kChunk, full);
           }
         }
       }
@@ -174,20 +202,23 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
       if (u.fresh) ++loads;
       const int buf = n & 1;
       if (n >= 2) ok = arrived(B_ACCFREE + buf, uint32_t(n / 2 - 1) & 1);
+      int in = 0;  // chunk of the slot
       for (int c = 0; c < A.chunks && ok; ++c) {
-        if (u.fresh) ok = arrived(B_WFULL + c, uint32_t(loads - 1) & 1);
-        ok = ok && arrived(B_XFULL + slot, phase);
+        if (u.fresh && (!kFew || (c & (gw - 1)) == 0)) ok = arrived(B_WFULL + (kFew ? c >> A.gw_log : c), uint32_t(loads - 1) & 1);
+        if (ok && (!kFew || in == 0)) ok = arrived(B_XFULL + slot, phase);
         if (!ok) break;
         tc_fence_after();
+        const bool done = !kFew || in + 1 == gx || c + 1 == A.chunks;  // with the slot
         if (elect_one()) {
-          const uint64_t a = smem_desc(data + off_x + slot * kXSlot, 16, 1024, kSwizzle128B);
+          const uint64_t a = smem_desc(data + off_x + slot * x_slot + (kFew ? in * x_chunk : 0), 16, 1024, kSwizzle128B);
           const uint64_t b = smem_desc(data + kOffData + c * w_chunk, A.w_k_major ? 16 : 8192, 1024, kSwizzle128B);
 #pragma unroll
           for (int k = 0; k < 4; ++k)
             mma_ss(acc + uint32_t(A.nt) * buf, desc_add(a, 32 * k), desc_add(b, w_step * k), id, c + k > 0);
-          mma_commit(bar(B_XEMPTY + slot));
+          if (done) mma_commit(bar(B_XEMPTY + slot));
         }
-        if (++slot == A.slots) slot = 0, phase ^= 1;
+        in = done ? 0 : in + 1;
+        if (done && ++slot == A.slots) slot = 0, phase ^= 1;
       }
       if (!ok) break;
       if (elect_one()) {
@@ -280,40 +311,55 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
   const int sms = sm_count();
   P.chunks = (A.k_dim + kChunk - 1) / kChunk;
   P.m_tiles = int((A.tokens + kRows - 1) / kRows);
-  // the widest tile whose weights fit and that still gives four of five SMs a unit: wide tiles read x
-  // less often, narrow ones spread few tokens over the SMs
-  P.nt = 64;
-  for (int nt : {256, 128}) {
-    if (uint32_t(P.chunks) * nt * 128u > kMaxWeights || nt >= 2 * A.n_dim) continue;
-    if (int64_t(A.heads) * ((A.n_dim + nt - 1) / nt) * P.m_tiles * 5 >= int64_t(sms) * 4) {
-      P.nt = nt;
-      break;
-    }
+  // the narrowest tile that still gives every unit an SM of its own (20 heads: one token to the latent space
+  // 4.1 us with 128, 4.6 with 256), else the widest whose weights fit, which reads x least often (1,024
+  // tokens, 64 heads: 14.8 us with 256, 16.9 with 128)
+  P.nt = 0;
+  for (int nt = 64; nt <= 256; nt *= 2) {
+    if (nt > 64 && (uint32_t(P.chunks) * nt * 128u > kMaxWeights || nt >= 2 * A.n_dim)) break;
+    P.nt = nt;
+    if (int64_t(A.heads) * ((A.n_dim + nt - 1) / nt) * P.m_tiles <= sms) break;
   }
   P.n_tiles = (A.n_dim + P.nt - 1) / P.nt;
   P.units = int64_t(A.heads) * P.n_tiles * P.m_tiles;
-  const uint32_t fixed = 1024 + kOffData + uint32_t(P.chunks) * P.nt * 128u + 4 * (P.nt > 128 ? 2 : 1) * kBlockBytes;
-  P.slots = int((227u * 1024u - fixed) / kXSlot);
-  if (P.slots > kMaxSlots) P.slots = kMaxSlots;
-  const uint32_t smem = fixed + P.slots * kXSlot;
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
-  // a copy takes time by its box, inside the tensor or not, so few tokens get a lower one; what the
-  // slot holds below it makes sums that nobody stores
-  const int x_rows = A.tokens < kRows ? int(A.tokens + 7) / 8 * 8 : kRows;
-  P.x_bytes = uint32_t(x_rows) * kChunk * 2;
   P.w_k_major = A.w_k == 1;
+  // A copy costs its issue (about 150 cycles) and its box, inside the tensor or not.  So one tile of tokens
+  // takes several chunks of weights and of x with a copy, x in boxes as low as it is (what a slot holds below
+  // such a box makes sums that nobody stores): values of 64 tokens 6.3 -> 5.4 us.  Many tokens stream chunk by
+  // chunk, which keeps more copies under way (8,191 tokens expanded: 104 us, with the other form 142).
+  const bool few = P.m_tiles == 1;
+  const int x_rows = few ? int(A.tokens + 7) / 8 * 8 : kRows;
+  P.x_bytes = uint32_t(x_rows) * kChunk * 2;
+  P.x_whole = few && A.k_dim % kChunk == 0, P.w_whole = few && (P.w_k_major ? A.k_dim : A.n_dim) % 64 == 0;
+  const int most = P.chunks % 4 == 0 ? 4 : P.chunks % 2 == 0 ? 2 : 1;
+  P.gw = P.w_k_major && P.w_whole ? most : 1, P.gw_log = P.gw / 2;
+  P.gx = P.x_whole ? most : 1;
+  const uint32_t fixed = 1024 + kOffData + uint32_t(P.chunks) * P.nt * 128u + 4 * (P.nt > 128 ? 2 : 1) * kBlockBytes +
+                         (kXSlot - P.x_bytes);
+  while (P.gx > 1 && fixed + 2 * P.gx * P.x_bytes > 227u * 1024u) P.gx /= 2;
+  P.slots = int((227u * 1024u - fixed) / (P.gx * P.x_bytes));
+  if (P.slots > kMaxSlots) P.slots = kMaxSlots;
+  const uint32_t smem = fixed + P.slots * P.gx * P.x_bytes;
   P.x_by_head = A.x_head != 0, P.w_by_head = A.w_head != 0, P.out_by_head = 1;
   if (A.heads == 1) P.x_by_head = P.w_by_head = P.out_by_head = 0;
   P.err = A.err, P.tokens = A.tokens, P.n_dim = A.n_dim;
-  const bool maps = encode_heads_map(&P.x, bf16, A.x, A.tokens, A.x_tok, A.heads, A.x_head, A.k_dim, 64, x_rows) &&
-                    (P.w_k_major ? encode_heads_map(&P.w, bf16, A.w, A.n_dim, A.w_n, A.heads, A.w_head, A.k_dim, 64, P.nt)
-                                 : encode_heads_map(&P.w, bf16, A.w, A.k_dim, A.w_k, A.heads, A.w_head, A.n_dim, 64, 64)) &&
-                    encode_heads_map(&P.out, bf16, A.out, A.tokens, A.out_tok, A.heads, A.out_head, A.n_dim, 64, 32);
+  // weights: rows, their stride, their length, and the rows of a box
+  const int64_t w_rows = P.w_k_major ? A.n_dim : A.k_dim, w_row = P.w_k_major ? A.w_n : A.w_k;
+  const int w_dim = P.w_k_major ? A.k_dim : A.n_dim, w_box = P.w_k_major ? P.nt : 64;
+  const bool maps =
+      (few ? encode_chunked_map(&P.x, bf16, A.x, A.tokens, A.x_tok, A.heads, A.x_head, A.k_dim, P.x_whole, x_rows, P.gx) &&
+                 encode_chunked_map(&P.w, bf16, A.w, w_rows, w_row, A.heads, A.w_head, w_dim, P.w_whole, w_box,
+                                    P.w_k_major ? P.gw : P.nt / 64)
+           : encode_heads_map(&P.x, bf16, A.x, A.tokens, A.x_tok, A.heads, A.x_head, A.k_dim, 64, kRows) &&
+                 encode_heads_map(&P.w, bf16, A.w, w_rows, w_row, A.heads, A.w_head, w_dim, 64, w_box)) &&
+      encode_heads_map(&P.out, bf16, A.out, A.tokens, A.out_tok, A.heads, A.out_head, A.n_dim, 64, 32);
   if (!maps) return cudaErrorInvalidValue;
-  const cudaError_t e = cudaFuncSetAttribute(head_product_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+  auto kernel = few ? head_product_kernel<T, true> : head_product_kernel<T, false>;
+  const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;
   const unsigned grid = unsigned(P.units < sms ? P.units : sms);
-  head_product_kernel<T><<<grid, kThreads, smem, st>>>(P);
+  kernel<<<grid, kThreads, smem, st>>>(P);
   return cudaGetLastError();
 }
 

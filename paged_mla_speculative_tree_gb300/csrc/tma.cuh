@@ -40,6 +40,24 @@ inline bool encode_heads_map(CUtensorMap* map, bool bf16, const void* base, int6
                 CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// The same for reads whose innermost extent may be cut into chunks of 64, so that
+// one copy brings several: a map over (64, heads, rows, dim / 64) with boxes of 64 x
+// 1 x box_rows x box_chunks.  With dim no multiple of 64 (`whole` false) it is (dim,
+// heads, rows, 1) with boxes of one chunk, whose start is the first coordinate.
+inline bool encode_chunked_map(CUtensorMap* map, bool bf16, const void* base, int64_t rows, int64_t row_stride, int heads,
+                               int64_t head_stride, int dim, bool whole, int box_rows, int box_chunks) {
+  const auto encode = tensor_map_encoder();
+  if (!encode) return false;
+  const bool one = heads == 1 || head_stride == 0;
+  const cuuint64_t dims[4] = {whole ? 64u : cuuint64_t(dim), one ? 1u : cuuint64_t(heads), cuuint64_t(rows),
+                              whole ? cuuint64_t(dim / 64) : 1u};
+  const cuuint64_t strides[3] = {one ? 16u : cuuint64_t(head_stride) * 2, rows == 1 ? 16u : cuuint64_t(row_stride) * 2, 128u};
+  const cuuint32_t box[4] = {64, 1, cuuint32_t(box_rows), whole ? cuuint32_t(box_chunks) : 1u}, steps[4] = {1, 1, 1, 1};
+  return encode(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4, const_cast<void*>(base),
+                dims, strides, box, steps, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // Whether encode_heads_map takes these strides (elements of 16 bits).
 inline bool mappable_stride(int64_t s) { return s >= 0 && s % 8 == 0 && s < (int64_t(1) << 38); }
 
@@ -49,6 +67,12 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const CUtensorMap* map
   asm volatile(
       "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst),
       "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(bar)
+      : "memory");
+}
+__device__ __forceinline__ void tma_load_4d(uint32_t dst, const CUtensorMap* map, int c0, int c1, int c2, int c3, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(dst),
+      "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(bar)
       : "memory");
 }
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, int c0, int c1, int c2, uint32_t src) {

@@ -562,6 +562,48 @@ def test_norm_rope_write_of_one_kind_matches_rope_write():
 
 # ------------------------------------------------------------- a run of them
 
+def test_captured_layer_follows_its_inputs():
+    """Norms, pool write, absorption and values in one graph: replays with other inputs, positions,
+    slots and numbers of valid tokens give what calls one by one give."""
+    bf, tokens, heads = torch.bfloat16, 37, 64
+    turns = pkg.rope_freqs(64, 10000.0)[0].to(DEV)
+    proj, down = rnd(1, (tokens, heads, 192), bf), rnd(2, (tokens, 576), bf)
+    up, qw, cw = rnd(3, (heads, 256, 512), bf, 0.05), rnd(4, (192,), bf), rnd(5, (512,), bf)
+    positions, loc, valid = i64(list(range(tokens))), i64(list(range(tokens, 0, -1))), i64([tokens])
+
+    def step(pool, nope, q, values):
+        pkg.norm_rope_write(turns, positions, 1e-6, q_in=proj, q_weight=qw, q_nope=nope, q_rope=q[:, :, 512:], c_in=down[:, :512],
+                            c_weight=cw, k_in=down[:, 512:], out_cache_loc=loc, kv_pool=pool, num_valid=valid)
+        pkg.head_product(nope, up[:, :128], q[:, :, :512])
+        pkg.head_product(q[:, :, :512], up[:, 128:].transpose(1, 2), values)
+
+    def buffers():
+        return (torch.zeros((64, 576), dtype=bf, device=DEV), torch.zeros((tokens, heads, 128), dtype=bf, device=DEV),
+                torch.zeros((tokens, heads, 576), dtype=bf, device=DEV), torch.zeros((tokens, heads, 128), dtype=bf, device=DEV))
+
+    captured = buffers()
+    step(*captured)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph, stream=side):
+        step(*captured)
+    for i, n in enumerate((tokens, 20, 0)):
+        proj.copy_(rnd(10 + i, proj.shape, bf))
+        down.copy_(rnd(20 + i, down.shape, bf))
+        positions.add_(1000)
+        loc.copy_(loc.roll(3))
+        valid.fill_(n)
+        want = buffers()
+        for t in captured:
+            t.zero_()
+        graph.replay()
+        step(*want)
+        torch.cuda.synchronize()
+        for a, b in zip(captured, want):
+            assert torch.equal(a, b)
+
+
 def test_absorbed_and_expanded_layers_agree():
     """One layer's attention both ways: norms, rotation and pool write, then
     absorbed queries through verify attention over the pool, and expanded keys
