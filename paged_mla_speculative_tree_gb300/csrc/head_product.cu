@@ -18,8 +18,8 @@
 // What bounds it (one GB300, 64 heads): the bytes where each head has rows of its
 // own (1,024 tokens: queries to the latent space 14.9 us, latent outputs to values
 // 13.9, floors 13.8; 4,000 tokens 70 and 57, floors 50); for few tokens the chain
-// launch -> copies -> sums -> stores (8 tokens to the latent space 4.5 us, 1.3 of
-// bytes; 64 to values 5.4, 2.0 of bytes); for one latent expanded to all heads the
+// launch -> copies -> sums -> stores (8 tokens to the latent space 4.6 us, 1.3 of
+// bytes; 64 to values 5.3, 2.0 of bytes); for one latent expanded to all heads the
 // copies of x under way beside 128 KB of weights: 36 bytes a cycle and SM, each of
 // which meets 128 outputs (8,191 tokens to 64 x 256: 104 us, 1,320 TFLOP/s; one
 // library product of that shape 85).  There, sharing x between two blocks by
@@ -326,7 +326,7 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
   P.w_k_major = A.w_k == 1;
   // A copy costs its issue (about 150 cycles) and its box, inside the tensor or not.  So one tile of tokens
   // takes several chunks of weights and of x with a copy, x in boxes as low as it is (what a slot holds below
-  // such a box makes sums that nobody stores): values of 64 tokens 6.3 -> 5.4 us.  Many tokens stream chunk by
+  // such a box makes sums that nobody stores): values of 64 tokens 6.3 -> 5.3 us.  Many tokens stream chunk by
   // chunk, which keeps more copies under way (8,191 tokens expanded: 104 us, with the other form 142).
   const bool few = P.m_tiles == 1;
   const int x_rows = few ? int(A.tokens + 7) / 8 * 8 : kRows;

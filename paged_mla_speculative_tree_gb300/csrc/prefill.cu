@@ -27,13 +27,13 @@
 // fp32.
 //
 // What bounds it (one GB300, 64 heads): the tensor core, for long prompts.  8,192
-// tokens in one piece take 0.773 ms, 1,780 TFLOP/s of what the causal mask leaves
+// tokens in one piece take 0.778 ms, 1,770 TFLOP/s of what the causal mask leaves
 // (92 % of the measured bf16 rate); a pair of tiles 2,800 cycles of 2,600, a block
 // 9,000 more for its first copies and its output.  What each step gave there:
 // MMAs and copies issued under warp-uniform branches by an elected thread (their
 // operands stay in uniform registers) 1.41 -> 1.04 ms; a warp a stage for the MMAs
 // -> 0.90; no spills in the softmax -> 0.87; turns -> 0.80; K's first slot filled
-// before V's release -> 0.77.  Dropped: blocks that take the next one's number and
+// before V's release -> 0.78.  Dropped: blocks that take the next one's number and
 // start its copies early (more registers: 0.85 ms), 64 columns a softmax thread
 // (0.95), P of both stages' rows in step (0.91).
 //
