@@ -1,11 +1,14 @@
-"""ctypes binding of the C ABI in ``include/mla_tree_verify.h``.
+"""Binding of the C ABI in ``include/``: ctypes, and for the calls of the layer
+(``mla_layer_ops.h``) an extension module that takes the tensors as they are.
 
 Argument marshalling only: every step of the verify attention runs in the CUDA
-library.  There is no fallback -- if the library is missing this raises.
+library.  There is no fallback -- if the library or the extension is missing
+this raises.
 """
 from __future__ import annotations
 
 import ctypes
+import importlib.util
 import os
 
 import torch
@@ -361,7 +364,6 @@ def tree_group_prefix(group_indptr, num_groups: int, max_group_prefix: int, kv_i
 
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
-_HALF_TYPES = (torch.bfloat16, torch.float16)
 
 
 # The current stream's handle without building a Stream object, where torch has it.
@@ -567,19 +569,40 @@ def token_logprobs(logits, stats, tokens=None, logprobs=None, top_tokens=None, t
                  _dense(top_logprobs, _F32, device, "top_logprobs", k * rows), _dense(err, _I32, device, "err"))
 
 
-def _heads(t, dtype, device, name, shape):
-    """(address, token stride, head stride) of a [tokens, heads, dim] view dense in its last dimension."""
-    at = _strided(t, dtype, device, name, shape)
-    tok, head, inner = t.stride()
-    if inner != 1 and shape[2] > 1:
-        raise ValueError(f"{name} must be dense in its last dimension")
-    return at, tok, head
+_ext = None
+_get_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 
 
-def _code_of(t, name, types):
-    if t.dtype not in types:
-        raise TypeError(f"{name} must be one of {list(types)}, got {t.dtype}")
-    return _DTYPES[t.dtype]
+def _extension():
+    """The extension module beside the library: checks and calls on tensors as they are."""
+    global _ext
+    if _ext is None:
+        load()
+        if not os.path.exists(_build.EXT):
+            raise RuntimeError(f"extension not built: {_build.EXT} (run __graft_entry__.build())")
+        spec = importlib.util.spec_from_file_location("binding_ext", _build.EXT)
+        _ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(_ext)
+    return _ext
+
+
+def _enqueue(fn, some, what, stream, check, *args):
+    """``_call`` of an entry of the extension: on the device of ``some`` and, by default, its current stream."""
+    device = some.get_device() if isinstance(some, torch.Tensor) else -1
+    if stream is None:
+        stream = _raw_stream(device) if device >= 0 else 0  # a CPU tensor is refused by the entry
+    elif isinstance(stream, torch.cuda.Stream):
+        if stream.device_index != device:
+            raise ValueError("the stream is on another device than the tensors")
+        stream = stream.cuda_stream
+    if device < 0 or device == _get_device():
+        rc = fn(*args, stream)
+    else:
+        with torch.cuda.device(device):
+            rc = fn(*args, stream)
+    if check and rc != MTV_OK:
+        raise MtvError(rc, what)
+    return rc
 
 
 def head_product(x, w, out, err=None, stream=None, check: bool = True) -> int:
@@ -588,17 +611,7 @@ def head_product(x, w, out, err=None, stream=None, check: bool = True) -> int:
     latent attention's absorbed and expanded forms (see the header).  ``x`` and
     ``out`` are views of any strides with a dense last dimension (an expanded
     head dimension of ``x`` gives every head the same rows), ``w`` one of any."""
-    code = _code_of(x, "x", _HALF_TYPES)
-    if x.dim() != 3 or w.dim() != 3:
-        raise ValueError("x must be [tokens, heads, k] and w [heads, k, n]")
-    tokens, heads, k_dim = x.shape
-    n_dim = w.shape[2]
-    device = _device_of(x, "x")
-    xp, x_tok, x_head = _heads(x, x.dtype, device, "x", (tokens, heads, k_dim))
-    wp = _strided(w, x.dtype, device, "w", (heads, k_dim, n_dim))
-    op, out_tok, out_head = _heads(out, x.dtype, device, "out", (tokens, heads, n_dim))
-    return _call(load().mla_head_product, device, stream, check, xp, x_tok, x_head, wp, *w.stride(), op, out_tok, out_head,
-                 tokens, heads, k_dim, n_dim, code, _dense(err, _I32, device, "err"))
+    return _enqueue(_extension().head_product, x, "mla_head_product", stream, check, x, w, out, err)
 
 
 def prefill_workspace(num_sms: int, bs: int, max_q: int, max_kv: int, num_q: int, num_heads: int):
@@ -618,28 +631,8 @@ def prefill_run(q, k_nope, k_rope, v, qo_indptr, kv_indptr, max_q: int, max_kv: 
     128], into ``out`` [rows, heads, 128] and ``lse`` [rows, heads] (see the
     header).  Requests are runs of rows and keys by ``qo_indptr`` and
     ``kv_indptr``, at most ``max_q`` and ``max_kv`` long."""
-    dtype, code = q.dtype, _code_of(q, "q", _HALF_TYPES)
-    if q.dim() != 3 or k_nope.dim() != 3:
-        raise ValueError("q must be [rows, heads, 192] and k_nope [keys, heads, 128]")
-    device = _device_of(q, "q")
-    num_q, heads = q.shape[:2]
-    num_kv = k_nope.shape[0]
-    bs = qo_indptr.numel() - 1
-    if bs < 0:
-        raise ValueError("qo_indptr must hold one element more than there are requests")
-    qp, q_tok, q_head = _heads(q, dtype, device, "q", (num_q, heads, 192))
-    kp, k_tok, k_head = _heads(k_nope, dtype, device, "k_nope", (num_kv, heads, 128))
-    vp, v_tok, v_head = _heads(v, dtype, device, "v", (num_kv, heads, 128))
-    rp = _strided(k_rope, dtype, device, "k_rope", (num_kv, 64))
-    kr_tok, kr_dim = k_rope.stride()
-    if kr_dim != 1:
-        raise ValueError("k_rope must be dense in its last dimension")
-    op, o_tok, o_head = _heads(out, dtype, device, "out", (num_q, heads, 128))
-    return _call(load().mla_prefill_run, device, stream, check, qp, q_tok, q_head, kp, k_tok, k_head, rp, kr_tok, vp, v_tok,
-                 v_head, _dense(qo_indptr, _I64, device, "qo_indptr"), _dense(kv_indptr, _I32, device, "kv_indptr", bs + 1),
-                 bs, max_q, max_kv, num_q, num_kv, heads, code, scale, 1 if causal else 0, op, o_tok, o_head,
-                 _dense(lse, _F32, device, "lse", num_q * heads), nsplit, _dense(workspace, torch.uint8, device, "workspace"),
-                 workspace.numel() if workspace is not None else 0, _dense(err, _I32, device, "err"))
+    return _enqueue(_extension().prefill_run, q, "mla_prefill_run", stream, check, q, k_nope, k_rope, v, qo_indptr, kv_indptr,
+                    max_q, max_kv, scale, out, lse, causal, nsplit, workspace, err)
 
 
 class MlaPrefill:
@@ -685,49 +678,9 @@ def norm_rope_write(turns, positions, eps: float, layout: int = ROPE_INTERLEAVED
     normalised by ``c_weight`` (if given) and the turned ``k_in`` [tokens, 64]
     written into ``kv_pool`` at ``out_cache_loc``.  Either half may be left out
     (see the header)."""
-    if (q_in is None) != (q_rope is None):
-        raise ValueError("q_in and q_rope go together")
-    some = q_in if q_in is not None else c_in
-    if some is None:
-        raise ValueError("neither q_in nor c_in is given")
-    dtype = some.dtype
-    code = _code_of(some, "q_in" if q_in is not None else "c_in", _DTYPES)
-    if num_valid is not None and num_valid.numel() != 1:
-        raise ValueError("num_valid must hold one element")
-    device = _device_of(some, "q_in" if q_in is not None else "c_in")
-    tokens, rope_dim = positions.numel(), 2 * turns.numel()
-    qi = qn = qr = kp = cp = lp = pool = None
-    q_tok = q_head = n_tok = n_head = r_tok = r_head = heads = nope = k_tok = c_tok = slots = 0
-    if q_in is not None:
-        if q_in.dim() != 3 or q_in.shape[2] < rope_dim:
-            raise ValueError("q_in must be [tokens, heads, nope + rope_dim]")
-        heads, nope = q_in.shape[1], q_in.shape[2] - rope_dim
-        qi, q_tok, q_head = _heads(q_in, dtype, device, "q_in", (tokens, heads, nope + rope_dim))
-        qr, r_tok, r_head = _heads(q_rope, dtype, device, "q_rope", (tokens, heads, rope_dim))
-        if (q_nope is not None) != (q_weight is not None and nope > 0):
-            raise ValueError("q_nope goes with q_weight")
-        if q_nope is not None:
-            qn, n_tok, n_head = _heads(q_nope, dtype, device, "q_nope", (tokens, heads, nope))
-    elif q_nope is not None or q_weight is not None:
-        raise ValueError("q_weight and q_nope need q_in")
-    if kv_pool is not None or c_in is not None or k_in is not None or out_cache_loc is not None or c_weight is not None:
-        if kv_pool is None or c_in is None or k_in is None or out_cache_loc is None:
-            raise ValueError("kv_pool, c_in, k_in and out_cache_loc go together")
-        slots = kv_pool.shape[0]
-        if slots == 0:
-            raise ValueError("kv_pool is empty")
-        kp, cp = _strided(k_in, dtype, device, "k_in", (tokens, 64)), _strided(c_in, dtype, device, "c_in", (tokens, 512))
-        (k_tok, k_dim), (c_tok, c_dim) = k_in.stride(), c_in.stride()
-        if k_dim != 1 or c_dim != 1:
-            raise ValueError("k_in and c_in must be dense in their last dimension")
-        lp = _dense(out_cache_loc, _I64, device, "out_cache_loc", tokens)
-        pool = _dense(kv_pool, _BF16, device, "kv_pool", 576 * slots)
-    return _call(load().mla_norm_rope_write, device, stream, check, _dense(turns, _I64, device, "turns"), rope_dim, amplitude,
-                 layout, _dense(positions, _I64, device, "positions"), tokens, _dense(num_valid, _I64, device, "num_valid"),
-                 code, eps, qi, q_tok, q_head, heads, nope, _dense(q_weight, dtype, device, "q_weight", nope + rope_dim), qn,
-                 n_tok, n_head, qr, r_tok, r_head, cp, c_tok, _dense(c_weight, dtype, device, "c_weight", 512), kp, k_tok,
-                 lp, pool, slots, _dense(err, _I32, device, "err"))
-
+    return _enqueue(_extension().norm_rope_write, q_in if q_in is not None else c_in, "mla_norm_rope_write", stream, check,
+                    turns, positions, eps, layout, amplitude, q_in, q_weight, q_nope, q_rope, c_in, c_weight, k_in, out_cache_loc,
+                    kv_pool, num_valid, err)
 
 
 class MlaTreeVerify:

@@ -190,3 +190,27 @@ def test_binding_wants_cuda_tensors():
         pkg.norm_rope_write(turns, pos, 1e-6, q_in=z((2, 3, 192), dtype=bf), q_rope=z((2, 3, 64), dtype=bf))
     with pytest.raises(TypeError):
         pkg.norm_rope_write(turns, pos, 1e-6, q_in=z((2, 3, 192), dtype=torch.float64), q_rope=z((2, 3, 64)))
+
+
+def test_binding_refuses_what_is_no_tensor(lib):
+    bf, z = torch.bfloat16, torch.zeros
+    x, w, out = z((2, 3, 8), dtype=bf), z((3, 8, 4), dtype=bf), z((2, 3, 4), dtype=bf)
+    for args in ((None, w, out), (x, None, out), (x, w, None), (x.tolist(), w, out), (x, w, out.float().numpy())):
+        with pytest.raises(TypeError):
+            pkg.head_product(*args)
+    with pytest.raises(TypeError):
+        pkg.head_product(x.to("meta"), w.to("meta"), out.to("meta"))
+    turns, pos = torch.zeros(32, dtype=torch.int64), torch.zeros(2, dtype=torch.int64)
+    with pytest.raises(TypeError):
+        pkg.norm_rope_write(None, pos, 1e-6, q_in=x, q_rope=x)
+    for fn, count in (("head_product", 5), ("prefill_run", 16), ("norm_rope_write", 17)):
+        for n in (0, count - 1, count + 1):
+            with pytest.raises(TypeError):
+                getattr(binding._extension(), fn)(*[None] * n)
+
+
+def test_extension_calls_the_library_that_ctypes_loaded(lib):
+    binding._extension()
+    with open("/proc/self/maps") as f:
+        loaded = {line.split()[-1] for line in f if "libmla_tree_verify" in line}
+    assert len(loaded) == 1 and loaded.pop().endswith("_lib/libmla_tree_verify.so")
