@@ -43,6 +43,8 @@ extern "C" {
 #define MTV_MAX_PREFILL_ROWS (1 << 30)
 /* Most splits of mla_prefill_run's keys. */
 #define MTV_MAX_PREFILL_SPLITS 64
+/* What mla_prefill_run's nsplit holds above the split count: see there. */
+#define MTV_PREFILL_SPLIT_LAST 256
 
 /*
  * mla_head_product -- one matrix product a head.
@@ -85,8 +87,10 @@ int mla_head_product(const void* x, int64_t x_tok_stride, int64_t x_head_stride,
  *
  * num_sms        SM count of the device (>= 1).
  * bs, max_q, max_kv, num_q, num_heads   as for mla_prefill_run.
- * nsplit_out     host: 1 .. MTV_MAX_PREFILL_SPLITS.  The keys are split where
- *                the queries alone leave SMs without work.
+ * nsplit_out     host: the nsplit of mla_prefill_run.  The keys are split where
+ *                the queries alone leave SMs without work: all blocks' where
+ *                there are fewer than SMs, else those of the last, part-filled
+ *                wave.
  * bytes_out      host: 0 with one split.
  */
 int mla_prefill_workspace(int num_sms, int bs, int64_t max_q, int64_t max_kv, int64_t num_q, int num_heads,
@@ -119,11 +123,14 @@ int mla_prefill_workspace(int num_sms, int bs, int64_t max_q, int64_t max_kv, in
  * causal         0 or 1.
  * out            device, [num_q, heads, 128] with strides as q.
  * lse            device, fp32 [num_q, heads], or NULL to leave it out.
- * nsplit         1, or mla_prefill_workspace's count (any value up to
- *                MTV_MAX_PREFILL_SPLITS is taken).
- * workspace      device, 256-byte aligned, with nsplit > 1:
- *                nsplit * num_q * num_heads * 129 * 4 bytes at least.  Calls that
- *                may overlap need one each.  With nsplit 1 it may be NULL.
+ * nsplit         mla_prefill_workspace's, or any n + MTV_PREFILL_SPLIT_LAST * b
+ *                with 1 <= n <= MTV_MAX_PREFILL_SPLITS: the keys of the last b
+ *                blocks (256 rows of a head; all blocks where b is 0 or more
+ *                than there are) are split n ways.
+ * workspace      device, 256-byte aligned, with n > 1: n * rows * 129 * 4 bytes at
+ *                least, rows being num_q * num_heads with b = 0, else 256 a split
+ *                block.  Calls that may overlap need one each.  With n = 1 it may
+ *                be NULL.
  * err            device uint32 or NULL.  MTV_DEVERR_INDPTR: a decreasing
  *                offset, one past num_q or num_kv, or a request past max_q or
  *                max_kv (its rows are left as they were).  MTV_DEVERR_TIMEOUT:

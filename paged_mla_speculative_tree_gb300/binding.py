@@ -615,7 +615,7 @@ def head_product(x, w, out, err=None, stream=None, check: bool = True) -> int:
 
 
 def prefill_workspace(num_sms: int, bs: int, max_q: int, max_kv: int, num_q: int, num_heads: int):
-    """(split count, workspace bytes) of ``prefill_run`` for batches within these bounds (host only)."""
+    """(``nsplit``, workspace bytes) of ``prefill_run`` for batches within these bounds (host only)."""
     nsplit, size = ctypes.c_int(0), ctypes.c_uint64(0)
     rc = load().mla_prefill_workspace(int(num_sms), int(bs), int(max_q), int(max_kv), int(num_q), int(num_heads),
                                       ctypes.byref(nsplit), ctypes.byref(size))
@@ -630,7 +630,8 @@ def prefill_run(q, k_nope, k_rope, v, qo_indptr, kv_indptr, max_q: int, max_kv: 
     heads, 128] with ``k_rope`` [keys, 64] behind it, and ``v`` [keys, heads,
     128], into ``out`` [rows, heads, 128] and ``lse`` [rows, heads] (see the
     header).  Requests are runs of rows and keys by ``qo_indptr`` and
-    ``kv_indptr``, at most ``max_q`` and ``max_kv`` long."""
+    ``kv_indptr``, at most ``max_q`` and ``max_kv`` long.  ``nsplit`` is
+    ``prefill_workspace``'s, or a count by which all blocks' keys are split."""
     return _enqueue(_extension().prefill_run, q, "mla_prefill_run", stream, check, q, k_nope, k_rope, v, qo_indptr, kv_indptr,
                     max_q, max_kv, scale, out, lse, causal, nsplit, workspace, err)
 

@@ -41,10 +41,11 @@
 // that ends the block's other waits; copies and MMAs in flight are waited for
 // (bounded too) before TMEM is freed.
 //
-// With few query rows the keys are split over blocks: each writes its
-// normalised part and its lse, and combine_kernel joins them (60 rows over 32,768
-// keys of 8 heads: 31 us, 21 of them the keys' way from memory).  Letting both
-// stages take the rows of such a block and its tiles in turn was no faster.
+// With few query rows the keys are split over blocks, and so are those of the last
+// blocks where they would leave most SMs idle: each writes its normalised part and
+// its lse, and combine_kernel joins them (60 rows over 32,768 keys of 8 heads: 30 us,
+// 21 of them the keys' way from memory).  Letting both stages take the rows of such a
+// block and its tiles in turn was no faster.
 #include <math.h>
 #include <stdint.h>
 
@@ -77,23 +78,37 @@ constexpr uint32_t kSmem = kOffCtl + 16 + 1024;  // + slack for 1 KB alignment
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
 constexpr float kRescaleLog2 = 8.f;
+constexpr int kSplitLast = MTV_PREFILL_SPLIT_LAST, kTailWaves = 8;
 
 struct PrefillArgs {
   CUtensorMap q, k_nope, k_rope, v;
   void* out;
   float* lse;
-  float* part;      // [nsplit, num_q * heads, 128], then the lse [nsplit, num_q * heads]
+  float* part;      // [nsplit, part_rows, 128], then the lse [nsplit, part_rows]
   const int64_t* qo_indptr;
   const int32_t* kv_indptr;
   uint32_t* err;
-  int64_t o_tok, o_head, num_q, num_kv, max_q, max_kv;
+  int64_t o_tok, o_head, num_q, num_kv, max_q, max_kv, part_rows;
   float scale;
-  int bs, heads, causal, nsplit, q_blocks;
+  int bs, heads, causal, q_blocks;
+  int nsplit, last;  // the last blocks, whose keys are split
+  unsigned whole;    // the blocks before them
+  int by_block;      // rows of parts: 256 a split block; else num_q * heads
   int q_by_head, k_by_head, v_by_head;  // 0: one map for all heads
 };
 
 struct PrefillReq {
   int q0, k0, n, len;
+};
+
+// What block b of bs x heads x q_blocks works on: blocks of a head side by side, the longest first.
+struct PrefillBlock {
+  int r, h, row0;
+  __device__ __forceinline__ PrefillBlock(const PrefillArgs& A, unsigned b) {
+    row0 = (A.q_blocks - 1 - int(b % unsigned(A.q_blocks))) * kBlockRows;
+    b /= unsigned(A.q_blocks);
+    h = int(b % unsigned(A.heads)), r = int(b / unsigned(A.heads));
+  }
 };
 
 // The request's rows, checked against the buffers and the bounds; n = 0 where
@@ -122,15 +137,13 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   auto bar = [&](int i) { return base + kOffBars + 8u * uint32_t(i); };
   const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
 
-  // blocks of a head side by side, the longest first; then splits, heads, requests
-  unsigned id = blockIdx.x;
-  const int qb = A.q_blocks - 1 - int(id % unsigned(A.q_blocks));
-  id /= unsigned(A.q_blocks);
-  const int split = int(id % unsigned(A.nsplit));
-  id /= unsigned(A.nsplit);
-  const int h = int(id % unsigned(A.heads)), r = int(id / unsigned(A.heads));
-  const PrefillReq R = load_prefill_req(A, r, tid == 0);
-  const int row0 = qb * kBlockRows;
+  // blocks of all their keys, then the others' first parts, second parts, ...
+  const bool split_keys = blockIdx.x >= A.whole && A.nsplit > 1;
+  const unsigned tail = split_keys ? (blockIdx.x - A.whole) % unsigned(A.last) : 0u;
+  const int split = split_keys ? int((blockIdx.x - A.whole) / unsigned(A.last)) : 0;
+  const PrefillBlock B(A, split_keys ? A.whole + tail : blockIdx.x);
+  const int row0 = B.row0, h = B.h;
+  const PrefillReq R = load_prefill_req(A, B.r, tid == 0);
   if (row0 >= R.n) return;
 
   // key tiles of both stages: up to the last key that a stage's last row sees
@@ -143,7 +156,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     return (keys + kKeys - 1) / kKeys;
   };
   const int tiles0 = tiles_of(0), tiles1 = tiles_of(1);
-  const int each = (max(tiles0, tiles1) + A.nsplit - 1) / A.nsplit, begin = split * each;
+  const int parts = split_keys ? A.nsplit : 1, each = (max(tiles0, tiles1) + parts - 1) / parts, begin = split * each;
   auto mine = [&](int tiles) { return max(0, min(tiles - begin, each)); };
   const int T0 = mine(tiles0), T1 = mine(tiles1), TN = max(T0, T1);
   auto stage_tiles = [&](int s) { return s ? T1 : T0; };
@@ -420,13 +433,15 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const bool some = l != 0.f;  // true for a NaN too, which the row then shows
       const float inv = some ? __frcp_rn(l) : 0.f;
       const int live = min(32, R.n - i0);
-      const int64_t all = A.num_q * A.heads, at = int64_t(R.q0 + i0) * A.heads + h;
+      const int64_t at = int64_t(R.q0 + i0) * A.heads + h;
+      const int64_t part_at = split * A.part_rows + (A.by_block ? int64_t(tail) * kBlockRows + (i0 - row0) : at);
+      const int part_step = A.by_block ? 1 : A.heads;
       tc_fence_after();
       // rows to memory through this stage's part of Q (every product that read it has run), so
       // that a warp stores whole rows; 16-byte units are swizzled by the row.  In short loops: a
       // block runs this once, and straight code waits for its instructions (4,000 cycles)
       const uint32_t mine_s = base + s * kQStage + uint32_t((warp & 3) * 32) * 256u;
-      const bool split_keys = A.nsplit > 1;  // fp32 parts, 64 columns at a time
+      // parts are in fp32, 64 columns at a time
 #pragma unroll 1
       for (int u0 = 0; u0 < 128; u0 += split_keys ? 64 : 128) {
         const int u1 = u0 + (split_keys ? 64 : 128);
@@ -453,8 +468,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         unsigned char* to;
         int64_t pitch;
         if (split_keys) {
-          to = reinterpret_cast<unsigned char*>(A.part + (split * all + at) * kV + u0);
-          pitch = int64_t(A.heads) * kV * 4;
+          to = reinterpret_cast<unsigned char*>(A.part + part_at * kV + u0);
+          pitch = int64_t(part_step) * kV * 4;
         } else {
           to = reinterpret_cast<unsigned char*>(static_cast<T*>(A.out) + int64_t(R.q0 + i0) * A.o_tok + int64_t(h) * A.o_head);
           pitch = A.o_tok * int64_t(sizeof(T));
@@ -469,9 +484,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       if (lane < live) {
         const float lse = some ? m * A.scale + logf(l) : -INFINITY;
-        const int64_t to = at + int64_t(lane) * A.heads;
-        if (split_keys) A.part[int64_t(A.nsplit) * all * kV + split * all + to] = lse;
-        else if (A.lse) A.lse[to] = lse;
+        if (split_keys) A.part[A.nsplit * A.part_rows * kV + part_at + int64_t(lane) * part_step] = lse;
+        else if (A.lse) A.lse[at + int64_t(lane) * A.heads] = lse;
       }
     }
   }
@@ -481,19 +495,26 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   if (warp == 8) tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of split keys by their lse: a block a row of one head, whose
-// four warps take every fourth part with eight loads in flight (one warp a row
-// with four took 6 us for 38 parts).
-template <typename T>
+// Joins the parts of split keys by their lse.  Up to 8 parts: a warp a row, four
+// rows a block; more: a block a row, whose four warps take every fourth part.  Either
+// way eight loads are in flight (one warp a row with four took 6 us for 38 parts; a block a row for 14,336 rows of two parts
+// 16 us, a warp a row 6).
+constexpr int kWarpParts = 8;
+
+template <typename T, bool kWarpRow>
 __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ PrefillArgs A) {
   __shared__ float4 sums[4][32];
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, h = blockIdx.y, i = blockIdx.x;
-  const PrefillReq R = load_prefill_req(A, blockIdx.z, false);
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const PrefillBlock B(A, A.whole + blockIdx.x);
+  const int row = kWarpRow ? int(blockIdx.y) * 4 + warp : int(blockIdx.y), h = B.h, i = B.row0 + row;
+  const PrefillReq R = load_prefill_req(A, B.r, false);
   if (i >= R.n) return;
-  const int64_t all = A.num_q * A.heads, at = int64_t(R.q0 + i) * A.heads + h;
-  const float* lse = A.part + int64_t(A.nsplit) * all * kV + at;
+  const int64_t at = int64_t(R.q0 + i) * A.heads + h, all = A.part_rows;
+  const int64_t part_at = A.by_block ? int64_t(blockIdx.x) * kBlockRows + row : at;
+  const float* lse = A.part + A.nsplit * all * kV + part_at;
   asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts are being written
-  const float a = lane < A.nsplit ? lse[lane * all] : -INFINITY, b = lane + 32 < A.nsplit ? lse[(lane + 32) * all] : -INFINITY;
+  const float a = lane < A.nsplit ? lse[lane * all] : -INFINITY;
+  const float b = !kWarpRow && lane + 32 < A.nsplit ? lse[(lane + 32) * all] : -INFINITY;
   float top = fmaxf(a, b);
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
@@ -504,17 +525,18 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pr
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   const float inv = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays
   float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int k0 = warp; k0 < A.nsplit; k0 += 32) {
+  constexpr int kStep = kWarpRow ? 1 : 4;
+  for (int k0 = kWarpRow ? 0 : warp; k0 < A.nsplit; k0 += 8 * kStep) {
     float4 v[8];
     float w[8];
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
-      const int k = k0 + 4 * e;
+      const int k = k0 + kStep * e;
       w[e] = __shfl_sync(0xffffffffu, k < 32 ? wa : wb, k & 31) * inv;
       if (k >= A.nsplit) w[e] = 0.f;
       v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
       // a part without weights was not written
-      if (w[e] != 0.f) v[e] = *reinterpret_cast<const float4*>(A.part + (k * all + at) * kV + 4 * lane);
+      if (w[e] != 0.f) v[e] = *reinterpret_cast<const float4*>(A.part + (k * all + part_at) * kV + 4 * lane);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -522,13 +544,15 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pr
       acc.z = fmaf(w[e], v[e].z, acc.z), acc.w = fmaf(w[e], v[e].w, acc.w);
     }
   }
-  sums[warp][lane] = acc;
-  __syncthreads();
-  if (warp != 0) return;
+  if constexpr (!kWarpRow) {
+    sums[warp][lane] = acc;
+    __syncthreads();
+    if (warp != 0) return;
 #pragma unroll
-  for (int e = 1; e < 4; ++e) {
-    const float4 v = sums[e][lane];
-    acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    for (int e = 1; e < 4; ++e) {
+      const float4 v = sums[e][lane];
+      acc.x += v.x, acc.y += v.y, acc.z += v.z, acc.w += v.w;
+    }
   }
   T* out = static_cast<T*>(A.out) + int64_t(R.q0 + i) * A.o_tok + int64_t(h) * A.o_head;
   *reinterpret_cast<uint2*>(out + 4 * lane) = make_uint2(join(acc.x, acc.y, T()), join(acc.z, acc.w, T()));
@@ -536,27 +560,40 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pr
 }
 
 template <typename T> cudaError_t launch_prefill(const PrefillArgs& A, cudaStream_t st) {
-  const int64_t blocks = int64_t(A.q_blocks) * A.nsplit * A.heads * A.bs;
+  const unsigned blocks = A.whole + unsigned(A.last) * unsigned(A.nsplit);
   cudaError_t e = cudaFuncSetAttribute(prefill_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
   if (e != cudaSuccess) return e;
-  prefill_kernel<T><<<unsigned(blocks), kThreads, kSmem, st>>>(A);
+  prefill_kernel<T><<<blocks, kThreads, kSmem, st>>>(A);
   e = cudaGetLastError();
   if (e != cudaSuccess || A.nsplit == 1) return e;
   cudaLaunchAttribute early[1];
   early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   early[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t config = {};
-  config.gridDim = dim3(unsigned(A.max_q), unsigned(A.heads), unsigned(A.bs));
+  const bool warp_row = A.nsplit <= kWarpParts;
+  const unsigned rows = unsigned(A.max_q < kBlockRows ? A.max_q : kBlockRows);
+  config.gridDim = dim3(unsigned(A.last), warp_row ? (rows + 3) / 4 : rows);
   config.blockDim = dim3(128);
   config.stream = st;
   config.attrs = early;
   config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, combine_kernel<T>, A);
+  return cudaLaunchKernelEx(&config, warp_row ? combine_kernel<T, true> : combine_kernel<T, false>, A);
 }
 
-uint64_t workspace_bytes_of(int nsplit, int64_t num_q, int heads) {
-  return nsplit > 1 ? uint64_t(nsplit) * uint64_t(num_q) * uint64_t(heads) * uint64_t(kV + 1) * 4u : 0u;
-}
+// nsplit's two numbers, of `blocks` blocks: how many of the last ones are split
+// (0 in it: all), and whether their parts have rows of their own.
+struct Splits {
+  int count;
+  int64_t last, rows;
+  bool by_block;
+  Splits(int nsplit, int64_t blocks, int64_t num_q, int heads) {
+    count = nsplit % kSplitLast, last = nsplit / kSplitLast;
+    by_block = last > 0;
+    if (!by_block || last > blocks) last = blocks;
+    rows = by_block ? last * kBlockRows : num_q * heads;
+  }
+  uint64_t bytes() const { return count > 1 ? uint64_t(count) * uint64_t(rows) * uint64_t(kV + 1) * 4u : 0u; }
+};
 
 }  // namespace
 }  // namespace mtv
@@ -571,11 +608,20 @@ extern "C" int mla_prefill_workspace(int num_sms, int bs, int64_t max_q, int64_t
   // as many splits as leave every block an SM, of four key tiles at least (a split costs a second launch
   // and its parts' way through memory)
   const int64_t blocks = int64_t(bs) * num_heads * ((max_q + kBlockRows - 1) / kBlockRows);
-  const int64_t most = blocks > 0 ? num_sms / blocks : 1, worth = (max_kv + kKeys - 1) / kKeys / 4;
-  int64_t n = most < worth ? most : worth;
+  int64_t n = blocks > 0 ? num_sms / blocks : 1, worth = (max_kv + kKeys - 1) / kKeys / 4;
+  // More blocks than SMs: those of a last wave that fills half of the SMs at most are split over all of them
+  // (256 new after 8,192, 160 heads: 233 -> 148 us; 2 x (1,000 after 5,760), 64 heads: 336 -> 311).  Blocks of
+  // a head start longest first, so what counts is the shortest one's tiles: below 16 the join costs what the
+  // split gives (3 x (256 after 1,024), 64 heads: 47 us, split 48; 2,048 new: 82 and 85).  After 8 waves the
+  // blocks have drifted apart (15 waves: 1,066 us, split 1,087; 5: 374 and 340).
+  const int64_t over = blocks > num_sms ? blocks % num_sms : 0;
+  const int64_t shortest = (max_kv - max_q + kBlockRows) / kKeys;
+  const bool tail = over > 0 && 2 * over <= num_sms && blocks < kTailWaves * int64_t(num_sms) && shortest >= 16;
+  if (tail) n = num_sms / over, worth = shortest / 4;
+  if (n > worth) n = worth;
   if (n > MTV_MAX_PREFILL_SPLITS) n = MTV_MAX_PREFILL_SPLITS;
-  *nsplit_out = n < 2 ? 1 : int(n);
-  *bytes_out = workspace_bytes_of(*nsplit_out, num_q, num_heads);
+  *nsplit_out = n < 2 ? 1 : int(n + (tail ? over * kSplitLast : 0));
+  *bytes_out = Splits(*nsplit_out, blocks, num_q, num_heads).bytes();
   return MTV_OK;
 }
 
@@ -591,11 +637,14 @@ extern "C" int mla_prefill_run(const void* q, int64_t q_tok_stride, int64_t q_he
       max_q > MTV_MAX_PREFILL_ROWS || max_kv > MTV_MAX_PREFILL_ROWS || num_q > MTV_MAX_PREFILL_ROWS ||
       num_kv > MTV_MAX_PREFILL_ROWS || num_heads < 0 ||
       num_heads > MTV_MAX_HEADS || (dtype != MTV_DTYPE_BF16 && dtype != MTV_DTYPE_FP16) || !isfinite(scale * mtv::kLog2e) ||
-      !(scale > 0) || (causal != 0 && causal != 1) || nsplit < 1 || nsplit > MTV_MAX_PREFILL_SPLITS)
+      !(scale > 0) || (causal != 0 && causal != 1) || nsplit < 1 || nsplit % kSplitLast < 1 ||
+      nsplit % kSplitLast > MTV_MAX_PREFILL_SPLITS)
     return MTV_E_BAD_ARGUMENT;
-  if (nsplit > 1) {
+  const int64_t q_blocks = (max_q + kBlockRows - 1) / kBlockRows;
+  const Splits splits(nsplit, q_blocks * num_heads * bs, num_q, num_heads);
+  if (splits.count > 1) {
     if (!workspace) return MTV_E_NULL_POINTER;
-    if (workspace_bytes < workspace_bytes_of(nsplit, num_q, num_heads)) return MTV_E_WORKSPACE_SMALL;
+    if (workspace_bytes < splits.bytes()) return MTV_E_WORKSPACE_SMALL;
     if (reinterpret_cast<uintptr_t>(workspace) & 255) return MTV_E_WORKSPACE_ALIGN;
   }
   if (bs == 0 || max_q == 0 || num_q == 0 || num_heads == 0) return MTV_OK;
@@ -611,9 +660,7 @@ extern "C" int mla_prefill_run(const void* q, int64_t q_tok_stride, int64_t q_he
     if (!mappable_stride(s)) return MTV_E_BAD_ARGUMENT;
   if ((num_q > 1 && q_tok_stride == 0) || (num_kv > 1 && (k_tok_stride == 0 || k_rope_stride == 0 || v_tok_stride == 0)))
     return MTV_E_BAD_ARGUMENT;
-  const int64_t q_blocks = (max_q + kBlockRows - 1) / kBlockRows;
-  if (q_blocks * nsplit > INT32_MAX || q_blocks * nsplit * num_heads > INT32_MAX ||
-      q_blocks * nsplit * num_heads * bs > INT32_MAX)
+  if (q_blocks * num_heads * bs + splits.last * (splits.count - 1) > INT32_MAX)
     return MTV_E_UNSUPPORTED;
   PrefillArgs A;
   const bool bf16 = dtype == MTV_DTYPE_BF16;
@@ -629,7 +676,8 @@ extern "C" int mla_prefill_run(const void* q, int64_t q_tok_stride, int64_t q_he
   A.out = out, A.lse = lse, A.part = static_cast<float*>(workspace), A.qo_indptr = qo_indptr, A.kv_indptr = kv_indptr;
   A.err = err, A.o_tok = out_tok_stride, A.o_head = out_head_stride, A.num_q = num_q, A.num_kv = num_kv;
   A.max_q = max_q, A.max_kv = max_kv, A.scale = scale, A.bs = bs, A.heads = num_heads, A.causal = causal;
-  A.nsplit = nsplit, A.q_blocks = int(q_blocks);
+  A.nsplit = splits.count, A.q_blocks = int(q_blocks), A.last = int(splits.last), A.part_rows = splits.rows;
+  A.whole = unsigned(q_blocks * num_heads * bs - splits.last), A.by_block = splits.by_block;
   A.q_by_head = q_head_stride != 0, A.k_by_head = k_head_stride != 0, A.v_by_head = v_head_stride != 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = bf16 ? launch_prefill<__nv_bfloat16>(A, st) : launch_prefill<__half>(A, st);

@@ -674,3 +674,98 @@ def test_absorbed_and_expanded_layers_agree():
     assert (lse - lse_a).abs().max() < 0.25
     assert (out.float() - values.float()).abs().max() < 0.16
     assert (out.float() - values.float()).square().mean().sqrt() < 0.02 * max(1.0, out.float().square().mean().sqrt().item())
+
+
+# ----------------------------------------- prefill, the last blocks' keys split
+
+LAST = 256  # one of nsplit's split blocks
+# two results of values below 5 in bf16: the weights' and the output's half step each
+TWICE = 4 * 5 * 2.0 ** -8
+
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("n,blocks", [(2, 1), (3, 2), (9, 3), (64, 5), (2, 20), (1, 2)])
+@pytest.mark.parametrize("name", ["two tiles", "odd", "ragged", "fewer keys", "first rows without keys"])
+def test_prefill_with_the_last_blocks_split(name, n, blocks, dtype):
+    check_prefill(prefill_batch(41, CASES[name], 2, TYPES[dtype]), TYPES[dtype], nsplit=n + LAST * blocks)
+
+
+def test_prefill_of_all_keys_with_the_last_blocks_split():
+    check_prefill(prefill_batch(43, CASES["odd"], 3, torch.bfloat16), torch.bfloat16, causal=False, nsplit=4 + LAST * 2)
+
+
+def test_prefill_splits_the_last_blocks_only():
+    """Blocks before the last are as without a split, and the workspace is used to its documented size."""
+    b = prefill_batch(47, [(300, 700), (200, 600)], 2, torch.bfloat16)
+    want, want_lse = check_prefill(b, torch.bfloat16)
+    size = 3 * 3 * 256 * 129 * 4
+    ws = torch.full((size + 256,), 77, dtype=torch.uint8, device=DEV)
+    out, lse, err = torch.zeros_like(want), torch.zeros_like(want_lse), torch.zeros(1, dtype=torch.int32, device=DEV)
+    run = lambda space: pkg.prefill_run(b["q"], b["k_nope"], b["k_rope"], b["v"], i64(b["qo"]), i32(b["kv"]), 300, 700,  # noqa: E731
+                                        192 ** -0.5, out, lse, nsplit=3 + LAST * 3, workspace=space, err=err)
+    run(ws[:size])
+    assert int(err) == 0 and (ws[size:] == 77).all()
+    # two blocks a head by its bound of 300 rows: the last three are those of the second request's rows
+    assert torch.equal(out[:300], want[:300]) and torch.equal(lse[:300], want_lse[:300])
+    ref = L.prefill(b["q"], b["k_nope"], b["k_rope"], b["v"], b["qo"], b["kv"], 192 ** -0.5, True)
+    real = slice(300, 500)
+    bound, lse_bound = prefill_bounds({k: v[real] for k, v in ref.items()}, 700, torch.bfloat16)
+    within(out.cpu()[real], ref["out"][real], bound, "out")
+    within(lse.cpu()[real], ref["lse"][real], lse_bound, "lse")
+    with pytest.raises(pkg.MtvError):
+        run(ws[:size - 1])
+
+
+@pytest.mark.parametrize("nsplit", [2 + LAST, 5 + LAST * 4])
+def test_prefill_with_the_last_blocks_split_flags_bad_offsets(nsplit):
+    b = prefill_batch(53, [(10, 20), (10, 20), (20, 30)], 2, torch.bfloat16)
+    out = torch.full((43, 2, 128), 5.0, dtype=torch.bfloat16, device=DEV)
+    lse, err = torch.full((43, 2), 5.0, device=DEV), torch.zeros(1, dtype=torch.int32, device=DEV)
+    ws = torch.full((64 * 4 * 256 * 129,), 255, dtype=torch.uint8, device=DEV)
+    pkg.prefill_run(b["q"], b["k_nope"], b["k_rope"], b["v"], i64([0, 10, 20, 40]), i32([0, 20, 40, 999]), 20, 40, 192 ** -0.5,
+                    out, lse, nsplit=nsplit, workspace=ws, err=err)
+    assert int(err) == binding.DEVERR_INDPTR
+    assert (out[20:] == 5).all() and (lse[20:] == 5).all()
+    want, want_lse = check_prefill({**b, "qo": b["qo"][:3], "kv": b["kv"][:3]}, torch.bfloat16)
+    torch.testing.assert_close(out[:20], want[:20], rtol=0, atol=TWICE)  # the first requests are there
+
+
+def test_prefill_object_splits_a_part_filled_wave():
+    """A few blocks more than SMs over long keys, and a smaller batch in the same object."""
+    sms = torch.cuda.get_device_properties(0).multi_processor_count
+    heads = sms + 3
+    p = pkg.MlaPrefill(1, 20, 23, 2100, heads)
+    assert p.nsplit % LAST > 1 and p.nsplit // LAST == 3
+    b = prefill_batch(59, [(20, 2100)], heads, torch.bfloat16)
+    want, want_lse = check_prefill(b, torch.bfloat16)
+    out, lse = p(b["q"], b["k_nope"], b["k_rope"], b["v"], i64(b["qo"]), i32(b["kv"]), 192 ** -0.5)
+    assert p.device_error() == 0
+    assert torch.equal(out[:20, :sms], want[:20, :sms]) and torch.equal(lse[:20, :sms], want_lse[:20, :sms])
+    few = slice(sms, heads)
+    ref = L.prefill(b["q"][:, few], b["k_nope"][:, few], b["k_rope"], b["v"][:, few], b["qo"], b["kv"], 192 ** -0.5, True)
+    bound, lse_bound = prefill_bounds({k: v[:20] for k, v in ref.items()}, 2100, torch.bfloat16)
+    within(out.cpu()[:20, few], ref["out"][:20], bound, "out")
+    within(lse.cpu()[:20, few], ref["lse"][:20], lse_bound, "lse")
+    short = {**b, "qo": [0, 5], "kv": [0, 700]}
+    got, _ = p(b["q"], b["k_nope"], b["k_rope"], b["v"], i64(short["qo"]), i32(short["kv"]), 192 ** -0.5)
+    want, _ = check_prefill(short, torch.bfloat16)
+    assert torch.equal(got[:5, :sms], want[:5, :sms])
+    torch.testing.assert_close(got[:5, few], want[:5, few], rtol=0, atol=TWICE)
+
+
+def test_prefill_with_the_last_blocks_split_in_a_graph():
+    b = prefill_batch(61, [(300, 700)], 2, torch.bfloat16)
+    eager, eager_lse = check_prefill(b, torch.bfloat16, nsplit=3 + LAST * 2)
+    out, lse = torch.full_like(eager, 5.0), torch.full_like(eager_lse, 5.0)
+    qo, kv = i64(b["qo"]), i32(b["kv"])
+    ws = torch.full((3 * 2 * 256 * 129 * 4,), 255, dtype=torch.uint8, device=DEV)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        for _ in range(2):
+            pkg.prefill_run(b["q"], b["k_nope"], b["k_rope"], b["v"], qo, kv, 300, 700, 192 ** -0.5, out, lse,
+                            nsplit=3 + LAST * 2, workspace=ws)
+    for _ in range(3):
+        out.fill_(5.0)
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, eager) and torch.equal(lse, eager_lse)

@@ -214,3 +214,30 @@ def test_extension_calls_the_library_that_ctypes_loaded(lib):
     with open("/proc/self/maps") as f:
         loaded = {line.split()[-1] for line in f if "libmla_tree_verify" in line}
     assert len(loaded) == 1 and loaded.pop().endswith("_lib/libmla_tree_verify.so")
+
+
+def test_prefill_workspace_splits_a_part_filled_wave():
+    def rule(bs, new, keys, heads):
+        nsplit, size = pkg.prefill_workspace(152, bs, new, keys, bs * new, heads)
+        n, last = nsplit % 256, nsplit // 256
+        assert size == (n * 129 * 4 * (last * 256 if last else bs * new * heads) if n > 1 else 0)
+        return n, last
+
+    assert rule(2, 1000, 6760, 64) == (2, 56)       # 512 blocks, 3 waves and 56
+    assert rule(1, 256, 8448, 160) == (16, 8)       # as many as the keys are worth
+    assert rule(1, 2048, 2048, 64) == (1, 0)        # the heads' last blocks are short
+    assert rule(1, 256, 1280, 160) == (1, 0)        # short keys
+    assert rule(1, 256, 8448, 152) == (1, 0)        # a whole wave
+    assert rule(1, 256, 8448, 152 + 76) == (2, 76)  # half a wave more
+    assert rule(1, 256, 8448, 152 + 77) == (1, 0)
+    assert rule(8, 256, 8448, 153) == (1, 0)        # many waves
+    assert rule(1, 256, 100, 160) == (1, 0)         # fewer keys than queries
+
+
+def test_prefill_refuses_split_counts(lib):
+    need = 2 * 256 * 129 * 4
+    assert prefill(lib, nsplit=2 + 256, ws=FAKE, ws_bytes=need - 1) == -4
+    assert prefill(lib, nsplit=2 + 256) == -1
+    for nsplit in (256, 65 + 256, 255, -255, -(1 << 31)):
+        assert prefill(lib, nsplit=nsplit, ws=FAKE, ws_bytes=1 << 40) == -3, nsplit
+    assert prefill(lib, nsplit=64 + 256 * 100, ws=FAKE, ws_bytes=64 * 8 * 256 * 129 * 4 - 1) == -4  # eight blocks are there
