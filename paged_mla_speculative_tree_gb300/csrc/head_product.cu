@@ -20,11 +20,12 @@
 // 13.9, floors 13.8; 4,000 tokens 70 and 57, floors 50); for few tokens the chain
 // launch -> copies -> sums -> stores (8 tokens to the latent space 4.6 us, 1.3 of
 // bytes; 64 to values 5.3, 2.0 of bytes); for one latent expanded to all heads the
-// copies of x under way beside 128 KB of weights: 36 bytes a cycle and SM, each of
-// which meets 128 outputs (8,191 tokens to 64 x 256: 104 us, 1,320 TFLOP/s; one
-// library product of that shape 85).  There, sharing x between two blocks by
-// multicast changed nothing (it is a block's own ring that binds, not L2); two
-// chunks a wait (+ 10 %) and eight warps for the sums (+ 5 %) were slower.  Copies
+// copies of x under way beside 128 KB of weights, each value of which meets 128
+// outputs (8,191 tokens to 64 x 256: 104 us), so that many tokens go to pairs of SMs
+// (head_product_pair_kernel: 87 us, 1,580 TFLOP/s; one library product of that shape
+// 85).  Without pairs, sharing x between two blocks by multicast changed nothing (it
+// is a block's own ring that binds, not L2); two chunks a wait (+ 10 %) and eight
+// warps for the sums (+ 5 %) were slower.  Copies
 // and MMAs are issued under warp-uniform branches by an elected thread: by lane 0
 // of a divergent one they took two to four times as long (186 us).
 //
@@ -281,6 +282,181 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
   if (warp == 1) tmem_dealloc(tmem, cols);
 }
 
+// Many tokens and k up to 512: a pair of SMs a unit of 256 tokens x 256 outputs, whose
+// products meet 256 outputs with every value of x that an SM takes in (the form above:
+// 128), so that the tensor cores are the bound.  Each CTA copies its 128 tokens and its
+// 128 outputs' weights, all completing on the even CTA's barriers; that CTA issues the
+// MMAs, whose commits arrive on both CTAs' barriers; each CTA stores its tokens' sums.
+constexpr int kPairTokens = 2 * kRows, kPairN = 256, kPairChunks = 8;
+constexpr uint32_t kPairW = 128 * kChunk * 2, kPairColumns = 512;
+constexpr int kAbortSpin = 1 << 20;
+
+
+template <typename T>
+__global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) head_product_pair_kernel(const __grid_constant__ TensorArgs A) {
+  extern __shared__ unsigned char smem_raw[];
+  const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
+  Ctl* ctl = reinterpret_cast<Ctl*>(smem_raw + (base - raw) + kOffCtl);
+  auto bar = [&](int i) { return base + 8u * uint32_t(i); };
+  const int tid = threadIdx.x, warp = uniform_warp(), lane = tid & 31;
+  const int rank = int(cluster_ctarank());
+  const uint32_t off_x = kOffData + uint32_t(A.chunks) * kPairW, off_out = off_x + uint32_t(A.slots) * kXSlot;
+  const int64_t pair = blockIdx.x / 2, pairs = gridDim.x / 2;
+  const int64_t first = A.units * pair / pairs, last = A.units * (pair + 1) / pairs;
+
+  if (tid == 0) {
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i == B_ACCFREE || i == B_ACCFREE + 1 ? 8 : 1);
+    ctl->abort = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == 1) {
+    tmem_alloc_pair(smem_u32(&ctl->tmem), kPairColumns);
+    tmem_relinquish_pair();
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();  // both CTAs' barriers are there
+  tc_fence_after();
+  const uint32_t tmem = ctl->tmem;
+
+  if (warp == 0) {
+    // ------------------------------------------------------------- copies
+    int slot = 0, items = 0, loads = 0, asked = 0;
+    uint32_t phase = 1;
+    const uint32_t data = uniform(base), lead = uniform(mapa(base, 0));  // its barriers take both CTAs' copies
+    auto released = [&](int b, uint32_t parity) {
+      return __all_sync(0xffffffffu, wait_for_call(bar(b), parity, ctl, A.err)) != 0;
+    };
+    bool ok = true;
+    for (Units u(first, last, A); u.more() && ok; u.next(A)) {
+      const int xh = A.x_by_head ? u.h : 0, wh = A.w_by_head ? u.h : 0;
+      const int n0 = u.n * kPairN + rank * 128, t0 = u.t * kPairTokens + rank * kRows;
+      for (int c = 0; c < A.chunks && ok; ++c) {
+        if (items >= A.slots) ok = released(B_XEMPTY + slot, phase);
+        if (!ok) break;
+        if (elect_one()) {
+          if (rank == 0) mbar_arrive_expect_tx(data + 8 * (B_XFULL + slot), 2 * kXSlot);
+          tma_load_3d_pair(data + off_x + slot * kXSlot, &A.x, c * kChunk, xh, t0, lead + 8 * (B_XFULL + slot));
+        }
+        items = items < A.slots ? items + 1 : items;
+        if (++slot == A.slots) slot = 0, phase ^= 1;
+        if (!u.fresh) continue;
+        if (c == 0) {
+          if (loads > 0) ok = released(B_WFREE, uint32_t(loads - 1) & 1);
+          if (!ok) break;
+          ++loads, asked = 0;
+        }
+        ++asked;
+        if (elect_one()) {
+          const uint32_t dst = data + kOffData + c * kPairW, full = lead + 8 * (B_WFULL + c);
+          if (rank == 0) mbar_arrive_expect_tx(data + 8 * (B_WFULL + c), 2 * kPairW);
+          if (A.w_k_major) tma_load_3d_pair(dst, &A.w, c * kChunk, wh, n0, full);
+          else for (int b = 0; b < 128; b += 64) tma_load_3d_pair(dst + b * 128, &A.w, n0 + b, wh, c * kChunk, full);
+        }
+      }
+    }
+    // what both CTAs asked for lands before either ends
+    if (rank == 0 && elect_one()) {
+      for (int i = 0; i < items; ++i) {
+        if (--slot < 0) slot = A.slots - 1, phase ^= 1;
+        drain(bar(B_XFULL + slot), phase ^ 1, A.err);
+      }
+      for (int c = 0; c < asked; ++c) drain(bar(B_WFULL + c), uint32_t(loads - 1) & 1, A.err);
+    }
+    __syncwarp();
+  } else if (warp == 1) {
+    // ------------------------------------------------------------- products
+    if (rank == 0) {
+      const uint32_t id = std::is_same<T, __nv_bfloat16>::value ? idesc_bf16_f32(kPairTokens, kPairN, 0, A.w_k_major ? 0 : 1)
+                                                                : idesc_fp16_f32(kPairTokens, kPairN, 0, A.w_k_major ? 0 : 1);
+      const uint32_t w_step = A.w_k_major ? 32u : 2048u, acc = uniform(tmem), data = uniform(base);
+      auto arrived = [&](int b, uint32_t parity) {
+        return __all_sync(0xffffffffu, wait_for_call(bar(b), parity, ctl, A.err)) != 0;
+      };
+      int slot = 0, loads = 0, n = 0;
+      uint32_t phase = 0;
+      bool ok = true;
+      for (Units u(first, last, A); u.more() && ok; u.next(A), ++n) {
+        if (u.fresh) ++loads;
+        const int buf = n & 1;
+        if (n >= 2) ok = __all_sync(0xffffffffu, wait_for_peer(bar(B_ACCFREE + buf), uint32_t(n / 2 - 1) & 1, ctl, A.err)) != 0;
+        for (int c = 0; c < A.chunks && ok; ++c) {
+          if (u.fresh) ok = arrived(B_WFULL + c, uint32_t(loads - 1) & 1);
+          if (ok) ok = arrived(B_XFULL + slot, phase);
+          if (!ok) break;
+          tc_fence_after();
+          if (elect_one()) {
+            const uint64_t a = smem_desc(data + off_x + slot * kXSlot, 16, 1024, kSwizzle128B);
+            const uint64_t b = smem_desc(data + kOffData + c * kPairW, A.w_k_major ? 16 : 8192, 1024, kSwizzle128B);
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+              mma_ss_pair(acc + uint32_t(kPairN) * buf, desc_add(a, 32 * k), desc_add(b, w_step * k), id, c + k > 0);
+            mma_commit_pair(bar(B_XEMPTY + slot));
+          }
+          if (++slot == A.slots) slot = 0, phase ^= 1;
+        }
+        if (!ok) break;
+        if (elect_one()) {
+          mma_commit_pair(bar(B_ACC + buf));
+          if (u.changes(A)) mma_commit_pair(bar(B_WFREE));
+        }
+      }
+      if (elect_one()) mma_commit_pair(bar(B_FIN));
+    }
+    if (elect_one()) drain(bar(B_FIN), 0, A.err);  // the last of the commits that arrive here
+    __syncwarp();
+  } else {
+    // ------------------------------------------------------------- sums to memory
+    const int q = warp & 3;
+    const uint32_t stage = base + off_out + uint32_t(q) * kBlockBytes;
+    const uint32_t freed = mapa(bar(B_ACCFREE), 0);
+    int n = 0;
+    for (Units u(first, last, A); u.more(); u.next(A), ++n) {
+      const int n0 = u.n * kPairN, buf = n & 1;
+      const int64_t t0 = int64_t(u.t) * kPairTokens + rank * kRows + q * 32;
+      const bool ok = wait_for_call(bar(B_ACC + buf), uint32_t(n / 2) & 1, ctl, A.err);
+      if (!__all_sync(0xffffffffu, ok)) break;
+      tc_fence_after();
+      const int width = t0 < A.tokens ? min(kPairN, A.n_dim - n0) : 0;
+      for (int b = 0; b < width; b += 64) {
+        uint32_t y[64];
+        tmem_ld64_sync(tmem + (uint32_t(q * 32) << 16) + uint32_t(kPairN) * buf + b, y);
+        if (lane == 0) bulk_wait_group_read<0>();  // the last store has read the block
+        __syncwarp();
+#pragma unroll
+        for (int e = 0; e < 64; e += 8) {
+          float f[8];
+#pragma unroll
+          for (int i = 0; i < 8; ++i) f[i] = __uint_as_float(y[e + i]);
+          const uint4 v = pack<T>(f);
+          st_shared_v4(stage + lane * 128 + (((e / 8) ^ (lane & 7)) << 4), v.x, v.y, v.z, v.w);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          tma_store_3d(&A.out, n0 + b, A.out_by_head ? u.h : 0, int(t0), stage);
+          bulk_commit_group();
+        }
+      }
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(freed + 8 * buf);
+    }
+    if (lane == 0) bulk_wait_group_read<0>();
+    __syncwarp();
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (ctl->abort) {  // copies may be under way that the even CTA's barriers do not count
+    const long long t0 = clock64();
+    while (clock64() - t0 < kAbortSpin) {}
+  }
+  cluster_sync();  // no product reads, and no copy or commit writes, the other CTA's memory any more
+  tc_fence_after();
+  if (warp == 1) tmem_dealloc_pair(tmem, kPairColumns);
+  cluster_sync();
+}
+
 int sm_count() {
   int device = 0, sms = 0;
   if (cudaGetDevice(&device) != cudaSuccess ||
@@ -323,12 +499,20 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
   P.n_tiles = (A.n_dim + P.nt - 1) / P.nt;
   P.units = int64_t(A.heads) * P.n_tiles * P.m_tiles;
   const bool bf16 = std::is_same<T, __nv_bfloat16>::value;
+  // Pairs of SMs where the weights of 256 outputs do not fit one and fill two (n_dim 320 would leave a quarter of
+  // the products empty: 4,000 tokens 64 us, not 55), where tokens do too (but for a ninth), from five units a pair on (8,191 tokens expanded to 64 x 256:
+  // 104 -> 87 us; 4,000 with rows for each head 105 -> 74; 1,400, 5 units: 24 and 24; 800, 3 units: 16 and 18).
+  const int pair_m = int((A.tokens + kPairTokens - 1) / kPairTokens), pair_n = (A.n_dim + kPairN - 1) / kPairN;
+  const int64_t pair_units = int64_t(A.heads) * pair_n * pair_m, pairs = sms / 2;
+  const bool pair = P.chunks > kPairChunks / 2 && P.chunks <= kPairChunks && (A.n_dim + 127) / 128 == 2 * pair_n &&
+                    16 * pair_m <= 9 * P.m_tiles && pairs > 0 && pair_units >= 5 * pairs;
+  if (pair) P.m_tiles = pair_m, P.n_tiles = pair_n, P.nt = kPairN, P.units = pair_units;
   P.w_k_major = A.w_k == 1;
   // A copy costs its issue (about 150 cycles) and its box, inside the tensor or not.  So one tile of tokens
   // takes several chunks of weights and of x with a copy, x in boxes as low as it is (what a slot holds below
   // such a box makes sums that nobody stores): values of 64 tokens 6.3 -> 5.3 us.  Many tokens stream chunk by
-  // chunk, which keeps more copies under way (8,191 tokens expanded: 104 us, with the other form 142).
-  const bool few = P.m_tiles == 1;
+  // chunk, which keeps more copies under way (8,191 tokens expanded without pairs: 104 us, with the other form 142).
+  const bool few = !pair && P.m_tiles == 1;
   const int x_rows = few ? int(A.tokens + 7) / 8 * 8 : kRows;
   P.x_bytes = uint32_t(x_rows) * kChunk * 2;
   P.x_whole = few && A.k_dim % kChunk == 0, P.w_whole = few && (P.w_k_major ? A.k_dim : A.n_dim) % 64 == 0;
@@ -341,12 +525,19 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
   P.slots = int((227u * 1024u - fixed) / (P.gx * P.x_bytes));
   if (P.slots > kMaxSlots) P.slots = kMaxSlots;
   const uint32_t smem = fixed + P.slots * P.gx * P.x_bytes;
+  uint32_t pair_smem = 0;
+  if (pair) {  // one staged block a warp: a slot more of x is worth more (87 us; four slots 89, three 97)
+    const uint32_t pair_fixed = 1024 + kOffData + uint32_t(P.chunks) * kPairW + 4 * kBlockBytes;
+    P.slots = int((227u * 1024u - pair_fixed) / kXSlot);
+    if (P.slots > kMaxSlots) P.slots = kMaxSlots;
+    pair_smem = pair_fixed + P.slots * kXSlot;
+  }
   P.x_by_head = A.x_head != 0, P.w_by_head = A.w_head != 0, P.out_by_head = 1;
   if (A.heads == 1) P.x_by_head = P.w_by_head = P.out_by_head = 0;
   P.err = A.err, P.tokens = A.tokens, P.n_dim = A.n_dim;
   // weights: rows, their stride, their length, and the rows of a box
   const int64_t w_rows = P.w_k_major ? A.n_dim : A.k_dim, w_row = P.w_k_major ? A.w_n : A.w_k;
-  const int w_dim = P.w_k_major ? A.k_dim : A.n_dim, w_box = P.w_k_major ? P.nt : 64;
+  const int w_dim = P.w_k_major ? A.k_dim : A.n_dim, w_box = P.w_k_major ? (pair ? 128 : P.nt) : 64;
   const bool maps =
       (few ? encode_chunked_map(&P.x, bf16, A.x, A.tokens, A.x_tok, A.heads, A.x_head, A.k_dim, P.x_whole, x_rows, P.gx) &&
                  encode_chunked_map(&P.w, bf16, A.w, w_rows, w_row, A.heads, A.w_head, w_dim, P.w_whole, w_box,
@@ -355,6 +546,12 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
                  encode_heads_map(&P.w, bf16, A.w, w_rows, w_row, A.heads, A.w_head, w_dim, 64, w_box)) &&
       encode_heads_map(&P.out, bf16, A.out, A.tokens, A.out_tok, A.heads, A.out_head, A.n_dim, 64, 32);
   if (!maps) return cudaErrorInvalidValue;
+  if (pair) {
+    const cudaError_t e = cudaFuncSetAttribute(head_product_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    if (e != cudaSuccess) return e;
+    head_product_pair_kernel<T><<<2 * unsigned(pairs), kThreads, pair_smem, st>>>(P);
+    return cudaGetLastError();
+  }
   auto kernel = few ? head_product_kernel<T, true> : head_product_kernel<T, false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;

@@ -40,6 +40,19 @@ static __device__ __noinline__ bool wait_slow_call(uint32_t bar, uint32_t parity
 __device__ __forceinline__ bool wait_for_call(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err) {
   return ptx::mbar_try_wait(bar, parity) || wait_slow_call(bar, parity, ctl, err);
 }
+// For a barrier that the other CTA of a cluster arrives on.
+static __device__ __noinline__ bool wait_for_peer(uint32_t bar, uint32_t parity, Ctl* ctl, uint32_t* err) {
+  const long long t0 = clock64();
+  while (!ptx::mbar_try_wait_cluster(bar, parity)) {
+    if (ctl->abort) return false;
+    if (clock64() - t0 > kWaitCycles) {
+      ctl->abort = 1;
+      if (err) atomicOr(err, MTV_DEVERR_TIMEOUT);
+      return false;
+    }
+  }
+  return true;
+}
 // For what has to land before the block may end: ignores the flag.
 __device__ __forceinline__ void drain(uint32_t bar, uint32_t parity, uint32_t* err) {
   const long long t0 = clock64();

@@ -769,3 +769,64 @@ def test_prefill_with_the_last_blocks_split_in_a_graph():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, eager) and torch.equal(lse, eager_lse)
+
+
+# ------------------------------------------------- products of pairs of SMs
+
+PAIRED = [(130, 400, 264, 136), (200, 191, 320, 400), (24400, 4, 264, 256), (97500, 1, 512, 200)]  # five units a pair and more
+
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("tokens,heads,k,n", PAIRED)
+@pytest.mark.parametrize("dense", ["n", "k"])
+def test_head_product_of_many_tokens(tokens, heads, k, n, dense, dtype):
+    """NaN behind x and around w; outputs inside wider rows."""
+    t = TYPES[dtype]
+    x = torch.full((tokens + 5, heads, k + 8), math.nan, dtype=t, device=DEV)
+    x[:tokens, :, :k] = rnd(tokens, (tokens, heads, k), t)
+    shape = (heads, k, n) if dense == "n" else (heads, n, k)
+    w = torch.full((heads, shape[1] + 8, shape[2] + 8), math.nan, dtype=t, device=DEV)
+    w[:, :shape[1], :shape[2]] = rnd(n + k, shape, t)
+    w = w[:, :shape[1], :shape[2]]
+    check_product(x[:tokens, :, :k], w if dense == "n" else w.transpose(1, 2), pad_dim=8)
+
+
+@pytest.mark.parametrize("dense", ["n", "k"])
+def test_head_product_of_many_tokens_shared_by_the_heads(dense):
+    rows = rnd(3, (2050, 576), torch.bfloat16)
+    x = rows[:, None, :512].expand(2050, 50, 512)
+    w = rnd(5, (50, 256, 512), torch.bfloat16, 0.05).transpose(1, 2)
+    check_product(x, w if dense == "k" else w.contiguous(), pad_dim=0)
+
+
+def test_head_product_of_many_tokens_again_and_in_a_graph():
+    x, w = rnd(1, (1024, 100, 512), torch.bfloat16), rnd(2, (100, 512, 256), torch.bfloat16)
+    first, again = torch.empty((2, 1024, 100, 256), dtype=torch.bfloat16, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    pkg.head_product(x, w, first, err=err)
+    graph, side = torch.cuda.CUDAGraph(), torch.empty_like(first)
+    with torch.cuda.graph(graph):
+        pkg.head_product(x, w, again, err=err)
+        pkg.head_product(x, w, side, err=err)
+    for _ in range(3):
+        again.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(first, again) and torch.equal(first, side) and int(err) == 0
+
+
+def test_head_products_of_many_tokens_on_two_streams():
+    x, w = rnd(1, (1024, 100, 512), torch.bfloat16), rnd(2, (100, 512, 256), torch.bfloat16)
+    want = torch.empty((1024, 100, 256), dtype=torch.bfloat16, device=DEV)
+    pkg.head_product(x, w, want)
+    few = torch.empty((8, 100, 256), dtype=torch.bfloat16, device=DEV)
+    pkg.head_product(x[:8], w, few)
+    outs, fews = [torch.zeros_like(want) for _ in range(6)], [torch.zeros_like(few) for _ in range(6)]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for i in range(6):
+        with torch.cuda.stream(streams[i % 2]):
+            pkg.head_product(x, w, outs[i])
+            pkg.head_product(x[:8], w, fews[i])
+    torch.cuda.synchronize()
+    assert all(torch.equal(o, want) for o in outs) and all(torch.equal(o, few) for o in fews)
