@@ -17,7 +17,8 @@
 //
 // What bounds it (one GB300, 64 heads): the bytes where each head has rows of its
 // own (1,024 tokens: queries to the latent space 14.9 us, latent outputs to values
-// 13.9, floors 13.8; 4,000 tokens 70 and 57, floors 50); for few tokens the chain
+// 13.9, floors 13.8; 4,000 tokens 70 and 57, floors 50, but the first writes 262 MB,
+// which a plain fill does in 68); for few tokens the chain
 // launch -> copies -> sums -> stores (8 tokens to the latent space 4.6 us, 1.3 of
 // bytes; 64 to values 5.3, 2.0 of bytes); for one latent expanded to all heads the
 // copies of x under way beside 128 KB of weights, each value of which meets 128

@@ -508,11 +508,12 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pr
   const PrefillBlock B(A, A.whole + blockIdx.x);
   const int row = kWarpRow ? int(blockIdx.y) * 4 + warp : int(blockIdx.y), h = B.h, i = B.row0 + row;
   const PrefillReq R = load_prefill_req(A, B.r, false);
+  // launched while the parts are being written; blocks without rows wait too: this kernel has to end after the other
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (i >= R.n) return;
   const int64_t at = int64_t(R.q0 + i) * A.heads + h, all = A.part_rows;
   const int64_t part_at = A.by_block ? int64_t(blockIdx.x) * kBlockRows + row : at;
   const float* lse = A.part + A.nsplit * all * kV + part_at;
-  asm volatile("griddepcontrol.wait;" ::: "memory");  // launched while the parts are being written
   const float a = lane < A.nsplit ? lse[lane * all] : -INFINITY;
   const float b = !kWarpRow && lane + 32 < A.nsplit ? lse[(lane + 32) * all] : -INFINITY;
   float top = fmaxf(a, b);
