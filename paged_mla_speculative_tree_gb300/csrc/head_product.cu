@@ -38,6 +38,7 @@
 #include <type_traits>
 
 #include "mla_layer_ops.h"
+#include "launch.cuh"
 #include "mtv_internal.cuh"
 #include "pipeline.cuh"
 #include "tc_ptx.cuh"
@@ -129,6 +130,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
     tmem_alloc(smem_u32(&ctl->tmem), cols);
     tmem_relinquish();
   }
+  launched_after();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -314,6 +316,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) head_pr
     tmem_alloc_pair(smem_u32(&ctl->tmem), kPairColumns);
     tmem_relinquish_pair();
   }
+  launched_after();
   tc_fence_before();
   __syncthreads();
   cluster_sync();  // both CTAs' barriers are there
@@ -550,15 +553,13 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
   if (pair) {
     const cudaError_t e = cudaFuncSetAttribute(head_product_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
-    head_product_pair_kernel<T><<<2 * unsigned(pairs), kThreads, pair_smem, st>>>(P);
-    return cudaGetLastError();
+    return launch_early(head_product_pair_kernel<T>, dim3(2 * unsigned(pairs)), kThreads, pair_smem, st, P);
   }
   auto kernel = few ? head_product_kernel<T, true> : head_product_kernel<T, false>;
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;
   const unsigned grid = unsigned(P.units < sms ? P.units : sms);
-  kernel<<<grid, kThreads, smem, st>>>(P);
-  return cudaGetLastError();
+  return launch_early(kernel, dim3(grid), kThreads, smem, st, P);
 }
 
 // The plain form, for any strides: a block a tile of 64 tokens x 64 outputs of

@@ -1,0 +1,28 @@
+// Launches whose blocks may start while the stream's kernel before is ending: they
+// set up, then wait for its end and its writes (launched_after) before they touch
+// global memory.  Every block waits, also one without work, so that a kernel never
+// ends before the one that it was launched after.
+#pragma once
+
+#include <cuda_runtime.h>
+
+namespace mtv {
+
+__device__ __forceinline__ void launched_after() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+template <typename... P>
+cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const P&... args) {
+  cudaLaunchAttribute early[1];
+  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  early[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t config = {};
+  config.gridDim = grid;
+  config.blockDim = dim3(threads);
+  config.dynamicSmemBytes = smem;
+  config.stream = st;
+  config.attrs = early;
+  config.numAttrs = 1;
+  return cudaLaunchKernelEx(&config, kernel, args...);
+}
+
+}  // namespace mtv

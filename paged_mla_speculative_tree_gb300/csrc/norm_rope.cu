@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "mla_layer_ops.h"
+#include "launch.cuh"
 #include "mtv_internal.cuh"
 #include "vec_io.cuh"
 
@@ -170,6 +171,7 @@ __global__ void __launch_bounds__(kVecThreads, NN <= 2 ? (sizeof(T) == 4 ? 3 : 4
   constexpr int V = 16 / int(sizeof(T)), M = kHalf ? 2 : 1;
   constexpr int kLatentUnits = kDLat / V / 32;
   __shared__ __align__(16) float cos_s[MTV_MAX_ROPE_DIM / 2], sin_s[MTV_MAX_ROPE_DIM / 2];
+  launched_after();
   const int64_t t = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 31, l = tid & 7, group = tid >> 3;
   const bool queries = A.q_in && tid < kGroups * 8, latents = A.pool && tid >= kGroups * 8;
@@ -327,12 +329,15 @@ template <typename T, bool kHalf> cudaError_t launch_norm_layout(const NormArgs&
   constexpr int v = 16 / int(sizeof(T));
   const unsigned grid = unsigned(tokens);
   const int plain = A.q_weight ? (A.nope_dim / v + 7) / 8 : 0, turned = (A.rope_dim / v / (kHalf ? 2 : 1) + 7) / 8;
-  if (!vector_form<T>(A) || plain > 8 || turned > 2) norm_rope_plain_kernel<T, kHalf><<<grid, kPlainThreads, 0, st>>>(A);
-  else if (plain == 0) norm_rope_vec_kernel<T, kHalf, 0, 2><<<grid, kVecThreads, 0, st>>>(A);
-  else if (plain <= 2 && turned == 1) norm_rope_vec_kernel<T, kHalf, 2, 1><<<grid, kVecThreads, 0, st>>>(A);
-  else if (plain <= 4) norm_rope_vec_kernel<T, kHalf, 4, 2><<<grid, kVecThreads, 0, st>>>(A);
-  else norm_rope_vec_kernel<T, kHalf, 8, 2><<<grid, kVecThreads, 0, st>>>(A);
-  return cudaGetLastError();
+  if (!vector_form<T>(A) || plain > 8 || turned > 2) {
+    norm_rope_plain_kernel<T, kHalf><<<grid, kPlainThreads, 0, st>>>(A);
+    return cudaGetLastError();
+  }
+  auto kernel = plain == 0                  ? norm_rope_vec_kernel<T, kHalf, 0, 2>
+                : plain <= 2 && turned == 1 ? norm_rope_vec_kernel<T, kHalf, 2, 1>
+                : plain <= 4                ? norm_rope_vec_kernel<T, kHalf, 4, 2>
+                                            : norm_rope_vec_kernel<T, kHalf, 8, 2>;
+  return launch_early(kernel, dim3(grid), kVecThreads, 0, st, A);
 }
 
 template <typename T> cudaError_t launch_norm(const NormArgs& A, int layout, int64_t tokens, cudaStream_t st) {

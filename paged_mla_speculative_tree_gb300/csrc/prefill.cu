@@ -53,6 +53,7 @@
 
 #include "mla_layer_ops.h"
 #include "mtv_internal.cuh"
+#include "launch.cuh"
 #include "pipeline.cuh"
 #include "tc_ptx.cuh"
 #include "tma.cuh"
@@ -143,6 +144,19 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const int split = split_keys ? int((blockIdx.x - A.whole) / unsigned(A.last)) : 0;
   const PrefillBlock B(A, split_keys ? A.whole + tail : blockIdx.x);
   const int row0 = B.row0, h = B.h;
+  // the set-up needs nothing from memory
+  if (tid == 0) {
+    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_KFREE && i < B_S ? 2 : i >= B_P && i < B_O ? 4 : 1);
+    ctl->abort = 0;
+    fence_mbar_init_cluster();
+  }
+  if (warp == 10 && lane == 0) {
+    prefetch_map(&A.q);
+    prefetch_map(&A.k_nope);
+    prefetch_map(&A.k_rope);
+    prefetch_map(&A.v);
+  }
+  launched_after();
   const PrefillReq R = load_prefill_req(A, B.r, tid == 0);
   if (row0 >= R.n) return;
 
@@ -161,17 +175,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const int T0 = mine(tiles0), T1 = mine(tiles1), TN = max(T0, T1);
   auto stage_tiles = [&](int s) { return s ? T1 : T0; };
 
-  if (tid == 0) {
-    for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_KFREE && i < B_S ? 2 : i >= B_P && i < B_O ? 4 : 1);
-    ctl->abort = 0;
-    fence_mbar_init_cluster();
-  }
-  if (warp == 10 && lane == 0) {
-    prefetch_map(&A.q);
-    prefetch_map(&A.k_nope);
-    prefetch_map(&A.k_rope);
-    prefetch_map(&A.v);
-  }
   if (warp == 8) {
     tmem_alloc(smem_u32(&ctl->tmem), 512);
     tmem_relinquish();
@@ -507,9 +510,8 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pr
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const PrefillBlock B(A, A.whole + blockIdx.x);
   const int row = kWarpRow ? int(blockIdx.y) * 4 + warp : int(blockIdx.y), h = B.h, i = B.row0 + row;
+  launched_after();
   const PrefillReq R = load_prefill_req(A, B.r, false);
-  // launched while the parts are being written; blocks without rows wait too: this kernel has to end after the other
-  asm volatile("griddepcontrol.wait;" ::: "memory");
   if (i >= R.n) return;
   const int64_t at = int64_t(R.q0 + i) * A.heads + h, all = A.part_rows;
   const int64_t part_at = A.by_block ? int64_t(blockIdx.x) * kBlockRows + row : at;
@@ -564,21 +566,12 @@ template <typename T> cudaError_t launch_prefill(const PrefillArgs& A, cudaStrea
   const unsigned blocks = A.whole + unsigned(A.last) * unsigned(A.nsplit);
   cudaError_t e = cudaFuncSetAttribute(prefill_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
   if (e != cudaSuccess) return e;
-  prefill_kernel<T><<<blocks, kThreads, kSmem, st>>>(A);
-  e = cudaGetLastError();
+  e = launch_early(prefill_kernel<T>, dim3(blocks), kThreads, kSmem, st, A);
   if (e != cudaSuccess || A.nsplit == 1) return e;
-  cudaLaunchAttribute early[1];
-  early[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  early[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t config = {};
   const bool warp_row = A.nsplit <= kWarpParts;
   const unsigned rows = unsigned(A.max_q < kBlockRows ? A.max_q : kBlockRows);
-  config.gridDim = dim3(unsigned(A.last), warp_row ? (rows + 3) / 4 : rows);
-  config.blockDim = dim3(128);
-  config.stream = st;
-  config.attrs = early;
-  config.numAttrs = 1;
-  return cudaLaunchKernelEx(&config, warp_row ? combine_kernel<T, true> : combine_kernel<T, false>, A);
+  return launch_early(warp_row ? combine_kernel<T, true> : combine_kernel<T, false>,
+                      dim3(unsigned(A.last), warp_row ? (rows + 3) / 4 : rows), 128, 0, st, A);
 }
 
 // nsplit's two numbers, of `blocks` blocks: how many of the last ones are split
