@@ -830,3 +830,72 @@ def test_head_products_of_many_tokens_on_two_streams():
             pkg.head_product(x[:8], w, fews[i])
     torch.cuda.synchronize()
     assert all(torch.equal(o, want) for o in outs) and all(torch.equal(o, few) for o in fews)
+
+
+# --------------------------------- kernels that set up while the one before ends
+
+@pytest.mark.parametrize("tokens,heads,dim", [(8, 64, 128), (300, 20, 512), (1024, 80, 512), (40, 3, 100)])
+def test_products_in_a_row_read_what_the_call_before_wrote(tokens, heads, dim):
+    """Each call's input is the output of the one before, or of a copy; in a row as with a wait after each."""
+    ws = [rnd(70 + i, (heads, dim, dim), torch.bfloat16, dim ** -0.5) for i in range(4)]
+    sources = [rnd(80 + i, (tokens, heads, dim), torch.bfloat16) for i in range(6)]
+    x = torch.empty_like(sources[0])
+    mids = [torch.empty_like(x) for _ in range(4)]
+
+    def run(source, wait):
+        x.copy_(source)
+        at = x
+        for w, mid in zip(ws, mids):
+            pkg.head_product(at, w, mid)
+            if wait:
+                torch.cuda.synchronize()
+            at = mid
+        return at.clone()
+
+    want = [run(s, True) for s in sources]
+    got = [run(s, False) for s in sources * 3]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        captured = [run(s, False) for s in sources]
+    graph.replay()
+    torch.cuda.synchronize()
+    for i, g in enumerate(got):
+        assert torch.equal(g, want[i % 6])
+    for g, w in zip(captured, want):
+        assert torch.equal(g, w)
+
+
+def test_a_layer_in_a_row_is_as_with_a_wait_after_each_call():
+    """Norms, expansion and prompt attention with and without split keys, a new pass right behind the last."""
+    heads, rows = 8, 40
+    up = rnd(91, (heads, 256, 512), torch.bfloat16, 512 ** -0.5)
+    q_in, c_in, k_in = rnd(92, (rows, heads, 192), torch.bfloat16), rnd(93, (rows, 512), torch.bfloat16), rnd(94, (rows, 64), torch.bfloat16)
+    q_weight, c_weight = rnd(95, (192,), torch.bfloat16), rnd(96, (512,), torch.bfloat16)
+    old = 1500
+    pool = rnd(97, (old + rows, 576), torch.bfloat16)
+    start = pool.clone()
+    turns, amplitude = pkg.rope_freqs(64, 1e4)
+    turns = turns.to(DEV)
+    positions, loc = torch.arange(old, old + rows, device=DEV), torch.arange(old, old + rows, device=DEV)
+    q = torch.empty_like(q_in)
+    kv = torch.empty((old + rows, heads, 256), dtype=torch.bfloat16, device=DEV)
+    qo, ko = i64([0, rows]), i32([0, old + rows])
+    attention = pkg.MlaPrefill(1, rows, rows, old + rows, heads)
+    assert attention.nsplit > 1
+
+    def run(wait):
+        step = torch.cuda.synchronize if wait else lambda: None
+        pool.copy_(start)
+        kv.fill_(math.nan), q.fill_(math.nan), step()
+        pkg.norm_rope_write(turns, positions, 1e-6, amplitude=amplitude, q_in=q_in, q_weight=q_weight, q_nope=q[:, :, :128],
+                            q_rope=q[:, :, 128:], c_in=c_in, c_weight=c_weight, k_in=k_in, out_cache_loc=loc, kv_pool=pool), step()
+        pkg.head_product(pool[:, None, :512].expand(-1, heads, -1), up.transpose(1, 2), kv), step()
+        out = torch.empty((rows, heads, 128), dtype=torch.bfloat16, device=DEV)
+        lse = torch.empty((rows, heads), device=DEV)
+        attention(q, kv[:, :, :128], pool[:, 512:], kv[:, :, 128:], qo, ko, 192 ** -0.5, out, lse), step()
+        return out.clone(), lse.clone()
+
+    want = run(True)
+    for out, lse in [run(False) for _ in range(20)]:
+        assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
+    assert torch.isfinite(want[0].float()).all()
