@@ -16,14 +16,14 @@
 // dense in n an MN-major one (blocks of 64 n x 64 k).
 //
 // What bounds it (one GB300, 64 heads): the bytes where each head has rows of its
-// own (1,024 tokens: queries to the latent space 14.9 us, latent outputs to values
+// own (1,024 tokens: queries to the latent space 14.6 us, latent outputs to values
 // 13.9, floors 13.8; 4,000 tokens 70 and 57, floors 50, but the first writes 262 MB,
 // which a plain fill does in 68); for few tokens the chain
-// launch -> copies -> sums -> stores (8 tokens to the latent space 4.6 us, 1.3 of
-// bytes; 64 to values 5.3, 2.0 of bytes); for one latent expanded to all heads the
+// launch -> copies -> sums -> stores (8 tokens to the latent space 4.2 us, 1.3 of
+// bytes; 64 to values 4.9, 2.0 of bytes); for one latent expanded to all heads the
 // copies of x under way beside 128 KB of weights, each value of which meets 128
 // outputs (8,191 tokens to 64 x 256: 104 us), so that many tokens go to pairs of SMs
-// (head_product_pair_kernel: 87 us, 1,580 TFLOP/s; one library product of that shape
+// (head_product_pair_kernel: 88 us, 1,560 TFLOP/s; one library product of that shape
 // 85).  Without pairs, sharing x between two blocks by multicast changed nothing (it
 // is a block's own ring that binds, not L2); two chunks a wait (+ 10 %) and eight
 // warps for the sums (+ 5 %) were slower.  Copies
