@@ -577,12 +577,15 @@ def _extension():
     """The extension module beside the library: checks and calls on tensors as they are."""
     global _ext
     if _ext is None:
-        load()
+        lib = load()
         if not os.path.exists(_build.EXT):
             raise RuntimeError(f"extension not built: {_build.EXT} (run __graft_entry__.build())")
         spec = importlib.util.spec_from_file_location("binding_ext", _build.EXT)
-        _ext = importlib.util.module_from_spec(spec)
-        spec.loader.exec_module(_ext)
+        ext = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(ext)
+        ext.bind(*(ctypes.cast(f, ctypes.c_void_p).value
+                   for f in (lib.mla_head_product, lib.mla_prefill_run, lib.mla_norm_rope_write)))
+        _ext = ext
     return _ext
 
 

@@ -2,7 +2,8 @@
 
 Each .cu translation unit is compiled in parallel, then linked into
 ``paged_mla_speculative_tree_gb300/_lib/libmla_tree_verify.so``, and beside it
-``binding_ext.so``, the Python extension (g++) that calls some of its entries.
+``binding_ext.so``, the Python extension (g++) through which some of its entries
+are called.
 """
 from __future__ import annotations
 
@@ -93,8 +94,7 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
     os.replace(tmp, LIB)
     tmp = EXT + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, ext, "-L" + OUT_DIR, "-l:" + os.path.basename(LIB), "-Wl,-rpath,$ORIGIN", "-L" + os.path.join(torch_dir, "lib"),
-           "-ltorch_python", "-ltorch_cpu", "-lc10"]
+    cmd = ["g++", "-shared", "-o", tmp, ext, "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")

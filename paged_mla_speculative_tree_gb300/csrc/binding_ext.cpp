@@ -13,6 +13,11 @@
 
 namespace {
 
+// The C entries, of the library that is loaded already.
+decltype(&mla_head_product) head_product_entry;
+decltype(&mla_prefill_run) prefill_run_entry;
+decltype(&mla_norm_rope_write) norm_rope_write_entry;
+
 struct Refused {};  // the Python error is set
 
 [[noreturn]] void refuse(PyObject* kind, const std::string& what) {
@@ -145,7 +150,7 @@ PyObject* head_product(PyObject*, PyObject* const* args, Py_ssize_t n) {
     void* stream = stream_of(a[4]);
     if (heads > INT32_MAX || k > INT32_MAX || cols > INT32_MAX) return MTV_E_BAD_ARGUMENT;
     const Unlocked unlocked;
-    return mla_head_product(vx.at, vx.tok, vx.head, w.data_ptr(), w.stride(0), w.stride(1), w.stride(2), vo.at, vo.tok, vo.head,
+    return head_product_entry(vx.at, vx.tok, vx.head, w.data_ptr(), w.stride(0), w.stride(1), w.stride(2), vo.at, vo.tok, vo.head,
                             tokens, int(heads), int(k), int(cols), code, err, stream);
   });
 }
@@ -178,7 +183,7 @@ PyObject* prefill_run(PyObject*, PyObject* const* args, Py_ssize_t n) {
     void* stream = stream_of(a[15]);
     if (bs > INT32_MAX || heads > INT32_MAX) return MTV_E_BAD_ARGUMENT;
     const Unlocked unlocked;
-    return mla_prefill_run(vq.at, vq.tok, vq.head, vk.at, vk.tok, vk.head, vr.at, vr.tok, vv.at, vv.tok, vv.head, qp, kp, int(bs),
+    return prefill_run_entry(vq.at, vq.tok, vq.head, vk.at, vk.tok, vk.head, vr.at, vr.tok, vv.at, vv.tok, vv.head, qp, kp, int(bs),
                            max_q, max_kv, rows, keys, int(heads), code, scale, causal, vo.at, vo.tok, vo.head, lse, nsplit, wp,
                            ws ? uint64_t(ws->numel()) : 0, err, stream);
   });
@@ -235,13 +240,27 @@ PyObject* norm_rope_write(PyObject*, PyObject* const* args, Py_ssize_t n) {
     void* stream = stream_of(a[16]);
     if (rope_dim > INT32_MAX || heads > INT32_MAX || nope > INT32_MAX) return MTV_E_BAD_ARGUMENT;
     const Unlocked unlocked;
-    return mla_norm_rope_write(tp, int(rope_dim), amplitude, layout, at_, tokens, np, code, eps, vq.at, vq.tok, vq.head,
+    return norm_rope_write_entry(tp, int(rope_dim), amplitude, layout, at_, tokens, np, code, eps, vq.at, vq.tok, vq.head,
                                int(heads), int(nope), qwp, vn.at, vn.tok, vn.head, vr.at, vr.tok, vr.head, vc.at, vc.tok, cwp,
                                vk.at, vk.tok, lp, pp, slots, err, stream);
   });
 }
 
+// The addresses of mla_head_product, mla_prefill_run and mla_norm_rope_write; called once, before the others.
+PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t n) {
+  return guarded(args, n, 3, [](PyObject* const* a) -> int {
+    void* at[3];
+    for (int i = 0; i < 3; ++i)
+      if (!(at[i] = PyLong_AsVoidPtr(a[i]))) refuse(PyExc_ValueError, "an entry has no address");
+    head_product_entry = reinterpret_cast<decltype(head_product_entry)>(at[0]);
+    prefill_run_entry = reinterpret_cast<decltype(prefill_run_entry)>(at[1]);
+    norm_rope_write_entry = reinterpret_cast<decltype(norm_rope_write_entry)>(at[2]);
+    return 0;
+  });
+}
+
 PyMethodDef methods[] = {
+    {"bind", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(bind)), METH_FASTCALL, nullptr},
     {"head_product", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(head_product)), METH_FASTCALL, nullptr},
     {"prefill_run", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(prefill_run)), METH_FASTCALL, nullptr},
     {"norm_rope_write", reinterpret_cast<PyCFunction>(reinterpret_cast<void*>(norm_rope_write)), METH_FASTCALL, nullptr},

@@ -899,3 +899,47 @@ def test_a_layer_in_a_row_is_as_with_a_wait_after_each_call():
     for out, lse in [run(False) for _ in range(20)]:
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
     assert torch.isfinite(want[0].float()).all()
+
+
+def test_products_behind_a_fork_and_a_join_of_streams_in_a_graph():
+    """The joining call waits for a kernel, a copy and a fill of other streams."""
+    x, w = rnd(1, (8, 16, 128), torch.bfloat16), rnd(2, (16, 128, 128), torch.bfloat16, 0.1)
+    big = rnd(3, (4000, 16, 128), torch.bfloat16)
+    a, far = torch.zeros((4008, 16, 128), dtype=torch.bfloat16, device=DEV), torch.zeros((4008, 16, 128), dtype=torch.bfloat16, device=DEV)
+    out, out2 = torch.zeros_like(a), torch.zeros_like(a)
+    sides = [torch.cuda.Stream() for _ in range(3)]
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        a.zero_()
+        for i, side in enumerate(sides):
+            side.wait_stream(main)
+            with torch.cuda.stream(side):
+                if i == 0:
+                    pkg.head_product(x, w, a[4000:])
+                elif i == 1:
+                    a[:4000].copy_(big)
+                else:
+                    far.fill_(0)
+        for side in sides:
+            main.wait_stream(side)
+        pkg.head_product(a, w, out)
+        sides[0].wait_stream(main)
+        with torch.cuda.stream(sides[0]):
+            pkg.head_product(out, w, far)
+        main.wait_stream(sides[0])
+        pkg.head_product(far, w, out2)
+    for _ in range(5):
+        out.zero_(), out2.zero_(), far.fill_(1)
+        graph.replay()
+    torch.cuda.synchronize()
+    want = torch.empty_like(a)
+    pkg.head_product(x, w, a[4000:])
+    torch.cuda.synchronize()
+    steps = [a.clone()]
+    steps[0][:4000] = big
+    for _ in range(3):
+        pkg.head_product(steps[-1], w, want)
+        torch.cuda.synchronize()
+        steps.append(want.clone())
+    assert torch.equal(out, steps[1]) and torch.equal(far, steps[2]) and torch.equal(out2, steps[3])

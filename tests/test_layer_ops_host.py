@@ -212,8 +212,8 @@ def test_binding_refuses_what_is_no_tensor(lib):
 def test_extension_calls_the_library_that_ctypes_loaded(lib):
     binding._extension()
     with open("/proc/self/maps") as f:
-        loaded = {line.split()[-1] for line in f if "libmla_tree_verify" in line}
-    assert len(loaded) == 1 and loaded.pop().endswith("_lib/libmla_tree_verify.so")
+        inodes = {line.split()[4] for line in f if "libmla_tree_verify" in line}
+    assert len(inodes) == 1
 
 
 def test_prefill_workspace_splits_a_part_filled_wave():
