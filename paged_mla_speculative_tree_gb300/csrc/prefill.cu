@@ -42,7 +42,8 @@
 // (bounded too) before TMEM is freed.
 //
 // With few query rows the keys are split over blocks, and so are those of the last
-// blocks where they would leave most SMs idle: each writes its normalised part and
+// blocks where they would leave most SMs idle (blocks of few unsplit keys take 128
+// rows, one stage, where 256 would leave half of the SMs idle): each writes its normalised part and
 // its lse, and combine_kernel joins them (60 rows over 32,768 keys of 8 heads: 30 us,
 // 21 of them the keys' way from memory).  Letting both stages take the rows of such a
 // block and its tiles in turn was no faster.
@@ -92,6 +93,7 @@ struct PrefillArgs {
   int64_t o_tok, o_head, num_q, num_kv, max_q, max_kv, part_rows;
   float scale;
   int bs, heads, causal, q_blocks;
+  int block_rows;    // 256, or 128: the second stage idle
   int nsplit, last;  // the last blocks, whose keys are split
   unsigned whole;    // the blocks before them
   int by_block;      // rows of parts: 256 a split block; else num_q * heads
@@ -106,7 +108,7 @@ struct PrefillReq {
 struct PrefillBlock {
   int r, h, row0;
   __device__ __forceinline__ PrefillBlock(const PrefillArgs& A, unsigned b) {
-    row0 = (A.q_blocks - 1 - int(b % unsigned(A.q_blocks))) * kBlockRows;
+    row0 = (A.q_blocks - 1 - int(b % unsigned(A.q_blocks))) * A.block_rows;
     b /= unsigned(A.q_blocks);
     h = int(b % unsigned(A.heads)), r = int(b / unsigned(A.heads));
   }
@@ -164,7 +166,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   const int shift = R.len - R.n;  // query i sees keys up to shift + i
   auto tiles_of = [&](int s) -> int {
     const int first = row0 + s * kStageRows;
-    if (first >= R.n) return 0;
+    if (first >= R.n || s * kStageRows >= A.block_rows) return 0;
     const int last = min(R.n, first + kStageRows) - 1;
     const int keys = A.causal ? max(0, min(R.len, shift + last + 1)) : R.len;
     return (keys + kKeys - 1) / kKeys;
@@ -432,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       l += a + b;
     }
     if (ok && Ts > 0) ok = __all_sync(0xffffffffu, wait_for(bar(B_O + s), 0, ctl, A.err));
-    if (ok && i0 < R.n) {
+    if (ok && i0 < R.n && s * kStageRows < A.block_rows) {
       const bool some = l != 0.f;  // true for a NaN too, which the row then shows
       const float inv = some ? __frcp_rn(l) : 0.f;
       const int live = min(32, R.n - i0);
@@ -574,6 +576,14 @@ template <typename T> cudaError_t launch_prefill(const PrefillArgs& A, cudaStrea
                       dim3(unsigned(A.last), warp_row ? (rows + 3) / 4 : rows), 128, 0, st, A);
 }
 
+int sm_count() {
+  int device = 0, sms = 0;
+  if (cudaGetDevice(&device) != cudaSuccess ||
+      cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, device) != cudaSuccess)
+    return 0;
+  return sms;
+}
+
 // nsplit's two numbers, of `blocks` blocks: how many of the last ones are split
 // (0 in it: all), and whether their parts have rows of their own.
 struct Splits {
@@ -613,6 +623,9 @@ extern "C" int mla_prefill_workspace(int num_sms, int bs, int64_t max_q, int64_t
   const bool tail = over > 0 && 2 * over <= num_sms && blocks < kTailWaves * int64_t(num_sms) && shortest >= 16;
   if (tail) n = num_sms / over, worth = shortest / 4;
   if (n > worth) n = worth;
+  // Blocks of 128 rows (below) give as much as two parts: 256 new after 3,700 keys, 64 heads, 45 us either way,
+  // 256 after 3,000 39 and 41, 900 new, 16 heads, 14 and 20; 200 after 8,000 85 and 72
+  if (!tail && n == 2 && max_q > kStageRows && max_kv < 28 * kKeys) n = 1;
   if (n > MTV_MAX_PREFILL_SPLITS) n = MTV_MAX_PREFILL_SPLITS;
   *nsplit_out = n < 2 ? 1 : int(n + (tail ? over * kSplitLast : 0));
   *bytes_out = Splits(*nsplit_out, blocks, num_q, num_heads).bytes();
@@ -672,6 +685,13 @@ extern "C" int mla_prefill_run(const void* q, int64_t q_tok_stride, int64_t q_he
   A.max_q = max_q, A.max_kv = max_kv, A.scale = scale, A.bs = bs, A.heads = num_heads, A.causal = causal;
   A.nsplit = splits.count, A.q_blocks = int(q_blocks), A.last = int(splits.last), A.part_rows = splits.rows;
   A.whole = unsigned(q_blocks * num_heads * bs - splits.last), A.by_block = splits.by_block;
+  // Where blocks of 256 rows leave half of the SMs idle and keys are not split, blocks of 128 take half as much
+  // in and out (one prompt, 64 heads of 256 tokens 8.2 -> 7.7 us, 16 heads of 900 16.2 -> 14.4)
+  A.block_rows = kBlockRows;
+  if (A.nsplit == 1 && max_q > kStageRows && 2 * q_blocks * num_heads * bs <= sm_count()) {
+    A.block_rows = kStageRows, A.q_blocks = int((max_q + kStageRows - 1) / kStageRows);
+    A.last = A.q_blocks * num_heads * bs, A.whole = 0;
+  }
   A.q_by_head = q_head_stride != 0, A.k_by_head = k_head_stride != 0, A.v_by_head = v_head_stride != 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = bf16 ? launch_prefill<__nv_bfloat16>(A, st) : launch_prefill<__half>(A, st);

@@ -943,3 +943,22 @@ def test_products_behind_a_fork_and_a_join_of_streams_in_a_graph():
         torch.cuda.synchronize()
         steps.append(want.clone())
     assert torch.equal(out, steps[1]) and torch.equal(far, steps[2]) and torch.equal(out2, steps[3])
+
+
+# ------------------------- prefill in blocks of 256 rows (few of them: of 128)
+
+@pytest.mark.parametrize("dtype", HALF)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("name", ["two tiles", "odd", "ragged", "fewer keys", "first rows without keys", "many blocks"])
+def test_prefill_of_more_blocks_than_half_of_the_sms(name, causal, dtype):
+    heads = 78 if len(CASES[name]) == 1 else 30
+    check_prefill(prefill_batch(67, CASES[name], heads, TYPES[dtype]), TYPES[dtype], causal=causal)
+
+
+def test_prefill_in_blocks_of_128_and_of_256_rows():
+    """A head's rows come out alike among few heads and among many."""
+    b = prefill_batch(71, [(300, 500), (129, 700)], 80, torch.bfloat16)
+    many, many_lse = check_prefill(b, torch.bfloat16)
+    few = {**b, **{k: b[k][:, 7:10] for k in ("q", "k_nope", "v")}}
+    out, lse = check_prefill(few, torch.bfloat16)
+    assert torch.equal(out, many[:, 7:10]) and torch.equal(lse, many_lse[:, 7:10])

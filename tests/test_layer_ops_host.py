@@ -241,3 +241,11 @@ def test_prefill_refuses_split_counts(lib):
     for nsplit in (256, 65 + 256, 255, -255, -(1 << 31)):
         assert prefill(lib, nsplit=nsplit, ws=FAKE, ws_bytes=1 << 40) == -3, nsplit
     assert prefill(lib, nsplit=64 + 256 * 100, ws=FAKE, ws_bytes=64 * 8 * 256 * 129 * 4 - 1) == -4  # eight blocks are there
+
+
+def test_prefill_workspace_prefers_smaller_blocks_to_two_parts():
+    nsplit = lambda new, keys, heads: pkg.prefill_workspace(152, 1, new, keys, new, heads)[0]  # noqa: E731
+    assert nsplit(256, 3256, 64) == 1    # blocks of 128 rows instead
+    assert nsplit(128, 3256, 64) == 2    # no smaller blocks to take
+    assert nsplit(256, 8192, 64) == 2    # long keys
+    assert nsplit(256, 3256, 48) == 3
