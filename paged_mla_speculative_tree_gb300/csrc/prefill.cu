@@ -42,11 +42,11 @@
 // (bounded too) before TMEM is freed.
 //
 // With few query rows the keys are split over blocks, and so are those of the last
-// blocks where they would leave most SMs idle (blocks of few unsplit keys take 128
-// rows, one stage, where 256 would leave half of the SMs idle): each writes its normalised part and
-// its lse, and combine_kernel joins them (60 rows over 32,768 keys of 8 heads: 30 us,
+// blocks where they would leave most SMs idle: each writes its normalised part and
+// its lse, and combine_kernel joins them (60 rows over 32,768 keys of 8 heads: 31 us,
 // 21 of them the keys' way from memory).  Letting both stages take the rows of such a
-// block and its tiles in turn was no faster.
+// block and its tiles in turn was no faster.  Few blocks of unsplit keys have 128
+// rows, one stage, where 256 would leave half of the SMs idle.
 #include <math.h>
 #include <stdint.h>
 
