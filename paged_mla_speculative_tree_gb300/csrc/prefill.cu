@@ -22,9 +22,12 @@
 // TMEM: S0, S1, O0, O1 of 128 columns each.
 //
 // The maximum that scores refer to moves only when a row's scores grow by more
-// than 2^8 past it (weights stay below 2^8), so O is rarely rescaled.  P is
-// rounded to the input type, which the tensor core takes; sums of weights stay in
-// fp32.
+// than 2^8 past it, so O is rarely rescaled.  P is rounded to the input type, which
+// the tensor core takes; sums of weights stay in fp32.  fp16 weights are held 2^7
+// times as large, P = 2^(S c - m c + 7), at most 2^15: a weight is then off by 2^-32
+// of the row's largest at most.  Without that a long tail of keys below 2^-25 counted
+// in the sum and not in O (one key 2^25.1 above 131,072 others: outputs off by 240 of
+// fp16's half steps in the median, now by 5, what fp32 sums of that length leave).
 //
 // What bounds it (one GB300, 64 heads): the tensor core, for long prompts.  8,192
 // tokens in one piece take 0.778 ms, 1,770 TFLOP/s of what the causal mask leaves
@@ -80,6 +83,9 @@ constexpr uint32_t kSmem = kOffCtl + 16 + 1024;  // + slack for 1 KB alignment
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
 constexpr float kRescaleLog2 = 8.f;
+// the reference's own weight, and its logarithm
+template <typename T> constexpr float kWeight = std::is_same<T, __half>::value ? 128.f : 1.f;
+template <typename T> constexpr float kWeightLog2 = std::is_same<T, __half>::value ? 7.f : 0.f;
 constexpr int kSplitLast = MTV_PREFILL_SPLIT_LAST, kTailWaves = 8;
 
 struct PrefillArgs {
@@ -410,8 +416,8 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         }
       }
       if (move) m = top;
-      const float ref = m == -INFINITY ? 0.f : m * c;
-      const uint64_t c2 = f2_pack(c, c), ref2 = f2_pack(-ref, -ref);
+      const float ref = m == -INFINITY ? 0.f : fmaf(-m, c, kWeightLog2<T>);
+      const uint64_t c2 = f2_pack(c, c), ref2 = f2_pack(ref, ref);
       uint64_t sum0 = f2_pack(0.f, 0.f), sum1 = sum0;
 #pragma unroll
       for (int half = 0; half < 2; ++half) {
@@ -488,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
         __syncwarp();
       }
       if (lane < live) {
-        const float lse = some ? m * A.scale + logf(l) : -INFINITY;
+        const float lse = some ? m * A.scale + logf(l * (1.f / kWeight<T>)) : -INFINITY;
         if (split_keys) A.part[A.nsplit * A.part_rows * kV + part_at + int64_t(lane) * part_step] = lse;
         else if (A.lse) A.lse[at + int64_t(lane) * A.heads] = lse;
       }
