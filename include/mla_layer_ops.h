@@ -104,7 +104,10 @@ int mla_prefill_workspace(int num_sms, int bs, int64_t max_q, int64_t max_kv, in
  *   s_j = scale (q[i, h, 0:128] . k_nope[j, h, :] + q[i, h, 128:192] . k_rope[j, :])
  *   out = softmax(s) v[:, h, :],  lse = ln sum exp(s)
  * over the keys j < L, and with `causal` j <= L - n + i (the last query sees
- * every key).  A query that sees no key has out = 0, lse = -inf.
+ * every key).  A query that sees no key has out = 0, lse = -inf.  Scores, sums
+ * and lse are held in fp32.  The product with v takes the weights rounded to dtype
+ * (by half a step at most, or in fp16 2^-32 of the row's largest where that is
+ * more), and out is divided by the sum of the rounded ones.
  *
  * q              device, [num_q, heads, 192]: element (t, h, d) at t * q_tok_stride
  *                + h * q_head_stride + d (strides in elements, here and below).

@@ -23,11 +23,18 @@
 //
 // The maximum that scores refer to moves only when a row's scores grow by more
 // than 2^8 past it, so O is rarely rescaled.  P is rounded to the input type, which
-// the tensor core takes; sums of weights stay in fp32.  fp16 weights are held 2^7
-// times as large, P = 2^(S c - m c + 7), at most 2^15: a weight is then off by 2^-32
-// of the row's largest at most.  Without that a long tail of keys below 2^-25 counted
-// in the sum and not in O (one key 2^25.1 above 131,072 others: outputs off by 240 of
-// fp16's half steps in the median, now by 5, what fp32 sums of that length leave).
+// the tensor core takes; sums of weights stay in fp32: one of the weights, for the lse,
+// and one of the rounded ones, by which O is divided, so that their rounding cancels
+// in what the values have in common instead of scaling the output (up to half a step
+// more: 300 equal values of 2 less a step came out a step too low).  The second sum is
+// taken while the tensor core has the weights, with adds that read them as they are
+// (8,192 tokens 781 -> 788 us, 2 x (1,000 after 5,760) 310 -> 315, the ragged fp16
+// batch 166 -> 171, a prompt of 256 7.7 -> 8.2; unpacked first: 848, 328, 183, 8.5).
+// fp16 weights are held 2^7 times as large, P = 2^(S c - m c + 7), at most 2^15: a
+// weight is then off by 2^-32 of the row's largest at most.  Without that a long tail
+// of keys below 2^-25 counted in the sum and not in O (one key 2^25.1 above 131,072
+// others: outputs off by 240 of fp16's half steps in the median, now by 5, what fp32
+// sums of that length leave).
 //
 // What bounds it (one GB300, 64 heads): the tensor core, for long prompts.  8,192
 // tokens in one piece take 0.778 ms, 1,770 TFLOP/s of what the causal mask leaves
@@ -136,6 +143,18 @@ __device__ __forceinline__ float ex2(float x) {
   float y;
   asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
   return y;
+}
+
+// Adds the two values of a packed pair to a and b, in fp32.
+__device__ __forceinline__ void add_halves(uint32_t v, float& a, float& b, __nv_bfloat16) {
+  asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %2;\n add.rn.f32.bf16 %0, x, %0;\n add.rn.f32.bf16 %1, y, %1;\n}"
+      : "+f"(a), "+f"(b)
+      : "r"(v));
+}
+__device__ __forceinline__ void add_halves(uint32_t v, float& a, float& b, __half) {
+  asm("{\n .reg .b16 x, y;\n mov.b32 {x, y}, %2;\n add.rn.f32.f16 %0, x, %0;\n add.rn.f32.f16 %1, y, %1;\n}"
+      : "+f"(a), "+f"(b)
+      : "r"(v));
 }
 
 template <typename T>
@@ -376,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     int end = A.causal ? max(0, min(R.len, shift + i + 1)) : R.len;
     int clear = A.causal ? max(0, min(R.len, shift + i0 + 1)) : R.len;
     end -= begin * kKeys, clear -= begin * kKeys;  // from the block's first tile on
-    float m = -INFINITY, l = 0.f;
+    float m = -INFINITY, l = 0.f, taken = 0.f;  // taken: the weights' sum as the product takes them
     bool ok = true;
     for (int j = 0; j < Ts; ++j) {
       uint32_t x[128];
@@ -404,7 +423,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       if (__any_sync(0xffffffffu, move && j > 0)) {
         // O holds all tiles before this one (its scores come after them)
         const float keep = move ? (m == -INFINITY ? 0.f : ex2((m - top) * c)) : 1.f;
-        l *= keep;
+        l *= keep, taken *= keep;
         const uint32_t o = tmem + lanes + kTmemO + 128 * s;
 #pragma unroll 1
         for (int u = 0; u < 128; u += 16) {
@@ -438,11 +457,18 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       float a, b;
       f2_unpack(f2_add(sum0, sum1), a, b);
       l += a + b;
+      float t0 = 0.f, t1 = 0.f, t2 = 0.f, t3 = 0.f;
+#pragma unroll
+      for (int u = 0; u < 32; ++u) {
+        add_halves(x[u], t0, t1, T());
+        add_halves(x[64 + u], t2, t3, T());
+      }
+      taken += (t0 + t1) + (t2 + t3);
     }
     if (ok && Ts > 0) ok = __all_sync(0xffffffffu, wait_for(bar(B_O + s), 0, ctl, A.err));
     if (ok && i0 < R.n && s * kStageRows < A.block_rows) {
       const bool some = l != 0.f;  // true for a NaN too, which the row then shows
-      const float inv = some ? __frcp_rn(l) : 0.f;
+      const float inv = some ? __frcp_rn(taken) : 0.f;
       const int live = min(32, R.n - i0);
       const int64_t at = int64_t(R.q0 + i0) * A.heads + h;
       const int64_t part_at = split * A.part_rows + (A.by_block ? int64_t(tail) * kBlockRows + (i0 - row0) : at);

@@ -70,3 +70,48 @@ def test_small_fp16_weights_of_many_keys_count(keys, at, nsplit):
 
 def test_small_bf16_weights_of_many_keys_count():
     check(one_key_above_all(131_072, 0, torch.bfloat16, 5), 1.0, 1, 2.0)
+
+
+@pytest.mark.parametrize("spread,scale", [(30.0, 192 ** -0.5), (1.5, 2.0), (1e-3, 192 ** -0.5)])
+def test_fp16_weights_of_sharp_and_flat_scores(spread, scale):
+    b = prefill_batch(7, [(140, 400)], 2, torch.float16, spread=spread)
+    check(b, scale, 1, b["v"][:400].abs().max().item() * 2)
+
+
+def test_fp16_weights_of_rising_scores():
+    """The maximum grows within what a row's reference allows, and past it."""
+    for top in (4.0, 40.0):
+        b = prefill_batch(9, [(130, 700)], 1, torch.float16)
+        b["q"][:, 0, 128] = 8.0
+        b["k_rope"][:, 0] = torch.linspace(-top, top, 703, device=DEV).to(torch.float16)
+        check(b, 192 ** -0.5, 1, b["v"][:700].abs().max().item() * 2)
+        check(b, 192 ** -0.5, 4, b["v"][:700].abs().max().item() * 2)
+
+
+@pytest.mark.parametrize("nsplit", [1, 3, 2 + LAST])
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("dtype", HALF)
+def test_values_that_all_keys_share_come_out_as_they_are(dtype, causal, nsplit):
+    """All values are the largest below 2 and every weight but one is a half and nearly half a step: what the weights'
+    rounding takes away, half a step of theirs, is more than half a step of the output."""
+    t = TYPES[dtype]
+    u = half_step(t)[0]
+    b = prefill_batch(11, [(1, 300)], 2, t, pad=0)
+    b["q"].zero_(), b["k_nope"].zero_(), b["k_rope"].zero_()
+    b["q"][:, :, 128], b["k_rope"][1:, 0] = 1, -1
+    b["v"].fill_(2 - 2 * u)
+    scale = -math.log(0.5 * (1 + 0.98 * u))
+    out, lse = run(b, scale, nsplit)
+    # sums of 300 values agree to 308 steps of 2^-23, a tenth of half a step of fp16
+    assert (out == 2 - 2 * u).all()
+    want = math.log(1 + 299 * 0.5 * (1 + 0.98 * u))
+    assert (lse - want).abs().max() < 2.0 ** -20 + 308 * 2.0 ** -23
+
+
+@pytest.mark.parametrize("nsplit", [1, 4, 3 + LAST * 2])
+@pytest.mark.parametrize("requests", [[(140, 400)], [(257, 515)], [(3, 3), (129, 200), (1, 64), (5, 127)]])
+@pytest.mark.parametrize("dtype", HALF)
+def test_values_with_a_common_part(dtype, requests, nsplit):
+    b = prefill_batch(13, requests, 2, TYPES[dtype])
+    b["v"].copy_((3 + b["v"].float() * 0.05).to(TYPES[dtype]))
+    check(b, 192 ** -0.5, nsplit, 4.0)
