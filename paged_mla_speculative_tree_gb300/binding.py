@@ -7,6 +7,7 @@ this raises.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import importlib.util
 import os
@@ -645,7 +646,9 @@ class MlaPrefill:
     each, in buffers of ``num_q`` query rows.
 
     ``__call__`` never synchronises, so it can be captured in a graph.  Calls of
-    one object share its workspace: order them, or use an object each."""
+    one object share its workspace: order them, or use an object each, and keep
+    it until they have ended.  The split count comes from the bounds alone: a batch
+    with far fewer rows or keys may be faster in an object of its own."""
 
     def __init__(self, bs, max_q, num_q, max_kv, num_heads, device=None):
         self.device = torch.device("cuda", torch.cuda.current_device() if device is None else device)
@@ -654,21 +657,37 @@ class MlaPrefill:
         self.nsplit, size = prefill_workspace(sms, bs, max_q, max_kv, num_q, num_heads)
         self.workspace = torch.empty(size, dtype=torch.uint8, device=self.device) if size else None
         self.err = torch.zeros(1, dtype=torch.int32, device=self.device)
+        with torch.cuda.device(self.device):
+            if not torch.cuda.is_current_stream_capturing():
+                torch.cuda.current_stream().synchronize()  # a call on any stream finds the word zeroed
 
     def __call__(self, q, k_nope, k_rope, v, qo_indptr, kv_indptr, scale, out=None, lse=None, causal=True, stream=None):
-        """Returns (out, lse), allocated where they are not given (zeroed then: rows of no request stay as they are)."""
+        """Returns (out, lse), allocated on the call's stream where they are not given (zeroed then: rows of no request
+        stay as they are)."""
         if q.shape[0] > self.num_q or q.shape[1] != self.num_heads or qo_indptr.numel() > self.bs + 1:
             raise ValueError("the batch exceeds the bounds of this object")
-        if out is None:
-            out = torch.zeros((q.shape[0], q.shape[1], 128), dtype=q.dtype, device=q.device)
-        if lse is None:
-            lse = torch.zeros(tuple(q.shape[:2]), dtype=torch.float32, device=q.device)
+        if out is None or lse is None:
+            with self._on(stream):
+                if out is None:
+                    out = torch.zeros((q.shape[0], q.shape[1], 128), dtype=q.dtype, device=q.device)
+                if lse is None:
+                    lse = torch.zeros(tuple(q.shape[:2]), dtype=torch.float32, device=q.device)
         prefill_run(q, k_nope, k_rope, v, qo_indptr, kv_indptr, self.max_q, self.max_kv, scale, out, lse, causal,
                     self.nsplit, self.workspace, self.err, stream)
         return out, lse
 
+    def _on(self, stream):
+        """The stream of a call as torch's current one."""
+        if stream is None:
+            return contextlib.nullcontext()
+        if not isinstance(stream, torch.cuda.Stream):
+            legacy = int(stream) == 1  # CUDA's own name of the default stream
+            stream = torch.cuda.ExternalStream(0 if legacy else int(stream), device=self.device)
+        return torch.cuda.stream(stream)
+
     def device_error(self) -> int:
-        """The sticky error word (synchronises)."""
+        """The sticky error word, of calls on all streams (synchronises the device)."""
+        torch.cuda.synchronize(self.device)
         return int(self.err.item())
 
 
