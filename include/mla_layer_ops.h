@@ -45,6 +45,10 @@ extern "C" {
 #define MTV_MAX_PREFILL_SPLITS 64
 /* What mla_prefill_run's nsplit holds above the split count: see there. */
 #define MTV_PREFILL_SPLIT_LAST 256
+/* Test only, added n times (1 .. 255) to the dtype of mla_head_product or
+ * mla_prefill_run: waits inside the tensor-core kernels that have to spin give
+ * up once 512 (n - 1) cycles of their block have passed, in place of a second. */
+#define MTV_TEST_GIVE_UP 0x100
 
 /*
  * mla_head_product -- one matrix product a head.
@@ -70,7 +74,7 @@ extern "C" {
  * k_dim, n_dim   1 .. MTV_MAX_HEAD_DIM.
  * dtype          MTV_DTYPE_BF16 or MTV_DTYPE_FP16, of x, w and out.
  * err            device uint32 or NULL: MTV_DEVERR_TIMEOUT when a bounded wait
- *                gave up.
+ *                gave up (outputs of that block may be missing).
  *
  * Any strides are taken.  The tensor-core kernel runs where every address and
  * every stride but the innermost is a multiple of 16 bytes, n_dim is a multiple

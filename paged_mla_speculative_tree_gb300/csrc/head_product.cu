@@ -56,7 +56,7 @@ struct ProductArgs {
   void* out;
   uint32_t* err;
   int64_t x_tok, x_head, w_head, w_k, w_n, out_tok, out_head, tokens;
-  int heads, k_dim, n_dim;
+  int heads, k_dim, n_dim, give_up;
 };
 
 constexpr int kRows = 128, kChunk = 64;   // tokens a unit, k a chunk
@@ -74,6 +74,7 @@ static_assert(kOffCtl + sizeof(Ctl) <= kOffData, "barriers");
 struct TensorArgs {
   CUtensorMap x, w, out;
   uint32_t* err;
+  int give_up;             // tests: see init_ctl
   int64_t units, tokens;   // units: heads * n_tiles * m_tiles
   uint32_t x_bytes;        // of a chunk of x: 64 k of 128 tokens, or of as many as there are
   int m_tiles, n_tiles, nt, chunks, slots;
@@ -106,7 +107,8 @@ struct Units {
 };
 
 // kFew: at most one tile of tokens, whose copies bring several chunks each.
-template <typename T, bool kFew>
+// kTest: waits that give up for a test.
+template <typename T, bool kFew, bool kTest>
 __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_constant__ TensorArgs A) {
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -123,7 +125,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
 
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i == B_ACCFREE || i == B_ACCFREE + 1 ? 4 : 1);
-    ctl->abort = 0;
+    init_ctl<kTest>(ctl, A.give_up);
     fence_mbar_init_cluster();
   }
   if (warp == 1) {
@@ -142,7 +144,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
     uint32_t phase = 1;                             // of the slots' releases: the first round waits for none
     const uint32_t data = uniform(base);
     auto released = [&](int b, uint32_t parity) {
-      return __all_sync(0xffffffffu, wait_for_call(bar(b), parity, ctl, A.err)) != 0;
+      return __all_sync(0xffffffffu, wait_for_call<kTest>(bar(b), parity, ctl, A.err)) != 0;
     };
     bool ok = true;
     for (Units u(first, last, A); u.more() && ok; u.next(A)) {
@@ -184,11 +186,12 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
     }
     // what was asked for lands before the block ends, read or not: the last items, slot by slot backwards
     if (elect_one()) {
+      const long long since = clock64();
       for (int i = 0; i < items; ++i) {
         if (--slot < 0) slot = A.slots - 1, phase ^= 1;
-        drain(bar(B_XFULL + slot), phase ^ 1, A.err);
+        drain(bar(B_XFULL + slot), phase ^ 1, since, A.err);
       }
-      for (int c = 0; c < asked; ++c) drain(bar(B_WFULL + c), uint32_t(loads - 1) & 1, A.err);
+      for (int c = 0; c < asked; ++c) drain(bar(B_WFULL + c), uint32_t(loads - 1) & 1, since, A.err);
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -197,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
                                                               : idesc_fp16_f32(kRows, A.nt, 0, A.w_k_major ? 0 : 1);
     const uint32_t w_step = A.w_k_major ? 32u : 2048u, acc = uniform(tmem), data = uniform(base);
     auto arrived = [&](int b, uint32_t parity) {
-      return __all_sync(0xffffffffu, wait_for_call(bar(b), parity, ctl, A.err)) != 0;
+      return __all_sync(0xffffffffu, wait_for_call<kTest>(bar(b), parity, ctl, A.err)) != 0;
     };
     int slot = 0, loads = 0, n = 0;
     uint32_t phase = 0;  // of the ring's slots
@@ -232,7 +235,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
     }
     if (elect_one()) {
       mma_commit(bar(B_FIN));  // every MMA issued has run once this arrives
-      drain(bar(B_FIN), 0, A.err);
+      drain(bar(B_FIN), 0, clock64(), A.err);
     }
     __syncwarp();
   } else {
@@ -244,7 +247,7 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
     for (Units u(first, last, A); u.more(); u.next(A), ++n) {
       const int h = u.h, n0 = u.n * A.nt, buf = n & 1;
       const int64_t t0 = int64_t(u.t) * kRows + q * 32;
-      const bool ok = wait_for_call(bar(B_ACC + buf), uint32_t(n / 2) & 1, ctl, A.err);
+      const bool ok = wait_for_call<kTest>(bar(B_ACC + buf), uint32_t(n / 2) & 1, ctl, A.err);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const int width = t0 < A.tokens ? min(A.nt, A.n_dim - n0) : 0;  // a store starts inside the tensor, which clips it
@@ -292,10 +295,8 @@ __global__ void __launch_bounds__(kThreads, 1) head_product_kernel(const __grid_
 // MMAs, whose commits arrive on both CTAs' barriers; each CTA stores its tokens' sums.
 constexpr int kPairTokens = 2 * kRows, kPairN = 256, kPairChunks = 8;
 constexpr uint32_t kPairW = 128 * kChunk * 2, kPairColumns = 512;
-constexpr int kAbortSpin = 1 << 20;
 
-
-template <typename T>
+template <typename T, bool kTest>
 __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) head_product_pair_kernel(const __grid_constant__ TensorArgs A) {
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -309,7 +310,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) head_pr
 
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i == B_ACCFREE || i == B_ACCFREE + 1 ? 8 : 1);
-    ctl->abort = 0;
+    init_ctl<kTest>(ctl, A.give_up, mapa(smem_u32(const_cast<int*>(&ctl->abort)), rank ^ 1));
     fence_mbar_init_cluster();
   }
   if (warp == 1) {
@@ -325,47 +326,44 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) head_pr
 
   if (warp == 0) {
     // ------------------------------------------------------------- copies
-    int slot = 0, items = 0, loads = 0, asked = 0;
-    uint32_t phase = 1;
+    int slot = 0, x_asked = 0, w_asked = 0;  // chunks
+    uint32_t phase = 1, w_phase = 1;
     const uint32_t data = uniform(base), lead = uniform(mapa(base, 0));  // its barriers take both CTAs' copies
     auto released = [&](int b, uint32_t parity) {
-      return __all_sync(0xffffffffu, wait_for_call(bar(b), parity, ctl, A.err)) != 0;
+      return __all_sync(0xffffffffu, wait_for_call<kTest>(bar(b), parity, ctl, A.err)) != 0;
     };
     bool ok = true;
     for (Units u(first, last, A); u.more() && ok; u.next(A)) {
       const int xh = A.x_by_head ? u.h : 0, wh = A.w_by_head ? u.h : 0;
       const int n0 = u.n * kPairN + rank * 128, t0 = u.t * kPairTokens + rank * kRows;
       for (int c = 0; c < A.chunks && ok; ++c) {
-        if (items >= A.slots) ok = released(B_XEMPTY + slot, phase);
+        if (x_asked >= A.slots) ok = released(B_XEMPTY + slot, phase);
         if (!ok) break;
         if (elect_one()) {
           if (rank == 0) mbar_arrive_expect_tx(data + 8 * (B_XFULL + slot), 2 * kXSlot);
           tma_load_3d_pair(data + off_x + slot * kXSlot, &A.x, c * kChunk, xh, t0, lead + 8 * (B_XFULL + slot));
         }
-        items = items < A.slots ? items + 1 : items;
+        ++x_asked;
         if (++slot == A.slots) slot = 0, phase ^= 1;
         if (!u.fresh) continue;
         if (c == 0) {
-          if (loads > 0) ok = released(B_WFREE, uint32_t(loads - 1) & 1);
+          if (w_asked > 0) ok = released(B_WFREE, w_phase);
           if (!ok) break;
-          ++loads, asked = 0;
+          w_phase ^= 1;
         }
-        ++asked;
         if (elect_one()) {
           const uint32_t dst = data + kOffData + c * kPairW, full = lead + 8 * (B_WFULL + c);
           if (rank == 0) mbar_arrive_expect_tx(data + 8 * (B_WFULL + c), 2 * kPairW);
           if (A.w_k_major) tma_load_3d_pair(dst, &A.w, c * kChunk, wh, n0, full);
           else for (int b = 0; b < 128; b += 64) tma_load_3d_pair(dst + b * 128, &A.w, n0 + b, wh, c * kChunk, full);
         }
+        ++w_asked;
       }
     }
-    // what both CTAs asked for lands before either ends
-    if (rank == 0 && elect_one()) {
-      for (int i = 0; i < items; ++i) {
-        if (--slot < 0) slot = A.slots - 1, phase ^= 1;
-        drain(bar(B_XFULL + slot), phase ^ 1, A.err);
-      }
-      for (int c = 0; c < asked; ++c) drain(bar(B_WFULL + c), uint32_t(loads - 1) & 1, A.err);
+    if (elect_one()) {
+      const uint32_t to = mapa(smem_u32(&ctl->asked[2 * rank]), 0);
+      st_cluster_u32(to, uint32_t(x_asked));
+      st_cluster_u32(to + 4, uint32_t(w_asked));
     }
     __syncwarp();
   } else if (warp == 1) {
@@ -375,7 +373,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) head_pr
                                                                 : idesc_fp16_f32(kPairTokens, kPairN, 0, A.w_k_major ? 0 : 1);
       const uint32_t w_step = A.w_k_major ? 32u : 2048u, acc = uniform(tmem), data = uniform(base);
       auto arrived = [&](int b, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_for_call(bar(b), parity, ctl, A.err)) != 0;
+        return __all_sync(0xffffffffu, wait_for_call<kTest>(bar(b), parity, ctl, A.err)) != 0;
       };
       int slot = 0, loads = 0, n = 0;
       uint32_t phase = 0;
@@ -383,7 +381,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) head_pr
       for (Units u(first, last, A); u.more() && ok; u.next(A), ++n) {
         if (u.fresh) ++loads;
         const int buf = n & 1;
-        if (n >= 2) ok = __all_sync(0xffffffffu, wait_for_peer(bar(B_ACCFREE + buf), uint32_t(n / 2 - 1) & 1, ctl, A.err)) != 0;
+        if (n >= 2) ok = __all_sync(0xffffffffu, wait_for_peer<kTest>(bar(B_ACCFREE + buf), uint32_t(n / 2 - 1) & 1, ctl, A.err)) != 0;
         for (int c = 0; c < A.chunks && ok; ++c) {
           if (u.fresh) ok = arrived(B_WFULL + c, uint32_t(loads - 1) & 1);
           if (ok) ok = arrived(B_XFULL + slot, phase);
@@ -407,7 +405,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) head_pr
       }
       if (elect_one()) mma_commit_pair(bar(B_FIN));
     }
-    if (elect_one()) drain(bar(B_FIN), 0, A.err);  // the last of the commits that arrive here
+    if (elect_one()) drain(bar(B_FIN), 0, clock64(), A.err);  // the last of the commits that arrive here
     __syncwarp();
   } else {
     // ------------------------------------------------------------- sums to memory
@@ -418,7 +416,7 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) head_pr
     for (Units u(first, last, A); u.more(); u.next(A), ++n) {
       const int n0 = u.n * kPairN, buf = n & 1;
       const int64_t t0 = int64_t(u.t) * kPairTokens + rank * kRows + q * 32;
-      const bool ok = wait_for_call(bar(B_ACC + buf), uint32_t(n / 2) & 1, ctl, A.err);
+      const bool ok = wait_for_call<kTest>(bar(B_ACC + buf), uint32_t(n / 2) & 1, ctl, A.err);
       if (!__all_sync(0xffffffffu, ok)) break;
       tc_fence_after();
       const int width = t0 < A.tokens ? min(kPairN, A.n_dim - n0) : 0;
@@ -451,13 +449,27 @@ __global__ void __cluster_dims__(2, 1, 1) __launch_bounds__(kThreads, 1) head_pr
   }
   tc_fence_before();
   __syncthreads();
-  if (ctl->abort) {  // copies may be under way that the even CTA's barriers do not count
-    const long long t0 = clock64();
-    while (clock64() - t0 < kAbortSpin) {}
-  }
-  cluster_sync();  // no product reads, and no copy or commit writes, the other CTA's memory any more
+  cluster_sync();  // no product reads, and no commit writes, the other CTA's memory any more; no copy will be asked for
   tc_fence_after();
   if (warp == 1) tmem_dealloc_pair(tmem, kPairColumns);
+  // After a wait that gave up, what either CTA asked for lands before one of them ends (else the products have taken
+  // it all).  One may have asked for more than the other, by a ring at most, since a slot's release takes both sides'
+  // copies: chunk i then has its barrier's open phase to itself, and the bytes that nobody asked for are made up or
+  // not expected.
+  if (ctl->abort && rank == 0 && warp == 0 && elect_one()) {
+    const long long since = clock64();
+    auto settle = [&](int full, int mine, int theirs, int ring, uint32_t bytes) {
+      const int all = max(mine, theirs);
+      for (int i = min(mine, theirs); i < all; ++i) {
+        if (i < mine) mbar_complete_tx(bar(full + i % ring), bytes);
+        else mbar_arrive_expect_tx(bar(full + i % ring), bytes);
+      }
+      for (int i = max(0, all - ring); i < all; ++i) drain(bar(full + i % ring), uint32_t(i / ring) & 1, since, A.err);
+    };
+    settle(B_XFULL, ctl->asked[0], ctl->asked[2], A.slots, kXSlot);
+    settle(B_WFULL, ctl->asked[1], ctl->asked[3], A.chunks, kPairW);
+  }
+  __syncwarp();
   cluster_sync();
 }
 
@@ -538,7 +550,7 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
   }
   P.x_by_head = A.x_head != 0, P.w_by_head = A.w_head != 0, P.out_by_head = 1;
   if (A.heads == 1) P.x_by_head = P.w_by_head = P.out_by_head = 0;
-  P.err = A.err, P.tokens = A.tokens, P.n_dim = A.n_dim;
+  P.err = A.err, P.give_up = A.give_up, P.tokens = A.tokens, P.n_dim = A.n_dim;
   // weights: rows, their stride, their length, and the rows of a box
   const int64_t w_rows = P.w_k_major ? A.n_dim : A.k_dim, w_row = P.w_k_major ? A.w_n : A.w_k;
   const int w_dim = P.w_k_major ? A.k_dim : A.n_dim, w_box = P.w_k_major ? (pair ? 128 : P.nt) : 64;
@@ -551,11 +563,13 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
       encode_heads_map(&P.out, bf16, A.out, A.tokens, A.out_tok, A.heads, A.out_head, A.n_dim, 64, 32);
   if (!maps) return cudaErrorInvalidValue;
   if (pair) {
-    const cudaError_t e = cudaFuncSetAttribute(head_product_pair_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
+    auto kernel = A.give_up ? head_product_pair_kernel<T, true> : head_product_pair_kernel<T, false>;
+    const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
     if (e != cudaSuccess) return e;
-    return launch_early(head_product_pair_kernel<T>, dim3(2 * unsigned(pairs)), kThreads, pair_smem, st, P);
+    return launch_early(kernel, dim3(2 * unsigned(pairs)), kThreads, pair_smem, st, P);
   }
-  auto kernel = few ? head_product_kernel<T, true> : head_product_kernel<T, false>;
+  auto kernel = A.give_up ? (few ? head_product_kernel<T, true, true> : head_product_kernel<T, false, true>)
+                          : (few ? head_product_kernel<T, true, false> : head_product_kernel<T, false, false>);
   const cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, 227 * 1024);
   if (e != cudaSuccess) return e;
   const unsigned grid = unsigned(P.units < sms ? P.units : sms);
@@ -619,6 +633,7 @@ extern "C" int mla_head_product(const void* x, int64_t x_tok_stride, int64_t x_h
                                 int64_t out_tok_stride, int64_t out_head_stride, int64_t num_tokens, int num_heads,
                                 int k_dim, int n_dim, int dtype, uint32_t* err, void* stream) {
   using namespace mtv;
+  const int give_up = take_give_up(&dtype);
   if (num_tokens < 0 || num_tokens > INT32_MAX || num_heads < 0 || num_heads > MTV_MAX_HEADS || k_dim < 1 ||
       k_dim > MTV_MAX_HEAD_DIM || n_dim < 1 || n_dim > MTV_MAX_HEAD_DIM ||
       (dtype != MTV_DTYPE_BF16 && dtype != MTV_DTYPE_FP16))
@@ -628,7 +643,7 @@ extern "C" int mla_head_product(const void* x, int64_t x_tok_stride, int64_t x_h
   if ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(w) | reinterpret_cast<uintptr_t>(out)) & 1)
     return MTV_E_BAD_ARGUMENT;
   const ProductArgs A{x, w, out, err, x_tok_stride, x_head_stride, w_head_stride, w_k_stride, w_n_stride, out_tok_stride,
-                      out_head_stride, num_tokens, num_heads, k_dim, n_dim};
+                      out_head_stride, num_tokens, num_heads, k_dim, n_dim, give_up};
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const bool bf16 = dtype == MTV_DTYPE_BF16;
   cudaError_t e;

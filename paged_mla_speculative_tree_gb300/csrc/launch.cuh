@@ -9,9 +9,19 @@
 
 #include <cuda_runtime.h>
 
+#include "mla_layer_ops.h"
+
 namespace mtv {
 
 __device__ __forceinline__ void launched_after() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
+// The count of MTV_TEST_GIVE_UP in a dtype argument, which is left without it; what is none stays as it is.
+inline int take_give_up(int* dtype) {
+  if (*dtype < 0 || *dtype >= 256 * MTV_TEST_GIVE_UP) return 0;
+  const int n = *dtype / MTV_TEST_GIVE_UP;
+  *dtype %= MTV_TEST_GIVE_UP;
+  return n;
+}
 
 template <typename... P>
 cudaError_t launch_early(void (*kernel)(P...), dim3 grid, unsigned threads, size_t smem, cudaStream_t st, const P&... args) {

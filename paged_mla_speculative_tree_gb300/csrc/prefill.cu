@@ -86,7 +86,7 @@ enum : int {
   B_Q = 0, B_KFULL = 2, B_VFULL = 4, B_KFREE = 6, B_VFREE = 8, B_S = 10, B_P = 12, B_O = 16, B_FIN = 18, B_TURN = 20, B_COUNT = 22
 };
 constexpr uint32_t kOffCtl = kOffBars + 8 * B_COUNT;
-constexpr uint32_t kSmem = kOffCtl + 16 + 1024;  // + slack for 1 KB alignment
+constexpr uint32_t kSmem = kOffCtl + sizeof(Ctl) + 1024;  // + slack for 1 KB alignment
 static_assert(kSmem <= 227 * 1024, "shared memory");
 constexpr uint32_t kTmemS = 0, kTmemO = 256;
 constexpr float kRescaleLog2 = 8.f;
@@ -105,7 +105,8 @@ struct PrefillArgs {
   uint32_t* err;
   int64_t o_tok, o_head, num_q, num_kv, max_q, max_kv, part_rows;
   float scale;
-  int bs, heads, causal, q_blocks;
+  int heads, causal, q_blocks;
+  int give_up;       // tests: see init_ctl
   int block_rows;    // 256, or 128: the second stage idle
   int nsplit, last;  // the last blocks, whose keys are split
   unsigned whole;    // the blocks before them
@@ -157,7 +158,8 @@ __device__ __forceinline__ void add_halves(uint32_t v, float& a, float& b, __hal
       : "r"(v));
 }
 
-template <typename T>
+// kTest: waits that give up for a test.
+template <typename T, bool kTest>
 __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_constant__ PrefillArgs A) {
   extern __shared__ unsigned char smem_raw[];
   const uint32_t raw = smem_u32(smem_raw), base = (raw + 1023u) & ~1023u;
@@ -174,7 +176,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   // the set-up needs nothing from memory
   if (tid == 0) {
     for (int i = 0; i < B_COUNT; ++i) mbar_init(bar(i), i >= B_KFREE && i < B_S ? 2 : i >= B_P && i < B_O ? 4 : 1);
-    ctl->abort = 0;
+    init_ctl<kTest>(ctl, A.give_up);
     fence_mbar_init_cluster();
   }
   if (warp == 10 && lane == 0) {
@@ -218,7 +220,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       const int qh = A.q_by_head ? h : 0, kh = A.k_by_head ? h : 0, vh = A.v_by_head ? h : 0;
       const uint32_t data = uniform(base), bars = uniform(bar(0));
       auto released = [&](int b, uint32_t parity) {
-        return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, A.err)) != 0;
+        return __all_sync(0xffffffffu, wait_for<kTest>(bar(b), parity, ctl, A.err)) != 0;
       };
       auto load_q = [&](int s) {
         if (stage_tiles(s) > 0 && elect_one()) {
@@ -268,10 +270,11 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       // what was asked for lands before the block ends, read or not (a second stage's Q is asked for with the first tile)
       if (elect_one()) {
+        const long long since = clock64();
         for (int s = 0; s < 2; ++s)
-          if (stage_tiles(s) > 0) drain(bar(B_Q + s), 0, A.err);
-        for (int j = max(0, k_asked - 2); j < k_asked; ++j) drain(bar(B_KFULL + (j & 1)), uint32_t(j / 2) & 1, A.err);
-        for (int j = max(0, v_asked - 2); j < v_asked; ++j) drain(bar(B_VFULL + (j & 1)), uint32_t(j / 2) & 1, A.err);
+          if (stage_tiles(s) > 0) drain(bar(B_Q + s), 0, since, A.err);
+        for (int j = max(0, k_asked - 2); j < k_asked; ++j) drain(bar(B_KFULL + (j & 1)), uint32_t(j / 2) & 1, since, A.err);
+        for (int j = max(0, v_asked - 2); j < v_asked; ++j) drain(bar(B_VFULL + (j & 1)), uint32_t(j / 2) & 1, since, A.err);
       }
     }
     __syncwarp();
@@ -284,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     const uint32_t tmem_s = uniform(tmem) + kTmemS + 128 * s, tmem_o = uniform(tmem) + kTmemO + 128 * s, data = uniform(base);
     auto slot_of = [&](int item) { return data + kOffRing + uint32_t(item % kSlots) * kSlot; };
     auto arrived = [&](int b, uint32_t parity) {
-      return __all_sync(0xffffffffu, wait_for(bar(b), parity, ctl, A.err)) != 0;
+      return __all_sync(0xffffffffu, wait_for<kTest>(bar(b), parity, ctl, A.err)) != 0;
     };
     // Where both stages have work they take turns, 0 1 0 1 ...: O += P V(j) and the next S are
     // one turn.  Left to themselves they drift into step, share the tensor core while both have
@@ -381,7 +384,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     }
     if (Ts > 0 && elect_one()) {  // every MMA issued has run once this arrives
       mma_commit(bar(B_FIN + s));
-      drain(bar(B_FIN + s), 0, A.err);
+      drain(bar(B_FIN + s), 0, clock64(), A.err);
     }
     __syncwarp();
   } else {
@@ -399,7 +402,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
     bool ok = true;
     for (int j = 0; j < Ts; ++j) {
       uint32_t x[128];
-      ok = wait_for(bar(B_S + s), j & 1, ctl, A.err);
+      ok = wait_for<kTest>(bar(B_S + s), j & 1, ctl, A.err);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) break;
       tc_fence_after();
@@ -465,7 +468,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       taken += (t0 + t1) + (t2 + t3);
     }
-    if (ok && Ts > 0) ok = __all_sync(0xffffffffu, wait_for(bar(B_O + s), 0, ctl, A.err));
+    if (ok && Ts > 0) ok = __all_sync(0xffffffffu, wait_for<kTest>(bar(B_O + s), 0, ctl, A.err));
     if (ok && i0 < R.n && s * kStageRows < A.block_rows) {
       const bool some = l != 0.f;  // true for a NaN too, which the row then shows
       const float inv = some ? __frcp_rn(taken) : 0.f;
@@ -598,9 +601,10 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pr
 
 template <typename T> cudaError_t launch_prefill(const PrefillArgs& A, cudaStream_t st) {
   const unsigned blocks = A.whole + unsigned(A.last) * unsigned(A.nsplit);
-  cudaError_t e = cudaFuncSetAttribute(prefill_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
+  auto kernel = A.give_up ? prefill_kernel<T, true> : prefill_kernel<T, false>;
+  cudaError_t e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(kSmem));
   if (e != cudaSuccess) return e;
-  e = launch_early(prefill_kernel<T>, dim3(blocks), kThreads, kSmem, st, A);
+  e = launch_early(kernel, dim3(blocks), kThreads, kSmem, st, A);
   if (e != cudaSuccess || A.nsplit == 1) return e;
   const bool warp_row = A.nsplit <= kWarpParts;
   const unsigned rows = unsigned(A.max_q < kBlockRows ? A.max_q : kBlockRows);
@@ -672,6 +676,7 @@ extern "C" int mla_prefill_run(const void* q, int64_t q_tok_stride, int64_t q_he
                                int64_t out_tok_stride, int64_t out_head_stride, float* lse, int nsplit,
                                void* workspace, uint64_t workspace_bytes, uint32_t* err, void* stream) {
   using namespace mtv;
+  const int give_up = take_give_up(&dtype);
   if (bs < 0 || bs > MTV_MAX_HEADS || max_q < 0 || max_kv < 0 || num_q < 0 || num_kv < 0 ||
       max_q > MTV_MAX_PREFILL_ROWS || max_kv > MTV_MAX_PREFILL_ROWS || num_q > MTV_MAX_PREFILL_ROWS ||
       num_kv > MTV_MAX_PREFILL_ROWS || num_heads < 0 ||
@@ -714,7 +719,7 @@ extern "C" int mla_prefill_run(const void* q, int64_t q_tok_stride, int64_t q_he
     return MTV_E_CUDA;
   A.out = out, A.lse = lse, A.part = static_cast<float*>(workspace), A.qo_indptr = qo_indptr, A.kv_indptr = kv_indptr;
   A.err = err, A.o_tok = out_tok_stride, A.o_head = out_head_stride, A.num_q = num_q, A.num_kv = num_kv;
-  A.max_q = max_q, A.max_kv = max_kv, A.scale = scale, A.bs = bs, A.heads = num_heads, A.causal = causal;
+  A.max_q = max_q, A.max_kv = max_kv, A.scale = scale, A.give_up = give_up, A.heads = num_heads, A.causal = causal;
   A.nsplit = splits.count, A.q_blocks = int(q_blocks), A.last = int(splits.last), A.part_rows = splits.rows;
   A.whole = unsigned(q_blocks * num_heads * bs - splits.last), A.by_block = splits.by_block;
   // Where blocks of 256 rows leave half of the SMs idle and keys are not split, blocks of 128 take half as much
