@@ -141,7 +141,8 @@ int mla_prefill_workspace(int num_sms, int bs, int64_t max_q, int64_t max_kv, in
  * err            device uint32 or NULL.  MTV_DEVERR_INDPTR: a decreasing
  *                offset, one past num_q or num_kv, or a request past max_q or
  *                max_kv (its rows are left as they were).  MTV_DEVERR_TIMEOUT:
- *                a bounded wait gave up.
+ *                a bounded wait gave up (rows of that block may be left as they
+ *                were, or NaN where its keys are split).
  * Rows of no request are left as they were.  Keys and values that no query of
  * their request sees may hold anything, NaN included; one that some query of a
  * request sees has to be finite for the request's other queries to be right.

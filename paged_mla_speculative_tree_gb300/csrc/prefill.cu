@@ -469,13 +469,16 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       taken += (t0 + t1) + (t2 + t3);
     }
     if (ok && Ts > 0) ok = __all_sync(0xffffffffu, wait_for<kTest>(bar(B_O + s), 0, ctl, A.err));
-    if (ok && i0 < R.n && s * kStageRows < A.block_rows) {
+    const int live = s * kStageRows < A.block_rows ? min(32, R.n - i0) : 0;  // rows of this warp
+    const int64_t at = int64_t(R.q0 + i0) * A.heads + h;
+    const int64_t part_at = split * A.part_rows + (A.by_block ? int64_t(tail) * kBlockRows + (i0 - row0) : at);
+    const int part_step = A.by_block ? 1 : A.heads;
+    float* part_lse = A.part + A.nsplit * A.part_rows * kV + part_at;
+    // a part that a wait gave up on makes its rows NaN, not what the workspace holds
+    if (!ok && split_keys && lane < live) part_lse[int64_t(lane) * part_step] = __uint_as_float(0x7fffffffu);
+    if (ok && live > 0) {
       const bool some = l != 0.f;  // true for a NaN too, which the row then shows
       const float inv = some ? __frcp_rn(taken) : 0.f;
-      const int live = min(32, R.n - i0);
-      const int64_t at = int64_t(R.q0 + i0) * A.heads + h;
-      const int64_t part_at = split * A.part_rows + (A.by_block ? int64_t(tail) * kBlockRows + (i0 - row0) : at);
-      const int part_step = A.by_block ? 1 : A.heads;
       tc_fence_after();
       // rows to memory through this stage's part of Q (every product that read it has run), so
       // that a warp stores whole rows; 16-byte units are swizzled by the row.  In short loops: a
@@ -491,7 +494,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
           tmem_ld32_sync(tmem + lanes + kTmemO + 128 * s + u, y);
 #pragma unroll
           for (int e = 0; e < 32; ++e) y[e] = some ? __float_as_uint(__uint_as_float(y[e]) * inv) : 0u;
-          if (split_keys) {  // a part without weights is not read by the combine
+          if (split_keys) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
               st_shared_v4(mine_s + lane * 256 + ((((u - u0 + e) / 4) ^ (lane & 15)) << 4), y[e], y[e + 1], y[e + 2], y[e + 3]);
@@ -524,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
       }
       if (lane < live) {
         const float lse = some ? m * A.scale + logf(l * (1.f / kWeight<T>)) : -INFINITY;
-        if (split_keys) A.part[A.nsplit * A.part_rows * kV + part_at + int64_t(lane) * part_step] = lse;
+        if (split_keys) part_lse[int64_t(lane) * part_step] = lse;
         else if (A.lse) A.lse[at + int64_t(lane) * A.heads] = lse;
       }
     }
@@ -575,7 +578,7 @@ __global__ void __launch_bounds__(128) combine_kernel(const __grid_constant__ Pr
       w[e] = __shfl_sync(0xffffffffu, k < 32 ? wa : wb, k & 31) * inv;
       if (k >= A.nsplit) w[e] = 0.f;
       v[e] = make_float4(0.f, 0.f, 0.f, 0.f);
-      // a part without weights was not written
+      // a part of weight 0 is not read
       if (w[e] != 0.f) v[e] = *reinterpret_cast<const float4*>(A.part + (k * all + part_at) * kV + 4 * lane);
     }
 #pragma unroll

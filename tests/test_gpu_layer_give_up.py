@@ -93,3 +93,39 @@ def test_prompt_attention_that_gives_up(requests, heads, nsplit, dtype):
     assert call(0) == 0
     want = [out.clone(), lse.clone()]
     run_all(call, [out, lse], want, err)
+
+
+@pytest.mark.parametrize("nsplit", [1, 3, 9, 2 + LAST * 3])
+def test_rows_of_prompt_attention_that_gave_up_are_left_or_nan(nsplit):
+    """Each row is as it should be, as it was, or (with split keys) NaN: never made of what the workspace held."""
+    b = prefill_batch(9, [(60, 3000), (300, 1700)], 2, torch.bfloat16, pad=0)
+    heads, rows = 2, 360
+    n, last = nsplit % LAST, nsplit // LAST
+    ws = torch.empty(n * max(last * 256, rows * heads) * 129, dtype=torch.float32, device=DEV)
+    qo, kv, err = i64(b["qo"]), i32(b["kv"]), i32([0])
+    out, lse = torch.empty((rows, heads, 128), dtype=torch.bfloat16, device=DEV), torch.empty((rows, heads), device=DEV)
+    q, kn, kr, v = b["q"], b["k_nope"], b["k_rope"], b["v"]
+
+    def call(count):
+        ws.fill_(3)
+        out.fill_(7), lse.fill_(7)
+        assert binding.load().mla_prefill_run(
+            q.data_ptr(), q.stride(0), q.stride(1), kn.data_ptr(), kn.stride(0), kn.stride(1), kr.data_ptr(), kr.stride(0),
+            v.data_ptr(), v.stride(0), v.stride(1), qo.data_ptr(), kv.data_ptr(), 2, 300, 3000, rows, kn.shape[0], heads,
+            GIVE_UP * count, 0.07, 1, out.data_ptr(), out.stride(0), out.stride(1), lse.data_ptr(), nsplit, ws.data_ptr(),
+            ws.numel() * 4, err.data_ptr(), torch.cuda.current_stream().cuda_stream) == 0
+        torch.cuda.synchronize()
+
+    call(0)
+    want = out.clone(), lse.clone()
+    missing = 0
+    for count in COUNTS:
+        call(count)
+        good = (out == want[0]).all(dim=2) & (lse == want[1])
+        left = (out == 7).all(dim=2) & (lse == 7)
+        nan = out.isnan().all(dim=2) & lse.isnan()
+        assert (good | left | nan).all(), f"count {count}"
+        assert n > 1 or not nan.any()
+        assert last or n == 1 or not left.any()
+        missing += int((~good).sum())
+    assert missing > 0 and int(err) == binding.DEVERR_TIMEOUT
