@@ -649,5 +649,6 @@ extern "C" int mla_head_product(const void* x, int64_t x_tok_stride, int64_t x_h
   cudaError_t e;
   if (tensor_form(A)) e = bf16 ? launch_tensor<__nv_bfloat16>(A, st) : launch_tensor<__half>(A, st);
   else e = bf16 ? launch_plain<__nv_bfloat16>(A, st) : launch_plain<__half>(A, st);
+  if (e != cudaSuccess) cudaGetLastError();  // or a later launch reports it
   return e == cudaSuccess ? MTV_OK : MTV_E_CUDA;
 }

@@ -387,5 +387,6 @@ extern "C" int mla_norm_rope_write(const uint64_t* turns, int rope_dim, float am
   if (dtype == MTV_DTYPE_BF16) e = launch_norm<__nv_bfloat16>(A, layout, num_tokens, st);
   else if (dtype == MTV_DTYPE_FP16) e = launch_norm<__half>(A, layout, num_tokens, st);
   else e = launch_norm<float>(A, layout, num_tokens, st);
+  if (e != cudaSuccess) cudaGetLastError();  // or a later launch reports it
   return e == cudaSuccess ? MTV_OK : MTV_E_CUDA;
 }

@@ -735,5 +735,6 @@ extern "C" int mla_prefill_run(const void* q, int64_t q_tok_stride, int64_t q_he
   A.q_by_head = q_head_stride != 0, A.k_by_head = k_head_stride != 0, A.v_by_head = v_head_stride != 0;
   cudaStream_t st = static_cast<cudaStream_t>(stream);
   const cudaError_t e = bf16 ? launch_prefill<__nv_bfloat16>(A, st) : launch_prefill<__half>(A, st);
+  if (e != cudaSuccess) cudaGetLastError();  // or a later launch reports it
   return e == cudaSuccess ? MTV_OK : MTV_E_CUDA;
 }
