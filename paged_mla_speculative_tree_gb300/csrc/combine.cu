@@ -34,11 +34,13 @@ __global__ void __launch_bounds__(kThreads) combine_kernel(const Params P) {
   const int t = int(blockIdx.x % unsigned(P.max_q));
   const int chunk = int(blockIdx.y);
   const Req R = load_req(P, r);
-  if (t >= R.n) return;
   const int ns = splits_used(P, R.keys);
   const int64_t stride_rows = P.total_q_max * kHeads;
   const int64_t row0 = (R.q_off + t) * kHeads;  // first (token, head) row of this block
-  grid_dependency_wait();                        // partials of the preceding kernel are complete
+  // Partials of the preceding kernel are complete.  Blocks without a row wait too, so that this kernel never ends
+  // before the one that it was launched after: a kernel launched early behind it waits for this one only.
+  grid_dependency_wait();
+  if (t >= R.n) return;
 
   const int tid = threadIdx.x;
   if (tid < kHeads) {

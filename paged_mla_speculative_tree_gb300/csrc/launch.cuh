@@ -1,10 +1,11 @@
 // Launches whose blocks may start while the stream's kernel before is ending: they
 // set up, then wait for its end and its writes (launched_after) before they touch
 // global memory.  Every block waits, also one without work, so that a kernel never
-// ends before the one that it was launched after.  (Calls in a row on one GB300: a
-// product of 8 tokens 4.6 -> 4.2 us in a graph, 6.2 -> 4.1 without, a prompt of 256
-// 12.1 -> 8.1.  Letting the next kernel start while this one still works gave 0.1 us
-// there and took 1.5 here.)
+// ends before the one that it was launched after; the library's other kernels that
+// are launched so (joins, second kernels of a call) keep to that too.  (Calls in a row
+// on one GB300: a product of 8 tokens 4.6 -> 4.2 us in a graph, 6.2 -> 4.1 without, a
+// prompt of 256 12.1 -> 8.1.  Letting the next kernel start while this one still works
+// gave 0.1 us there and took 1.5 here.)
 #pragma once
 
 #include <cuda_runtime.h>
