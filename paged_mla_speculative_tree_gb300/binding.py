@@ -579,9 +579,10 @@ def _extension():
     global _ext
     if _ext is None:
         lib = load()
-        if not os.path.exists(_build.EXT):
-            raise RuntimeError(f"extension not built: {_build.EXT} (run __graft_entry__.build())")
-        spec = importlib.util.spec_from_file_location("binding_ext", _build.EXT)
+        path = _build.extension_path()
+        if not os.path.exists(path):
+            raise RuntimeError(f"extension not built for this torch and Python: {path} (run __graft_entry__.build())")
+        spec = importlib.util.spec_from_file_location("binding_ext", path)
         ext = importlib.util.module_from_spec(spec)
         spec.loader.exec_module(ext)
         ext.bind(*(ctypes.cast(f, ctypes.c_void_p).value

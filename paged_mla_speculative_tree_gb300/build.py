@@ -1,9 +1,9 @@
 """Builds the CUDA library in-tree for sm_103a with plain nvcc (no CMake).
 
 Each .cu translation unit is compiled in parallel, then linked into
-``paged_mla_speculative_tree_gb300/_lib/libmla_tree_verify.so``, and beside it
-``binding_ext.so``, the Python extension (g++) through which some of its entries
-are called.
+``paged_mla_speculative_tree_gb300/_lib/libmla_tree_verify.so``.  Beside it g++ makes
+the Python extension through which some of its entries are called; it needs the
+headers of Python and torch, and without them the library is built all the same.
 """
 from __future__ import annotations
 
@@ -22,12 +22,12 @@ INCLUDE = os.path.join(ROOT, "include")
 OUT_DIR = os.path.join(PKG, "_lib")
 LIB = os.path.join(OUT_DIR, "libmla_tree_verify.so")
 EXT_SRC = os.path.join(CSRC, "binding_ext.cpp")
-EXT = os.path.join(OUT_DIR, "binding_ext.so")
 BUILD_DIR = os.path.join(ROOT, "_build")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr",
               "-Xptxas", "-warn-spills"]
+CXX = "g++"
 
 
 def nvcc() -> str:
@@ -41,64 +41,83 @@ def sources():
     return sorted(os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith(".cu"))
 
 
-def _deps():
-    return sources() + [EXT_SRC] + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))] + \
-        [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
+def _abi():
+    return [os.path.join(INCLUDE, f) for f in os.listdir(INCLUDE)]
+
+
+def _current(made, sources) -> bool:
+    return os.path.exists(made) and all(os.path.getmtime(d) <= os.path.getmtime(made) for d in sources)
+
+
+def _library_current() -> bool:
+    headers = [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
+    return _current(LIB, sources() + headers + _abi())
+
+
+def _extension_current() -> bool:
+    return _current(extension_path(), [EXT_SRC] + _abi())
 
 
 def up_to_date() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(EXT):
-        return False
-    t = min(os.path.getmtime(LIB), os.path.getmtime(EXT))
-    return all(os.path.getmtime(d) <= t for d in _deps())
+    return _library_current() and _extension_current()
 
 
-def build(force: bool = False, verbose: bool = False, extra=()) -> str:
-    if not force and up_to_date():
-        return LIB
-    os.makedirs(BUILD_DIR, exist_ok=True)
-    os.makedirs(OUT_DIR, exist_ok=True)
+def extension_path() -> str:
+    return os.path.join(OUT_DIR, "binding_ext.so")
+
+
+def _run(what, cmd):
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{what} failed:\n{r.stdout}\n{r.stderr}")
+    return r
+
+
+def _build_extension() -> None:
+    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
+    path = extension_path()
+    obj, tmp = os.path.join(BUILD_DIR, "binding_ext.o"), path + f".tmp{os.getpid()}"
+    inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
+           os.path.join(torch_dir, "include", "torch", "csrc", "api", "include")]
+    _run(f"{CXX} on {EXT_SRC}", [CXX, "-O2", "-std=c++17", "-fPIC", *(f"-I{d}" for d in inc), "-c", EXT_SRC, "-o", obj])
+    _run("link", [CXX, "-shared", "-o", tmp, obj, "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"])
+    os.replace(tmp, path)
+
+
+def _build_library(ex, verbose, extra) -> None:
     cc = nvcc()
 
     def compile_one(src):
         obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-        cmd = [cc, *ARCH, *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"nvcc failed on {src}:\n{r.stdout}\n{r.stderr}")
+        r = _run(f"nvcc on {src}", [cc, *ARCH, *NVCC_FLAGS, *extra, "-I", INCLUDE, "-I", CSRC, "-c", src, "-o", obj])
         if verbose and (r.stdout or r.stderr):
             sys.stderr.write(r.stdout + r.stderr)
         return obj
 
-    torch_dir = list(importlib.util.find_spec("torch").submodule_search_locations)[0]
-
-    def compile_ext():
-        obj = os.path.join(BUILD_DIR, "binding_ext.o")
-        inc = [INCLUDE, sysconfig.get_paths()["include"], os.path.join(torch_dir, "include"),
-               os.path.join(torch_dir, "include", "torch", "csrc", "api", "include")]
-        cmd = ["g++", "-O2", "-std=c++17", "-fPIC", *(f"-I{d}" for d in inc), "-c", EXT_SRC, "-o", obj]
-        r = subprocess.run(cmd, capture_output=True, text=True)
-        if r.returncode != 0:
-            raise RuntimeError(f"g++ failed on {EXT_SRC}:\n{r.stdout}\n{r.stderr}")
-        return obj
-
-    srcs = sources()
-    with cf.ThreadPoolExecutor(max_workers=min(len(srcs) + 1, os.cpu_count() or 4)) as ex:
-        ext = ex.submit(compile_ext)
-        objs = list(ex.map(compile_one, srcs))
-        ext = ext.result()
     tmp = LIB + f".tmp{os.getpid()}"
-    cmd = [cc, *ARCH, "-shared", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
+    _run("link", [cc, *ARCH, "-shared", "-o", tmp, *ex.map(compile_one, sources())])
     os.replace(tmp, LIB)
-    tmp = EXT + f".tmp{os.getpid()}"
-    cmd = ["g++", "-shared", "-o", tmp, ext, "-L" + os.path.join(torch_dir, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10"]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        raise RuntimeError(f"link failed:\n{r.stdout}\n{r.stderr}")
-    os.replace(tmp, EXT)
+
+
+def build(force: bool = False, verbose: bool = False, extra=()) -> str:
+    """Builds what is missing or older than its sources; returns the library's path.  An extension that could not be
+    built is reported on stderr: the calls that go through it raise, all others need only the library."""
+    library, extension = force or not _library_current(), force or not _extension_current()
+    if not library and not extension:
+        return LIB
+    os.makedirs(BUILD_DIR, exist_ok=True)
+    os.makedirs(OUT_DIR, exist_ok=True)
+    with cf.ThreadPoolExecutor(max_workers=min(len(sources()) + 1, os.cpu_count() or 4)) as ex:
+        made = ex.submit(_build_extension) if extension else None
+        if library:
+            _build_library(ex, verbose, extra)
+        try:
+            if made:
+                made.result()
+        except (RuntimeError, OSError) as e:  # no headers, no compiler
+            sys.stderr.write(f"the extension was not built: {e}\n")
+            if os.path.exists(extension_path()):
+                os.remove(extension_path())  # of other sources
     return LIB
 
 
