@@ -63,7 +63,9 @@ def up_to_date() -> bool:
 
 
 def extension_path() -> str:
-    return os.path.join(OUT_DIR, "binding_ext.so")
+    """The extension for this torch and this Python, whose layouts are compiled into it."""
+    import torch
+    return os.path.join(OUT_DIR, f"binding_ext.torch-{torch.__version__}.{sysconfig.get_config_var('SOABI')}.so")
 
 
 def _run(what, cmd):

@@ -35,3 +35,20 @@ def test_a_failing_library_raises(elsewhere, monkeypatch):
     with pytest.raises(RuntimeError):
         build.build(extra=["--no-such-option"])
     assert not os.path.exists(build.LIB)
+
+
+def test_extension_of_another_torch_is_not_taken(monkeypatch):
+    """Inline code of torch's and Python's headers is compiled into it."""
+    import torch
+
+    from paged_mla_speculative_tree_gb300 import binding
+    build.build()
+    assert build.up_to_date() and os.path.exists(build.extension_path())
+    monkeypatch.setattr(torch, "__version__", "0.0.0+other")
+    assert not build.up_to_date() and not os.path.exists(build.extension_path())
+    monkeypatch.setattr(binding, "_ext", None)
+    with pytest.raises(RuntimeError, match="not built"):
+        binding._extension()
+    monkeypatch.undo()
+    monkeypatch.setattr(build.sysconfig, "get_config_var", lambda name: "cpython-399-other")
+    assert not build.up_to_date() and not os.path.exists(build.extension_path())
