@@ -213,7 +213,6 @@ __global__ void __launch_bounds__(kThreads, 1) prefill_kernel(const __grid_const
   tc_fence_after();
   const uint32_t tmem = ctl->tmem;
 
-  auto slot_at = [&](int item) { return base + kOffRing + uint32_t(item % kSlots) * kSlot; };
   if (warp == 10) {
     // ------------------------------------------------------------- copies
     if (TN > 0) {
