@@ -103,13 +103,16 @@ struct View {
   void* at = nullptr;
   int64_t tok = 0, head = 0;
 };
+// What an empty tensor gives for its address: one that no kernel reads, but not NULL, by which the C entries know an
+// argument that is left out.
+void* const kNothing = reinterpret_cast<void*>(256);
 // A [tokens, heads, dim] or [tokens, dim] view, dense in its last dimension.
 View view(const at::Tensor& t, at::ScalarType type, int device, const char* name, at::IntArrayRef shape) {
   check_kind(t, type, device, name);
   check_shape(t, shape, name);
   if (t.stride(-1) != 1 && shape.back() > 1)
     refuse(PyExc_ValueError, std::string(name) + " must be dense in its last dimension");
-  return {t.data_ptr(), t.stride(0), shape.size() == 3 ? t.stride(1) : 0};
+  return {t.numel() ? t.data_ptr() : kNothing, t.stride(0), shape.size() == 3 ? t.stride(1) : 0};
 }
 
 // Other Python threads run during the C call: it may wait for a full queue, and the

@@ -58,3 +58,21 @@ def test_a_refused_launch_is_not_reported_by_the_next_call(kind):
     assert torch.equal(out, want)
     assert call() == 0
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32])
+@pytest.mark.parametrize("tokens,heads", [(0, 4), (0, 0), (5, 0)])
+def test_norms_of_no_tokens_or_no_heads(tokens, heads, dtype):
+    """Norms of both kinds given: nothing to do, or the latent rows alone."""
+    turns = pkg.rope_freqs(64, 10000.0)[0].to(DEV)
+    q, down = rnd(1, (tokens, heads, 192), dtype), rnd(2, (tokens, 576), dtype)
+    qw, cw = rnd(3, (192,), dtype), rnd(4, (512,), dtype)
+    q_nope, q_rope = torch.empty((tokens, heads, 128), dtype=dtype, device=DEV), torch.empty((tokens, heads, 64), dtype=dtype, device=DEV)
+    pools = [torch.full((8, 576), 9.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    kw = dict(c_in=down[:, :512], c_weight=cw, k_in=down[:, 512:], out_cache_loc=torch.arange(tokens, device=DEV))
+    positions = torch.arange(tokens, device=DEV)
+    assert pkg.norm_rope_write(turns, positions, 1e-6, q_in=q, q_weight=qw, q_nope=q_nope, q_rope=q_rope, kv_pool=pools[0], **kw) == 0
+    assert pkg.norm_rope_write(turns, positions, 1e-6, kv_pool=pools[1], **kw) == 0
+    assert pkg.norm_rope_write(turns, positions, 1e-6, q_in=q, q_weight=qw, q_nope=q_nope, q_rope=q_rope) == 0
+    assert torch.equal(pools[0], pools[1]) and (pools[0][tokens:] == 9).all()
+    assert tokens == 0 or not (pools[0][:tokens] == 9).any(dim=1).all()
