@@ -1,6 +1,7 @@
 // The host side of the layer's calls from Python: argument checks and the call of
 // the C entry, on tensors as they are.  Through ctypes a call of eleven tensors
-// spends 12 us in checks and conversions, several times its kernel; here about one.
+// spends 12 us in checks and conversions, several times its kernel; here 0.6 to 0.9, of
+// the 3.0 to 3.6 that a call takes with its launch.
 // The order of the arguments stands at each entry.
 #include <Python.h>
 

@@ -15,18 +15,19 @@
 // Weights dense in k are a K-major operand (chunks of 64 k x nt rows), weights
 // dense in n an MN-major one (blocks of 64 n x 64 k).
 //
-// What bounds it (one GB300, 64 heads): the bytes where each head has rows of its
-// own (1,024 tokens: queries to the latent space 14.6 us, latent outputs to values
-// 13.9, floors 13.8; 4,000 tokens 70 and 57, floors 50, but the first writes 262 MB,
-// which a plain fill does in 68); for few tokens the chain
+// What bounds it (one GB300, 64 heads; replays of one graph, which find part of their
+// bytes in L2): the bytes where each head has rows of its own (1,024 tokens: queries
+// to the latent space 14.6 us, latent outputs to values 13.9, floors 13.8, but 18.7 for
+// the first called on and on over changing inputs; 4,000 tokens 70 and 57, floors 50,
+// but the first writes 262 MB, which a plain fill does in 68); for few tokens the chain
 // launch -> copies -> sums -> stores (8 tokens to the latent space 4.2 us, 1.3 of
 // bytes; 64 to values 4.9, 2.0 of bytes); for one latent expanded to all heads the
 // copies of x under way beside 128 KB of weights, each value of which meets 128
-// outputs (8,191 tokens to 64 x 256: 104 us), so that many tokens go to pairs of SMs
-// (head_product_pair_kernel: 88 us, 1,560 TFLOP/s; one library product of that shape
-// 85).  Without pairs, sharing x between two blocks by multicast changed nothing (it
-// is a block's own ring that binds, not L2); two chunks a wait (+ 10 %) and eight
-// warps for the sums (+ 5 %) were slower.  Copies
+// outputs (8,191 tokens to 64 x 256: 104 us, 115 over changing inputs), so that many
+// tokens go to pairs of SMs (head_product_pair_kernel: 88 us, 1,560 TFLOP/s, and 103;
+// one library product of that shape 85 to 87).  Without pairs, sharing x between two
+// blocks by multicast changed nothing (it is a block's own ring that binds, not L2);
+// two chunks a wait (+ 10 %) and eight warps for the sums (+ 5 %) were slower.  Copies
 // and MMAs are issued under warp-uniform branches by an elected thread: by lane 0
 // of a divergent one they took two to four times as long (186 us).
 //
@@ -577,7 +578,9 @@ template <typename T> cudaError_t launch_tensor(const ProductArgs& A, cudaStream
 }
 
 // The plain form, for any strides: a block a tile of 64 tokens x 64 outputs of
-// one head, 16 k at a time through shared memory, 4 x 4 sums a thread.
+// one head, 16 k at a time through shared memory, 4 x 4 sums a thread.  What it costs
+// a caller whose rows are not in whole 16 bytes (64 heads): 8 tokens to the latent
+// space 31 us, 64 to values 74, 1,024 to the latent space 355 (the tensor core: 4, 5, 15).
 constexpr int kTile = 64, kSum = 16;
 
 template <typename T>

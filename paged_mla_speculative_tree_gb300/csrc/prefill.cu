@@ -28,8 +28,8 @@
 // in what the values have in common instead of scaling the output (up to half a step
 // more: 300 equal values of 2 less a step came out a step too low).  The second sum is
 // taken while the tensor core has the weights, with adds that read them as they are
-// (8,192 tokens 781 -> 788 us, 2 x (1,000 after 5,760) 310 -> 315, the ragged fp16
-// batch 166 -> 171, a prompt of 256 7.7 -> 8.2; unpacked first: 848, 328, 183, 8.5).
+// (8,192 tokens 780 -> 783 us, 2 x (1,000 after 5,760) 312 -> 317, the ragged fp16
+// batch 168 -> 172, a prompt of 256 7.6 -> 8.1; unpacked first: 848, 328, 183, 8.5).
 // fp16 weights are held 2^7 times as large, P = 2^(S c - m c + 7), at most 2^15: a
 // weight is then off by 2^-32 of the row's largest at most.  Without that a long tail
 // of keys below 2^-25 counted in the sum and not in O (one key 2^25.1 above 131,072
@@ -37,9 +37,11 @@
 // sums of that length leave).
 //
 // What bounds it (one GB300, 64 heads): the tensor core, for long prompts.  8,192
-// tokens in one piece take 0.778 ms, 1,770 TFLOP/s of what the causal mask leaves
-// (92 % of the measured bf16 rate); a pair of tiles 2,800 cycles of 2,600, a block
-// 9,000 more for its first copies and its output.  What each step gave there:
+// tokens in one piece take 0.78 ms in short replays, 1,760 TFLOP/s of what the causal
+// mask leaves (91 % of the measured bf16 rate), and 0.88 called on and on (1,570, 90 %
+// of what the power cap leaves one library product); a pair of tiles 2,800 cycles of
+// 2,600, a block 9,000 more for its first copies and its output.  What each step gave
+// there, in short replays:
 // MMAs and copies issued under warp-uniform branches by an elected thread (their
 // operands stay in uniform registers) 1.41 -> 1.04 ms; a warp a stage for the MMAs
 // -> 0.90; no spills in the softmax -> 0.87; turns -> 0.80; K's first slot filled
